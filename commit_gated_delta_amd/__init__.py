@@ -25,15 +25,22 @@ GDN_BF16, GDN_F32 = 0, 1
 GDN_FLAG_L2NORM_QK = 1
 GDN_FLAG_PREFILL_ONE_CHAIN = 2
 GDN_FLAG_TOKENWISE = 4
+GDN_FLAG_HEAD_DECAY = 8
+GDN_FLAG_KEEP_STATE = 16
 GDN_MAX_LANES = 256
 GDN_MAX_T = 64
+GDN_MAX_TOP = 32
 
 EXPORTED = ("gdn_records_bytes", "gdn_verify", "gdn_commit",
             "gdn_commit_verify", "gdn_verify_tree", "gdn_commit_path",
             "gdn_kda_records_bytes", "gdn_kda_verify", "gdn_kda_commit",
             "gdn_state_snapshot", "gdn_state_restore",
             "gdn_prefill_workspace_bytes", "gdn_prefill_chunked",
-            "gdn_prefill_chunked_noalloc", "gdn_strerror", "gdn_last_error")
+            "gdn_prefill_chunked_noalloc", "gdn_decay_step",
+            "gdn_decay_prefill_workspace_bytes", "gdn_decay_prefill",
+            "gdn_paged_attention_workspace_bytes", "gdn_paged_attention",
+            "gdn_kv_append", "gdn_token_scores_workspace_bytes",
+            "gdn_token_scores", "gdn_strerror", "gdn_last_error")
 PREFILL_SCRATCH_BYTES = 64 << 20
 
 
@@ -53,6 +60,17 @@ class Dims(ctypes.Structure):
     @classmethod
     def of(cls, n_layers, n_lanes, h_v, h_k, d_k, d_v, t_max):
         return cls(n_layers, n_lanes, h_v, h_k, d_k, d_v, t_max)
+
+
+class KvDims(ctypes.Structure):
+    _fields_ = [("n_lanes", ctypes.c_int32), ("t_max", ctypes.c_int32),
+                ("h_q", ctypes.c_int32), ("h_kv", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+    @classmethod
+    def of(cls, n_lanes, t_max, h_q, h_kv, d, page_size, n_pages, max_pages):
+        return cls(n_lanes, t_max, h_q, h_kv, d, page_size, n_pages, max_pages)
 
 
 def _load_library():
@@ -103,6 +121,28 @@ def _load_library():
     lib.gdn_prefill_chunked_noalloc.argtypes = [i32] * 8 + [vp] * 3 + [
         ctypes.c_int] + [vp] * 6 + [f, ctypes.c_int, vp]
     lib.gdn_prefill_chunked_noalloc.restype = ctypes.c_int
+    kp = ctypes.POINTER(KvDims)
+    lib.gdn_decay_step.argtypes = [dp, ip, vp, vp, vp, ctypes.c_int, vp, vp,
+                                   vp, f, ctypes.c_int, vp]
+    lib.gdn_decay_step.restype = ctypes.c_int
+    lib.gdn_decay_prefill_workspace_bytes.argtypes = [i32, ip] + [i32] * 4
+    lib.gdn_decay_prefill_workspace_bytes.restype = sz
+    lib.gdn_decay_prefill.argtypes = [i32, ip] + [i32] * 4 + [vp] * 3 + [
+        ctypes.c_int] + [vp] * 5 + [sz, f, ctypes.c_int, vp]
+    lib.gdn_decay_prefill.restype = ctypes.c_int
+    lib.gdn_paged_attention_workspace_bytes.argtypes = [kp]
+    lib.gdn_paged_attention_workspace_bytes.restype = sz
+    lib.gdn_paged_attention.argtypes = [kp, ip] + [vp] * 3 + [
+        ctypes.c_int] + [vp] * 4 + [sz, f, vp]
+    lib.gdn_paged_attention.restype = ctypes.c_int
+    lib.gdn_kv_append.argtypes = [kp, ip, vp, vp, ctypes.c_int] + [vp] * 5
+    lib.gdn_kv_append.restype = ctypes.c_int
+    lib.gdn_token_scores_workspace_bytes.argtypes = [i32] * 3
+    lib.gdn_token_scores_workspace_bytes.restype = sz
+    lib.gdn_token_scores.argtypes = [i32, i32, ctypes.c_int64, vp,
+                                     ctypes.c_int, vp, i32, f] + [
+                                         vp] * 5 + [sz, vp]
+    lib.gdn_token_scores.restype = ctypes.c_int
     lib.gdn_strerror.argtypes = [ctypes.c_int]
     lib.gdn_strerror.restype = ctypes.c_char_p
     lib.gdn_last_error.argtypes = []
@@ -352,3 +392,182 @@ def prefill_chunked_noalloc(n_seqs, seq_len, h_v, h_k, d_k, d_v, q, k, v,
     if raw_status:
         return st
     _check(st, "gdn_prefill_chunked_noalloc")
+
+
+# The entry points below also check the tensors they are given: the kernels
+# index them by the sizes alone, so a wrong element type, a view that is not
+# contiguous, too few elements or another device is refused here.
+def _tensor(t, name, dtype, numel):
+    if (t.dtype is not dtype or not t.is_contiguous() or t.numel() < numel
+            or not t.is_cuda):
+        raise ValueError(
+            "%s: expected a contiguous device tensor of %s with %d elements, "
+            "got %s %s on %s%s" % (name, dtype, numel, t.dtype,
+                                   tuple(t.shape), t.device,
+                                   "" if t.is_contiguous() else
+                                   ", not contiguous"))
+    return t.data_ptr()
+
+
+def _optional(t, name, dtype, numel):
+    return None if t is None else _tensor(t, name, dtype, numel)
+
+
+def _one_device(*tensors):
+    import torch
+    at = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != at:
+            raise ValueError("a tensor is on %s, the current device is cuda:%d"
+                             % (t.device, at))
+
+
+def _floats():
+    import torch
+    return torch.float32, torch.int32, torch.uint8
+
+
+def decay_step(dims: Dims, t_lane, q, k, v, g, S, o, scale=1.0,
+               head_decay=False, keep_state=False, stream=None,
+               raw_status=False):
+    """gdn_decay_step on torch tensors.  keep_state=True is the verify of a
+    window, o=None (q may be None then) with t_lane = m its commit."""
+    f32, _, _ = _floats()
+    lanes = _int_array(t_lane, dims.n_lanes)
+    kind = k.dtype
+    code = _dtype_code(k)
+    rows = dims.n_layers * dims.n_lanes * dims.t_max
+    nk, nv = rows * dims.h_k * dims.d_k, rows * dims.h_v * dims.d_v
+    ng = dims.n_layers * dims.h_v if head_decay else rows * dims.h_v
+    ns = dims.n_layers * dims.n_lanes * dims.h_v * dims.d_k * dims.d_v
+    _one_device(q, k, v, g, S, o)
+    st = lib.gdn_decay_step(
+        ctypes.byref(dims), lanes, _optional(q, "q", kind, nk),
+        _tensor(k, "k", kind, nk), _tensor(v, "v", kind, nv), code,
+        _tensor(g, "g", f32, ng), _tensor(S, "S", f32, ns),
+        _optional(o, "o", f32, nv), float(scale),
+        (GDN_FLAG_HEAD_DECAY if head_decay else 0) |
+        (GDN_FLAG_KEEP_STATE if keep_state else 0), _stream(stream))
+    if raw_status:
+        return st
+    _check(st, "gdn_decay_step")
+
+
+def _lengths(seq_len):
+    vals = [int(x) for x in seq_len]
+    return len(vals), (ctypes.c_int32 * max(len(vals), 1))(*vals), sum(vals)
+
+
+def decay_prefill_workspace_bytes(seq_len, h_v, h_k, d_k, d_v) -> int:
+    n, arr, _ = _lengths(seq_len)
+    return int(lib.gdn_decay_prefill_workspace_bytes(n, arr, h_v, h_k, d_k,
+                                                     d_v))
+
+
+def decay_prefill(seq_len, h_v, h_k, d_k, d_v, q, k, v, g, S_init, S_final, o,
+                  workspace, scale=1.0, head_decay=False, stream=None,
+                  raw_status=False):
+    """gdn_decay_prefill on torch tensors; seq_len lists the lengths of the
+    packed sequences."""
+    f32, _, u8 = _floats()
+    n, arr, tokens = _lengths(seq_len)
+    kind = k.dtype
+    code = _dtype_code(k)
+    nk, nv, ns = tokens * h_k * d_k, tokens * h_v * d_v, n * h_v * d_k * d_v
+    ws_bytes = 0 if workspace is None else workspace.numel()
+    _one_device(q, k, v, g, S_init, S_final, o, workspace)
+    st = lib.gdn_decay_prefill(
+        n, arr, h_v, h_k, d_k, d_v, _optional(q, "q", kind, nk),
+        _tensor(k, "k", kind, nk), _tensor(v, "v", kind, nv), code,
+        _tensor(g, "g", f32, h_v if head_decay else tokens * h_v),
+        _optional(S_init, "S_init", f32, ns),
+        _optional(S_final, "S_final", f32, ns), _optional(o, "o", f32, nv),
+        _optional(workspace, "workspace", u8, 0), ws_bytes, float(scale),
+        GDN_FLAG_HEAD_DECAY if head_decay else 0, _stream(stream))
+    if raw_status:
+        return st
+    _check(st, "gdn_decay_prefill")
+
+
+def paged_attention_workspace_bytes(dims: KvDims) -> int:
+    return int(lib.gdn_paged_attention_workspace_bytes(ctypes.byref(dims)))
+
+
+def paged_attention(dims: KvDims, t_lane, q, k_cache, v_cache, page_table,
+                    kv_len, o, workspace, scale=1.0, stream=None,
+                    raw_status=False):
+    """gdn_paged_attention on torch tensors."""
+    f32, i32, u8 = _floats()
+    lanes = _int_array(t_lane, dims.n_lanes)
+    kind = q.dtype
+    code = _dtype_code(q)
+    nq = dims.n_lanes * dims.t_max * dims.h_q * dims.d
+    nc = dims.n_pages * dims.h_kv * dims.page_size * dims.d
+    ws_bytes = 0 if workspace is None else workspace.numel()
+    _one_device(q, k_cache, v_cache, page_table, kv_len, o, workspace)
+    st = lib.gdn_paged_attention(
+        ctypes.byref(dims), lanes, _tensor(q, "q", kind, nq),
+        _tensor(k_cache, "k_cache", kind, nc),
+        _tensor(v_cache, "v_cache", kind, nc), code,
+        _tensor(page_table, "page_table", i32, dims.n_lanes * dims.max_pages),
+        _tensor(kv_len, "kv_len", i32, dims.n_lanes),
+        _tensor(o, "o", f32, nq), _optional(workspace, "workspace", u8, 0),
+        ws_bytes, float(scale), _stream(stream))
+    if raw_status:
+        return st
+    _check(st, "gdn_paged_attention")
+
+
+def kv_append(dims: KvDims, t_lane, k, v, k_cache, v_cache, page_table,
+              kv_len, stream=None, raw_status=False):
+    """gdn_kv_append on torch tensors."""
+    _, i32, _ = _floats()
+    lanes = _int_array(t_lane, dims.n_lanes)
+    kind = k.dtype
+    code = _dtype_code(k)
+    nr = dims.n_lanes * dims.t_max * dims.h_kv * dims.d
+    nc = dims.n_pages * dims.h_kv * dims.page_size * dims.d
+    _one_device(k, v, k_cache, v_cache, page_table, kv_len)
+    st = lib.gdn_kv_append(
+        ctypes.byref(dims), lanes, _tensor(k, "k", kind, nr),
+        _tensor(v, "v", kind, nr), code,
+        _tensor(k_cache, "k_cache", kind, nc),
+        _tensor(v_cache, "v_cache", kind, nc),
+        _tensor(page_table, "page_table", i32, dims.n_lanes * dims.max_pages),
+        _tensor(kv_len, "kv_len", i32, dims.n_lanes), _stream(stream))
+    if raw_status:
+        return st
+    _check(st, "gdn_kv_append")
+
+
+def token_scores_workspace_bytes(n_rows, vocab, n_top) -> int:
+    return int(lib.gdn_token_scores_workspace_bytes(n_rows, vocab, n_top))
+
+
+def token_scores(logits, tokens, n_top, logprob, entropy, top_ids,
+                 top_logprobs, workspace, inv_temperature=1.0, stream=None,
+                 raw_status=False):
+    """gdn_token_scores on torch tensors.  logits is [n_rows, vocab] with
+    contiguous rows (their stride may be larger than vocab)."""
+    f32, i32, u8 = _floats()
+    code = _dtype_code(logits)
+    if logits.dim() != 2 or not logits.is_cuda or (
+            logits.size(1) > 1 and logits.stride(1) != 1):
+        raise ValueError("logits: expected a device tensor [n_rows, vocab] "
+                         "with contiguous rows")
+    rows, vocab = logits.shape
+    stride = logits.stride(0) if rows > 1 else vocab
+    ws_bytes = 0 if workspace is None else workspace.numel()
+    _one_device(logits, tokens, logprob, entropy, top_ids, top_logprobs,
+                workspace)
+    st = lib.gdn_token_scores(
+        rows, vocab, stride, logits.data_ptr(), code,
+        _optional(tokens, "tokens", i32, rows), n_top, float(inv_temperature),
+        _optional(logprob, "logprob", f32, rows),
+        _optional(entropy, "entropy", f32, rows),
+        _optional(top_ids, "top_ids", i32, rows * n_top),
+        _optional(top_logprobs, "top_logprobs", f32, rows * n_top),
+        _optional(workspace, "workspace", u8, 0), ws_bytes, _stream(stream))
+    if raw_status:
+        return st
+    _check(st, "gdn_token_scores")

@@ -63,6 +63,7 @@
 #include <type_traits>
 
 #include "gdn.h"
+#include "gdn_decay.h"
 #include "gdn_internal.h"
 
 namespace gdnp {

@@ -26,6 +26,8 @@
 
 #include "gdn.h"
 #include "gdn_internal.h"
+#include "gdn_paged.h"
+#include "gdn_scores.h"
 
 namespace gdns {
 

@@ -26,6 +26,15 @@
  *   gdn_prefill_chunked_noalloc  the same with the library's fixed scratch
  *                        array as workspace, for callers that cannot
  *                        allocate.
+ *   gdn_decay_prefill,   linear attention with a decay per head and no delta
+ *   gdn_decay_step       write: packed prompts in chunks, and windows or
+ *                        single tokens step by step.
+ *   gdn_paged_attention, the full-attention layers of a hybrid model: draft
+ *   gdn_kv_append        windows or single tokens against a paged key-value
+ *                        cache, and the cache's writer.
+ *   gdn_token_scores     log probabilities of given tokens, entropies and
+ *                        top alternatives of rows of logits: what the
+ *                        accepted prefix m of a window is decided from.
  *
  * The rule (Yang, Kautz & Hatamizadeh, "Gated Delta Networks: Improving
  * Mamba2 with Delta Rule", ICLR 2025, Sec. 3), per value head with state S
@@ -95,7 +104,9 @@ typedef enum { GDN_BF16 = 0, GDN_F32 = 1 } gdn_dtype;
 enum {
   GDN_FLAG_L2NORM_QK = 1,        /* normalise q and k inside the kernels */
   GDN_FLAG_PREFILL_ONE_CHAIN = 2, /* gdn_prefill_chunked*: never in segments */
-  GDN_FLAG_TOKENWISE = 4         /* the verify calls: always token by token */
+  GDN_FLAG_TOKENWISE = 4,        /* the verify calls: always token by token */
+  GDN_FLAG_HEAD_DECAY = 8,       /* gdn_decay_*: g holds one constant a head */
+  GDN_FLAG_KEEP_STATE = 16       /* gdn_decay_step: S is read, not written  */
 };
 
 typedef struct {
@@ -404,6 +415,176 @@ int gdn_state_snapshot(const gdn_dims* dims, int32_t n_sel,
 int gdn_state_restore(const gdn_dims* dims, int32_t n_sel,
                       const int32_t* lanes, const float* snapshot, float* S,
                       void* stream);
+
+/*
+ * Linear attention with a decay per head (the rule of retention and of
+ * scalar-gated state-space layers; the GDN rule without its delta write).
+ * Per value head h with key head h / (h_v / h_k) and state S (stored
+ * [d_k][d_v] as everywhere):
+ *
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T
+ *   o_t = scale * S_t^T q_t
+ *
+ * q and k are used as they are (no norm).  g is the log-decay: one value per
+ * token and value head, or with GDN_FLAG_HEAD_DECAY one constant per value
+ * head.  A gate below -1000 (-inf among them) counts as -1000, whose decay
+ * is 0 in f32 all the same.  Every state, sum and decay is f32 or wider.
+ *
+ * gdn_decay_step: the recurrent form, for single tokens (t_max = 1) and
+ * draft windows.  Advances every (layer, lane, value head) by t_lane[lane]
+ * tokens, one token at a time in f32, so that the state and the outputs
+ * after a token do not depend, bit for bit, on how the tokens were split
+ * into windows.  The window protocol needs no records here: the inputs are
+ * the transitions.  Verify is a call with GDN_FLAG_KEEP_STATE, commit of a
+ * prefix m a call on the same inputs with t_lane = m and o = NULL.
+ *   dims     as for gdn_verify (d_k 16, 32, 64 or 128; d_v 1..1024)
+ *   t_lane   host int32[n_lanes], 0..t_max (0: nothing of the lane is read
+ *            or written)
+ *   q, k, v  device, in_dtype, layouts as for gdn_verify (q may be NULL
+ *            when o is)
+ *   g        device f32 [n_layers][n_lanes][t_max][h_v], or [n_layers][h_v]
+ *            with GDN_FLAG_HEAD_DECAY
+ *   S        device f32 [n_layers][n_lanes][h_v][d_k][d_v], advanced in
+ *            place (read only with GDN_FLAG_KEEP_STATE)
+ *   o        device f32 [n_layers][n_lanes][t_max][h_v][d_v], or NULL
+ *   flags    GDN_FLAG_HEAD_DECAY, GDN_FLAG_KEEP_STATE (not with o = NULL)
+ * Every device pointer must be 16-byte aligned (GDN_EINVAL).
+ */
+int gdn_decay_step(const gdn_dims* dims, const int32_t* t_lane, const void* q,
+                   const void* k, const void* v, int in_dtype, const float* g,
+                   float* S, float* o, float scale, int flags, void* stream);
+
+/*
+ * Workspace bytes that gdn_decay_prefill needs for these sizes (0 when none
+ * is needed, and for invalid or unsupported sizes).
+ */
+size_t gdn_decay_prefill_workspace_bytes(int32_t n_seqs,
+                                         const int32_t* seq_len, int32_t h_v,
+                                         int32_t h_k, int32_t d_k,
+                                         int32_t d_v);
+
+/*
+ * The same rule over whole prompts of different lengths, packed one after
+ * another without padding.
+ *   n_seqs   1..GDN_MAX_LANES sequences
+ *   seq_len  host int32[n_seqs], >= 0 (0: S_final is S_init, or zero); the
+ *            sum is the number of token rows
+ *   q, k     device [tokens][h_k][d_k] in_dtype (bf16 or f32)
+ *   v        device [tokens][h_v][d_v] in_dtype
+ *   g        device f32 [tokens][h_v], or [h_v] with GDN_FLAG_HEAD_DECAY
+ *   S_init   device f32 [n_seqs][h_v][d_k][d_v], or NULL (zero states)
+ *   S_final  device f32, same shape, or NULL; may be S_init itself (other
+ *            overlaps are undefined)
+ *   o        device f32 [tokens][h_v][d_v], or NULL when only the states
+ *            are wanted (q may then be NULL); not both NULL
+ *   workspace  device, ws_bytes >= gdn_decay_prefill_workspace_bytes(...)
+ *            (may be NULL when that is 0); calls that overlap in time need
+ *            workspaces of their own
+ *   flags    GDN_FLAG_HEAD_DECAY or 0
+ * Sizes: d_k 16, 32, 64 or 128, d_v 1..1024, h_v a multiple of h_k.
+ * Every device pointer must be 16-byte aligned (GDN_EINVAL).
+ */
+int gdn_decay_prefill(int32_t n_seqs, const int32_t* seq_len, int32_t h_v,
+                      int32_t h_k, int32_t d_k, int32_t d_v, const void* q,
+                      const void* k, const void* v, int in_dtype,
+                      const float* g, const float* S_init, float* S_final,
+                      float* o, void* workspace, size_t ws_bytes, float scale,
+                      int flags, void* stream);
+
+/*
+ * Attention of draft windows or single tokens over a paged key-value cache
+ * (the full-attention layers of a hybrid model; GDN / KDA state and key-value
+ * history live side by side in the review's engine, section "Architecture 2:
+ * context byte pool and prefix reuse").
+ */
+typedef struct {
+  int32_t n_lanes;   /* 1..GDN_MAX_LANES requests                          */
+  int32_t t_max;     /* 1..GDN_MAX_T: window stride (new tokens per lane)  */
+  int32_t h_q;       /* query heads, a multiple of h_kv                    */
+  int32_t h_kv;      /* key-value heads                                    */
+  int32_t d;         /* head dim: 64, 128 or 256                           */
+  int32_t page_size; /* token rows per page, >= 1                          */
+  int32_t n_pages;   /* pages in the cache, >= 1                           */
+  int32_t max_pages; /* columns of the page table, >= 1;                   */
+                     /* max_pages * page_size < 2^30                       */
+} gdn_kv_dims;
+
+/*
+ *   t_lane      host int32[n_lanes], 0..t_max new tokens (0: nothing of the
+ *               lane is read or written)
+ *   q           device [n_lanes][t_max][h_q][d], dtype (bf16 or f32)
+ *   k_cache, v_cache  device [n_pages][h_kv][page_size][d], dtype
+ *   page_table  device int32 [n_lanes][max_pages]: row i of page j of a lane
+ *               is position j * page_size + i.  A page number outside
+ *               0..n_pages-1 is never read: its positions are masked.
+ *   kv_len      device int32[n_lanes]: positions the lane's cache holds, the
+ *               new tokens' own rows (see gdn_kv_append) the last t_lane of
+ *               them; taken as 0..max_pages*page_size
+ *   o           device f32 [n_lanes][t_max][h_q][d]: softmax over positions
+ *               0 .. kv_len - t_lane + t of scale * (q_t . k), times v.  A
+ *               token that sees no position gets zeros.  What masked rows of
+ *               the cache hold (NaN, infinities) does not matter.
+ *   workspace   device, ws_bytes >= gdn_paged_attention_workspace_bytes(dims)
+ *               (which depends on the dims alone; 0 for invalid dims); calls
+ *               that overlap in time need workspaces of their own
+ * Query head h reads key-value head h / (h_q / h_kv).  page_table and kv_len
+ * are read when the kernels run, so a captured call follows them.  Scores,
+ * softmax sums and outputs are f32 or wider.  q, the caches, o and the
+ * workspace must be 16-byte aligned (GDN_EINVAL).
+ */
+size_t gdn_paged_attention_workspace_bytes(const gdn_kv_dims* dims);
+int gdn_paged_attention(const gdn_kv_dims* dims, const int32_t* t_lane,
+                        const void* q, const void* k_cache,
+                        const void* v_cache, int dtype,
+                        const int32_t* page_table, const int32_t* kv_len,
+                        float* o, void* workspace, size_t ws_bytes,
+                        float scale, void* stream);
+
+/*
+ * Writes the key and value rows of new tokens into the cache: token t of
+ * lane n goes to position kv_len[n] - t_lane[n] + t, that is kv_len counts
+ * the new tokens already, as gdn_paged_attention wants it.  A row whose
+ * position is negative or past the page table, or whose page number is
+ * outside 0..n_pages-1, is dropped.  Rows that two lanes place in one page
+ * row (a page listed twice) are in undefined order.
+ *   k, v     device [n_lanes][t_max][h_kv][d], dtype; the rest as above
+ */
+int gdn_kv_append(const gdn_kv_dims* dims, const int32_t* t_lane,
+                  const void* k, const void* v, int dtype, void* k_cache,
+                  void* v_cache, const int32_t* page_table,
+                  const int32_t* kv_len, void* stream);
+
+/*
+ * Log probabilities of given tokens, with entropy and top alternatives, for
+ * rows of logits: x = inv_temperature * logit, p = softmax(x).
+ *   n_rows, vocab  >= 1
+ *   row_stride  elements from one row of logits to the next, >= vocab
+ *   logits      device, in_dtype (bf16 or f32), element-aligned
+ *   tokens      device int32[n_rows] or NULL (then logprob is NULL too)
+ *   n_top       0..GDN_MAX_TOP and at most vocab
+ *   inv_temperature  finite, > 0
+ *   logprob     device f32[n_rows]: log p of the row's token; 0 for a
+ *               negative token (no token given), NaN for one >= vocab
+ *   entropy     device f32[n_rows] or NULL: -sum p log p
+ *   top_ids, top_logprobs  device int32 / f32 [n_rows][n_top] (may be NULL
+ *               when n_top is 0): the largest logits, largest first, equal
+ *               ones by the lower id, and their log p
+ * A logit of -inf has probability 0 (log p = -inf, nothing in the entropy).
+ * A row of nothing but -inf gives log p = -inf and entropy 0; a row that
+ * holds a NaN or +inf gives NaN in every f32 output (a negative token's 0
+ * excepted) and -1 in top_ids.
+ *   workspace   device, 16-byte aligned, ws_bytes >=
+ *               gdn_token_scores_workspace_bytes(...); calls that overlap in
+ *               time need workspaces of their own
+ */
+#define GDN_MAX_TOP 32
+size_t gdn_token_scores_workspace_bytes(int32_t n_rows, int32_t vocab,
+                                        int32_t n_top);
+int gdn_token_scores(int32_t n_rows, int32_t vocab, int64_t row_stride,
+                     const void* logits, int in_dtype, const int32_t* tokens,
+                     int32_t n_top, float inv_temperature, float* logprob,
+                     float* entropy, int32_t* top_ids, float* top_logprobs,
+                     void* workspace, size_t ws_bytes, void* stream);
 
 /* Static description of a status code; never NULL. */
 const char* gdn_strerror(int status);
