@@ -20,11 +20,6 @@ using gdn::misaligned;
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// Tokens of sequence s are the rows start[s] .. start[s + 1] - 1.
-struct SeqTable {
-  int start[GDN_MAX_LANES + 1];
-};
-
 struct DecayArgs {
   const void *q, *k, *v;
   const float* g;
@@ -206,28 +201,579 @@ __global__ __launch_bounds__(256) void step_kernel(DecayArgs p,
       ks, vs, p.per_head ? 0 : p.h_v, T, p.d_v, col0, p.scale);
 }
 
-template <int DK, typename TIn, bool V4>
-__global__ __launch_bounds__(256) void prompt_chain_kernel(DecayArgs p,
-                                                           SeqTable seq) {
-  const int ncb = (p.d_v + kStepCols - 1) / kStepCols;
-  const long unit = (long)blockIdx.x * 4 + threadIdx.x / 64;
-  const long item = unit / ncb;
-  const int col0 = (int)(unit % ncb) * kStepCols;
-  const int h = (int)(item % p.h_v);
-  const long s = item / p.h_v;
-  if (s >= p.lanes) return;
-  const long tok = seq.start[s];
-  const int T = seq.start[s + 1] - seq.start[s];
-  const int hk = h / (p.h_v / p.h_k);
-  const long ks = (long)p.h_k * DK, vs = (long)p.h_v * p.d_v;
-  const long qo = tok * ks + (long)hk * DK, vo = tok * vs + (long)h * p.d_v;
-  const long so = item * DK * p.d_v;
-  decay_chain<DK, TIn, V4>(
-      (const TIn*)p.q + qo, (const TIn*)p.k + qo, (const TIn*)p.v + vo,
-      p.per_head ? p.g + h : p.g + tok * p.h_v + h,
-      p.s_in ? p.s_in + so : nullptr, p.s_out ? p.s_out + so : nullptr,
-      p.o ? p.o + vo : nullptr, ks, vs, p.per_head ? 0 : p.h_v, T, p.d_v, col0,
-      p.scale);
+// -------------------------------------------------------------- chunked form
+// Prompts run in chunks of 64 tokens.  With b_t the sum of the chunk's gates
+// up to token t, B the whole sum and S0 the state before the chunk:
+//   o_t = scale (exp(b_t) S0^T q_t + sum_{s <= t} exp(b_t - b_s)(q_t.k_s) v_s)
+//   S   = exp(B) S0 + sum_s k_s (exp(B - b_s) v_s)^T
+// Four products per chunk: Q K^T, Q S0, P V and K^T W, all on the matrix
+// cores.  bf16 operands enter exactly; f32 ones (S0, P, W) as two bf16 parts,
+// hi + lo, off by at most 2^-18 of each entry: one part alone would put the
+// f32 outputs and states 2^-9 off.  f32 inputs use the f32 matrix cores.
+//
+// The transposed forms are computed (O^T = S0^T Q^T + V^T P^T with
+// P^T = mask(K Q^T)), because then every intermediate is born in the layout
+// the next product reads, and only V and K need a transposed read from LDS:
+//   * K Q^T leaves its 16 x 16 result at lane (g, n) as rows (tokens s)
+//     4g + e of column (token t) n; two such tiles are the B operand of
+//     V^T P^T when slot (g, e) of the 32-token step stands for token 4g + e
+//     (e < 4) or 16 + 4g + e - 4 of it.
+//   * the state is held as lane (g, n) = column n, rows 32 ks + 8 g + e: the
+//     A operand of S0^T Q^T.  K^T W lands on it when row m of the A operand
+//     stands for state row 8 (m / 4) + 4 a + m % 4 of its 32 (a = 0, 1 the
+//     two halves).
+//   * a token's decays belong to one lane (column n) of O^T.
+// A workgroup of four waves takes 4 CW columns of d_v of one head; every
+// wave holds its CW columns of the state in registers and never exchanges
+// anything but the staged rows.  (Each wave forms all of K Q^T itself: 40 of
+// its 192 matrix instructions per chunk, against a barrier and an LDS round
+// trip of P in two parts.)
+//
+// Long sequences are cut into segments so that a launch fills the GPU: a
+// first pass forms each segment's own state (from zero) and decay, a scan
+// turns those into the segments' start states, and the output pass runs all
+// segments at once.
+constexpr int kChunk = 64;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Operand fragments of eight k-slots.  Raw: inputs as they are; Wide: f32
+// values.
+template <typename TIn>
+struct Op;
+
+template <>
+struct Op<uint16_t> {
+  typedef u32x4 Raw;
+  struct Wide {
+    u32x4 hi, lo;
+  };
+  static __device__ __forceinline__ f32x4 mul(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+        __builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+        0);
+  }
+  static __device__ __forceinline__ f32x4 mul(const Wide& a, u32x4 b, f32x4 c) {
+    return mul(a.hi, b, mul(a.lo, b, c));
+  }
+  static __device__ __forceinline__ f32x4 mul(u32x4 a, const Wide& b, f32x4 c) {
+    return mul(a, b.hi, mul(a, b.lo, c));
+  }
+  // x = hi + lo, each rounded to nearest even.
+  static __device__ __forceinline__ Wide wide(f32x4 x, f32x4 y) {
+    Wide w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 v = i < 2 ? f32x2{x[2 * i], x[2 * i + 1]}
+                            : f32x2{y[2 * i - 4], y[2 * i - 3]};
+      const uint32_t h =
+          __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+      const f32x2 r = {v[0] - __uint_as_float(h << 16),
+                       v[1] - __uint_as_float(h & 0xffff0000u)};
+      w.hi[i] = h;
+      w.lo[i] =
+          __builtin_bit_cast(uint32_t, __builtin_convertvector(r, bf16x2));
+    }
+    return w;
+  }
+  // Slots e = 0..7 of a raw fragment as f32, times s.
+  static __device__ __forceinline__ Wide scaled(u32x4 a, f32x4 s0, f32x4 s1) {
+    f32x4 x, y;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x[2 * i] = __uint_as_float(a[i] << 16) * s0[2 * i];
+      x[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u) * s0[2 * i + 1];
+      y[2 * i] = __uint_as_float(a[2 + i] << 16) * s1[2 * i];
+      y[2 * i + 1] = __uint_as_float(a[2 + i] & 0xffff0000u) * s1[2 * i + 1];
+    }
+    return wide(x, y);
+  }
+  // Eight consecutive entries of a staged row.
+  static __device__ __forceinline__ u32x4 row(const uint16_t* p) {
+    return *reinterpret_cast<const u32x4*>(p);
+  }
+  // Column reads.  Lane l of 16 l' + i receives rows r .. r + 3 (first half
+  // of the slots) and r + 16 .. r + 19 (second) with r = 4 (l / 16), at the
+  // column given by `col(i)`, i = l % 16.  The transposing LDS read hands
+  // lane i entry i % 4 of the 8 bytes addressed by lane 4 e + i / 4 of its
+  // 16 as its entry e: the lane addresses row r + (i / 4), entries
+  // col0 + step * (i % 4) .. + 3.
+  static __device__ __forceinline__ u32x4 column(const uint16_t* tile,
+                                                 int pitch, int col0,
+                                                 int step, int lane) {
+    const uint16_t* p = tile + (4 * (lane >> 4) + ((lane & 15) >> 2)) * pitch +
+                        col0 + step * (lane & 3);
+    const uint2 a = tr(p), b = tr(p + 16 * pitch);
+    return u32x4{a.x, a.y, b.x, b.y};
+  }
+  static __device__ __forceinline__ uint2 tr(const uint16_t* p) {
+    return __builtin_bit_cast(
+        uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                   (__attribute__((address_space(3))) s16x4*)p));
+  }
+};
+
+template <>
+struct Op<float> {
+  struct Raw {
+    f32x4 x, y;
+  };
+  typedef Raw Wide;
+  static __device__ __forceinline__ f32x4 mul(const Raw& a, const Raw& b,
+                                              f32x4 c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x[e], b.x[e], c, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.y[e], b.y[e], c, 0, 0, 0);
+    return c;
+  }
+  static __device__ __forceinline__ Raw wide(f32x4 x, f32x4 y) {
+    return {x, y};
+  }
+  static __device__ __forceinline__ Raw scaled(const Raw& a, f32x4 s0,
+                                               f32x4 s1) {
+    return {a.x * s0, a.y * s1};
+  }
+  static __device__ __forceinline__ Raw row(const float* p) {
+    return {reinterpret_cast<const f32x4*>(p)[0],
+            reinterpret_cast<const f32x4*>(p)[1]};
+  }
+  static __device__ __forceinline__ Raw column(const float* tile, int pitch,
+                                               int col0, int step, int lane) {
+    const int i = lane & 15;
+    const float* p =
+        tile + 4 * (lane >> 4) * pitch + col0 + step * (i >> 2) + (i & 3);
+    Raw r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      r.x[e] = p[e * pitch];
+      r.y[e] = p[(16 + e) * pitch];
+    }
+    return r;
+  }
+};
+
+// Segments of the sequences: sequence s has the segments first[s] ..
+// first[s + 1] - 1 of seg tokens each (the last one shorter).
+struct SegTable {
+  int n, seg;
+  int first[GDN_MAX_LANES + 1];
+  int start[GDN_MAX_LANES + 1];  // token rows start[s] .. start[s + 1] - 1
+};
+
+struct ChunkArgs {
+  DecayArgs a;
+  int d_k;
+  float* slots;  // [segments][h_v][d_k][d_v]: start states of the segments
+  float* decay;  // [segments][h_v]: decay over a whole segment
+};
+
+// Sequence of a segment.
+__device__ __forceinline__ int seq_of(const SegTable& t, int seg) {
+  int lo = 0, hi = t.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (t.first[mid] <= seg) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Inclusive sum over the 64 lanes in f64 (DPP row shifts, then the sums of
+// the rows before).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_part(double x) {
+  const long v = __builtin_bit_cast(long, x);
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+  const int hi =
+      __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, ((long)hi << 32) | (uint32_t)lo);
+}
+__device__ __forceinline__ double wave_scan(double x) {
+  x += dpp_part<0x111, 0xf>(x);  // row_shr 1, 2, 4, 8
+  x += dpp_part<0x112, 0xf>(x);
+  x += dpp_part<0x114, 0xf>(x);
+  x += dpp_part<0x118, 0xf>(x);
+  x += dpp_part<0x142, 0xa>(x);  // row_bcast 15 into rows 1 and 3
+  x += dpp_part<0x143, 0xc>(x);  // row_bcast 31 into rows 2 and 3
+  return x;
+}
+
+constexpr double kLog2e = 1.4426950408889634;
+
+// Decays of a chunk's tokens, in LDS.  Sums of gates are kept in f64 and
+// handed on as hi + lo pairs of f32 (in units of log 2), so that differences
+// of large sums keep their small values.
+struct Gates {
+  float2 b[kChunk];      // sum of the gates up to the token
+  float in[kChunk];      // exp(b_t)
+  float out[kChunk];     // exp(B - b_t)
+  float all;             // exp(B)
+};
+
+__device__ __forceinline__ double set_gates(Gates& G, float g, int lane) {
+  g = g < -1000.f ? -1000.f : g;
+  const double b = wave_scan((double)g * kLog2e);
+  const long bits = __builtin_bit_cast(long, b);
+  const double B = __builtin_bit_cast(
+      double, ((long)__builtin_amdgcn_readlane((int)(bits >> 32), 63) << 32) |
+                  (uint32_t)__builtin_amdgcn_readlane((int)bits, 63));
+  const float hi = (float)b;
+  G.b[lane] = make_float2(hi, (float)(b - (double)hi));
+  G.in[lane] = __builtin_amdgcn_exp2f((float)b);
+  G.out[lane] = __builtin_amdgcn_exp2f((float)(B - b));
+  if (lane == 0) G.all = __builtin_amdgcn_exp2f((float)B);
+  return B;
+}
+
+// 64 token rows of W entries of a tensor in transit from memory to LDS: each
+// thread holds pieces of 16 bytes.
+template <typename TIn, int W>
+struct Transit {
+  static constexpr int kPer = 16 / sizeof(TIn);  // entries per piece
+  static constexpr int kPieces = kChunk * W / kPer / 256;
+  static constexpr int kPitch = W + kPer;
+  u32x4 r[kPieces];
+  // Rows base[t * stride], entries 0 .. n - 1; rows from `rows` on and
+  // entries past n read as zero.  VEC: rows are 16-byte aligned and n is a
+  // multiple of kPer.
+  template <bool VEC>
+  __device__ __forceinline__ void load(const TIn* __restrict__ base,
+                                       long stride, int rows, int n) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int p = threadIdx.x + 256 * i;
+      const int t = p / (W / kPer), c = p % (W / kPer) * kPer;
+      r[i] = u32x4{0, 0, 0, 0};
+      if (t < rows) {
+        const TIn* src = base + t * stride + c;
+        if constexpr (VEC) {
+          if (c < n) r[i] = *reinterpret_cast<const u32x4*>(src);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e)
+            if (c + e < n) {
+              if constexpr (sizeof(TIn) == 4)
+                r[i][e] = __float_as_uint((float)src[e]);
+              else
+                r[i][e / 2] |= (uint32_t)src[e] << (16 * (e & 1));
+            }
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(TIn* tile) const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int p = threadIdx.x + 256 * i;
+      const int t = p / (W / kPer), c = p % (W / kPer) * kPer;
+      *reinterpret_cast<u32x4*>(tile + t * kPitch + c) = r[i];
+    }
+  }
+};
+
+// What a chunk kernel is for: the states of segments from zero (kLocal), or
+// outputs and final states from the segments' start states (kOutput).
+enum { kLocal = 0, kOutput = 1 };
+
+template <int DK, int CW, typename TIn, int MODE, bool VEC>
+__global__ __launch_bounds__(256, 2) void chunk_kernel(ChunkArgs p,
+                                                       SegTable tab,
+                                                       int last_only) {
+  typedef Op<TIn> O;
+  typedef typename O::Raw Raw;
+  constexpr int KS = DK / 32, CT = CW / 16, W = 4 * CW;
+  typedef Transit<TIn, DK> KT;
+  typedef Transit<TIn, W> VT;
+  __shared__ __attribute__((aligned(16))) TIn Ks[kChunk * KT::kPitch];
+  __shared__ __attribute__((aligned(16))) TIn Qs[MODE == kOutput ? kChunk * KT::kPitch : 8];
+  __shared__ __attribute__((aligned(16))) TIn Vs[kChunk * VT::kPitch];
+  __shared__ __attribute__((aligned(16))) Gates G;
+
+  const DecayArgs& a = p.a;
+  const int ncb = (a.d_v + W - 1) / W;
+  int item = gdn::xcd_item(blockIdx.x, gridDim.x);
+  const int cb = item % ncb;
+  item /= ncb;
+  const int h = item % a.h_v;
+  item /= a.h_v;
+  // the segment: all of them, or (last_only) the last of each sequence, or
+  // (kLocal) all but the last of each sequence
+  int s, seg;
+  if (last_only) {
+    s = item;
+    seg = tab.first[s + 1] - 1;
+  } else if (MODE == kLocal) {
+    int lo = 0, hi = tab.n - 1;  // first[s] - s segments lie before sequence s
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (tab.first[mid] - mid <= item) lo = mid;
+      else hi = mid - 1;
+    }
+    s = lo;
+    seg = item + s;
+  } else {
+    seg = item;
+    s = seq_of(tab, seg);
+  }
+  const int nth = seg - tab.first[s], n_seg = tab.first[s + 1] - tab.first[s];
+  const long tok0 = (long)tab.start[s] + (long)nth * tab.seg;
+  const long rest = tab.start[s + 1] - tok0;
+  const int T = rest < tab.seg ? (int)rest : tab.seg;
+  const bool last = nth == n_seg - 1;
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = lane & 15, g4 = lane >> 4;
+  const int hk = h / (a.h_v / a.h_k);
+  const int col = cb * W, wcol = wave * CW;  // of d_v; of the block
+  const int cols = a.d_v - col < W ? a.d_v - col : W;
+  const long ks = (long)a.h_k * p.d_k, vs = (long)a.h_v * a.d_v;
+  const TIn* __restrict__ K = (const TIn*)a.k + tok0 * ks + (long)hk * p.d_k;
+  const TIn* __restrict__ Q = (const TIn*)a.q + tok0 * ks + (long)hk * p.d_k;
+  const TIn* __restrict__ V = (const TIn*)a.v + tok0 * vs + (long)h * a.d_v + col;
+  const float* __restrict__ g = a.per_head ? a.g + h : a.g + tok0 * a.h_v + h;
+  const long gs = a.per_head ? 0 : a.h_v;
+  float* __restrict__ out =
+      MODE == kOutput && a.o ? a.o + tok0 * vs + (long)h * a.d_v + col : nullptr;
+
+  // state entry (32 ks + 8 g4 + 4 a + e, column 16 ct + n): st[ct][ks][a][e]
+  f32x4 st[CT][KS][2];
+  const float* from = nullptr;
+  if constexpr (MODE == kOutput) {
+    if (n_seg > 1 && (nth > 0 || a.s_in))
+      from = p.slots + ((long)seg * a.h_v + h) * p.d_k * a.d_v;
+    else if (n_seg == 1 && a.s_in)
+      from = a.s_in + ((long)s * a.h_v + h) * p.d_k * a.d_v;
+  }
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = 32 * i + 8 * g4 + 4 * x + e, c = wcol + 16 * ct + n;
+          st[ct][i][x][e] = from && j < p.d_k && c < cols
+                                ? from[(long)j * a.d_v + col + c]
+                                : 0.f;
+        }
+
+  KT kt, qt;
+  VT vt;
+  float gate = 0.f;
+  double total = 0.0;
+  auto fetch = [&](int t0) {
+    const int rows = T - t0;
+    kt.template load<true>(K + t0 * ks, ks, rows, p.d_k);
+    if constexpr (MODE == kOutput) {
+      if (out) qt.template load<true>(Q + t0 * ks, ks, rows, p.d_k);
+    }
+    vt.template load<VEC>(V + t0 * vs, vs, rows, cols);
+    gate = lane < rows ? g[(t0 + lane) * gs] : 0.f;
+  };
+  auto place = [&]() {
+    kt.store(Ks);
+    if constexpr (MODE == kOutput) {
+      if (out) qt.store(Qs);
+    }
+    vt.store(Vs);
+    if (wave == 0) total += set_gates(G, gate, lane);
+  };
+
+  if (T > 0) {
+    fetch(0);
+    place();
+  }
+  for (int t0 = 0; t0 < T; t0 += kChunk) {
+    __syncthreads();
+    const bool more = t0 + kChunk < T;
+    if (more) fetch(t0 + kChunk);
+    Raw vf[2][CT];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+        vf[x][ct] = O::column(Vs + 32 * x * VT::kPitch, VT::kPitch,
+                              wcol + 16 * ct, 4, lane);
+    if constexpr (MODE == kOutput) {
+      if (out) {
+        // O^T of the state: tokens 16 j + n, columns 16 ct + 4 g4 + e
+        f32x4 acc[CT][4];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[ct][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          typename O::Wide sw[CT];
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct)
+            sw[ct] = O::wide(st[ct][i][0], st[ct][i][1]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const Raw qf =
+                O::row(Qs + (16 * j + n) * KT::kPitch + 32 * i + 8 * g4);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+              acc[ct][j] = O::mul(sw[ct], qf, acc[ct][j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t = 16 * j + n;
+          const float in = G.in[t];
+          const float2 bt = G.b[t];
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) acc[ct][j] *= in;
+          // P^T of the tokens s of blocks 0 .. j
+          f32x4 pt[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pt[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int x = 0; x < KS; ++x) {
+            const Raw qf =
+                O::row(Qs + (16 * j + n) * KT::kPitch + 32 * x + 8 * g4);
+#pragma unroll
+            for (int i = 0; i <= j; ++i)
+              pt[i] = O::mul(
+                  O::row(Ks + (16 * i + n) * KT::kPitch + 32 * x + 8 * g4), qf,
+                  pt[i]);
+          }
+#pragma unroll
+          for (int i = 0; i <= j; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int sr = 16 * i + 4 * g4 + e;
+              const float2 bs = G.b[sr];
+              const float w = __builtin_amdgcn_exp2f((bt.x - bs.x) +
+                                                     (bt.y - bs.y));
+              pt[i][e] = sr <= t ? pt[i][e] * w : 0.f;
+            }
+#pragma unroll
+          for (int x = 0; x <= j / 2; ++x) {
+            const typename O::Wide pw = O::wide(pt[2 * x], pt[2 * x + 1]);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+              acc[ct][j] = O::mul(vf[x][ct], pw, acc[ct][j]);
+          }
+          if (t0 + t < T) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+              const int c = wcol + 16 * ct + 4 * g4;
+              float* dst = out + (t0 + t) * vs + c;
+              const f32x4 y = acc[ct][j] * a.scale;
+              if constexpr (VEC) {
+                if (c < cols) *reinterpret_cast<f32x4*>(dst) = y;
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (c + e < cols) dst[e] = y[e];
+              }
+            }
+          }
+        }
+      }
+    }
+    // the state after the chunk
+    const float all = G.all;
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) st[ct][i][x] *= all;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const f32x4 w0 = *reinterpret_cast<const f32x4*>(&G.out[32 * x + 4 * g4]);
+      const f32x4 w1 =
+          *reinterpret_cast<const f32x4*>(&G.out[32 * x + 16 + 4 * g4]);
+      typename O::Wide ww[CT];
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) ww[ct] = O::scaled(vf[x][ct], w0, w1);
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const Raw kf = O::column(Ks + 32 * x * KT::kPitch, KT::kPitch,
+                                   32 * i + 4 * y, 8, lane);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct)
+            st[ct][i][y] = O::mul(kf, ww[ct], st[ct][i][y]);
+        }
+    }
+    __syncthreads();
+    if (more) place();
+  }
+
+  float* to = nullptr;
+  if constexpr (MODE == kLocal) {
+    to = p.slots + ((long)(seg + 1) * a.h_v + h) * p.d_k * a.d_v;
+    if (tid == 0 && cb == 0)
+      p.decay[(long)seg * a.h_v + h] = __builtin_amdgcn_exp2f((float)total);
+  } else if (last && a.s_out) {
+    to = a.s_out + ((long)s * a.h_v + h) * p.d_k * a.d_v;
+  }
+  if (to) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = 32 * i + 8 * g4 + 4 * x + e, c = wcol + 16 * ct + n;
+            if (j < p.d_k && c < cols)
+              to[(long)j * a.d_v + col + c] = st[ct][i][x][e];
+          }
+  }
+}
+
+// Start states of the segments of every sequence that has more than one:
+// slot 0 becomes S_init, slot i + 1 (which holds segment i's own state)
+// decay_i * start_i + own_i.  One thread per state entry, the own states of
+// eight segments in flight at a time.
+__global__ __launch_bounds__(256) void segment_scan_kernel(ChunkArgs p,
+                                                           SegTable tab) {
+  const DecayArgs& a = p.a;
+  const long size = (long)p.d_k * a.d_v;
+  const long per_head = (size + 255) / 256;
+  const long blk = blockIdx.x;
+  const long at = blk % per_head * 256 + threadIdx.x;
+  const int h = (int)(blk / per_head % a.h_v);
+  const int s = (int)(blk / per_head / a.h_v);
+  const int first = tab.first[s], n_seg = tab.first[s + 1] - first;
+  if (n_seg < 2 || at >= size) return;
+  float* slot = p.slots + ((long)first * a.h_v + h) * size + at;
+  const float* dec = p.decay + (long)first * a.h_v + h;
+  const long step = a.h_v * size;
+  float S = 0.f;
+  if (a.s_in) {
+    S = a.s_in[((long)s * a.h_v + h) * size + at];
+    slot[0] = S;
+  }
+  constexpr int kAhead = 8;
+  for (int i = 0; i < n_seg - 1; i += kAhead) {
+    float own[kAhead], d[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (i + u < n_seg - 1) {
+        own[u] = slot[(i + u + 1) * step];
+        d[u] = dec[(long)(i + u) * a.h_v];
+      }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (i + u < n_seg - 1) {
+        S = __builtin_fmaf(d[u], S, own[u]);
+        slot[(i + u + 1) * step] = S;
+      }
+  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -284,18 +830,78 @@ static long step_blocks(long states, int d_v) {
   return (units + 3) / 4;
 }
 
-// Prefix sums of the sequence lengths; the number of tokens, or -1.
-static long seq_starts(int32_t n_seqs, const int32_t* seq_len, SeqTable& t) {
+// Sequences and segments of a prefill call.  Segments are as long as it
+// takes for about two workgroups per CU (one launch then fills the GPU at the
+// kernel's occupancy), and at least kMinSeg tokens: a segment costs its state
+// twice written and twice read and its keys and values read once more.
+constexpr int kTargetBlocks = 512;
+constexpr int kMinSeg = 8 * kChunk;
+
+static int block_cols(int d_v) { return d_v <= 64 ? 64 : 128; }
+
+// The number of tokens, or -1 for bad lengths.
+static long plan_segments(int32_t n_seqs, const int32_t* seq_len, int h_v,
+                          int d_v, SegTable& t) {
   if (n_seqs < 1 || n_seqs > GDN_MAX_LANES || !seq_len) return -1;
   memset(&t, 0, sizeof(t));
-  long sum = 0;
+  t.n = n_seqs;
+  long tokens = 0, chunks = 0;
   for (int i = 0; i < n_seqs; ++i) {
     if (seq_len[i] < 0) return -1;
-    sum += seq_len[i];
-    if (sum > INT_MAX) return -1;
-    t.start[i + 1] = (int)sum;
+    tokens += seq_len[i];
+    if (tokens > INT_MAX) return -1;
+    chunks += (seq_len[i] + (long)kChunk - 1) / kChunk;
+    t.start[i + 1] = (int)tokens;
   }
-  return sum;
+  const int w = block_cols(d_v);
+  const long work = chunks * h_v * ((d_v + w - 1) / w);
+  long seg = (work + kTargetBlocks - 1) / kTargetBlocks * kChunk;
+  if (seg < kMinSeg) seg = kMinSeg;
+  if (seg > (1 << 30)) seg = 1 << 30;
+  t.seg = (int)seg;
+  for (int i = 0; i < n_seqs; ++i) {
+    const long n = (seq_len[i] + seg - 1) / seg;
+    t.first[i + 1] = t.first[i] + (int)(n < 1 ? 1 : n);
+  }
+  return tokens;
+}
+
+// Workspace: a slot per segment and head, then the segments' decays.  Slots
+// of sequences of one segment stay unused.
+static size_t slots_bytes(const SegTable& t, int h_v, int d_k, int d_v) {
+  return (size_t)t.first[t.n] * h_v * d_k * d_v * sizeof(float);
+}
+static size_t workspace_bytes(const SegTable& t, int h_v, int d_k, int d_v) {
+  if (t.first[t.n] == t.n) return 0;
+  return (slots_bytes(t, h_v, d_k, d_v) + 255) / 256 * 256 +
+         (size_t)t.first[t.n] * h_v * sizeof(float);
+}
+
+template <int MODE, typename... Args>
+static hipError_t launch_chunks(int d_k, int d_v, int in_dtype, bool vec,
+                                long items, hipStream_t st, Args&&... args) {
+  const int w = block_cols(d_v);
+  const dim3 grid((unsigned)(items * ((d_v + w - 1) / w)));
+  auto go = [&](auto dk, auto cw, auto t, auto v) {
+    return launch(chunk_kernel<decltype(dk)::value, decltype(cw)::value,
+                               decltype(t), MODE, decltype(v)::value>,
+                  grid, dim3(256), st, args...);
+  };
+  auto of_vec = [&](auto dk, auto cw, auto t) {
+    if (vec) return go(dk, cw, t, std::true_type{});
+    return go(dk, cw, t, std::false_type{});
+  };
+  auto of_type = [&](auto dk, auto cw) {
+    if (in_dtype == GDN_BF16) return of_vec(dk, cw, uint16_t{});
+    return of_vec(dk, cw, float{});
+  };
+  auto of_cols = [&](auto dk) {
+    if (w == 64) return of_type(dk, std::integral_constant<int, 16>{});
+    return of_type(dk, std::integral_constant<int, 32>{});
+  };
+  if (d_k <= 32) return of_cols(std::integral_constant<int, 32>{});
+  if (d_k == 64) return of_cols(std::integral_constant<int, 64>{});
+  return of_cols(std::integral_constant<int, 128>{});
 }
 
 }  // namespace gdnd
@@ -351,12 +957,12 @@ extern "C" size_t gdn_decay_prefill_workspace_bytes(int32_t n_seqs,
                                                     int32_t h_v, int32_t h_k,
                                                     int32_t d_k, int32_t d_v) {
   using namespace gdnd;
-  SeqTable t;
+  SegTable t;
   if (check_heads("gdn_decay_prefill_workspace_bytes", h_v, h_k, d_k, d_v) !=
           GDN_OK ||
-      seq_starts(n_seqs, seq_len, t) < 0)
+      plan_segments(n_seqs, seq_len, h_v, d_v, t) < 0)
     return 0;
-  return 0;
+  return workspace_bytes(t, h_v, d_k, d_v);
 }
 
 extern "C" int gdn_decay_prefill(int32_t n_seqs, const int32_t* seq_len,
@@ -370,8 +976,8 @@ extern "C" int gdn_decay_prefill(int32_t n_seqs, const int32_t* seq_len,
   const char* fn = "gdn_decay_prefill";
   int rc = check_heads(fn, h_v, h_k, d_k, d_v);
   if (rc != GDN_OK) return rc;
-  SeqTable seq;
-  const long tokens = seq_starts(n_seqs, seq_len, seq);
+  SegTable tab;
+  const long tokens = plan_segments(n_seqs, seq_len, h_v, d_v, tab);
   if (tokens < 0)
     return fail(GDN_EINVAL, "gdn_decay_prefill: bad n_seqs or seq_len");
   if (flags & ~GDN_FLAG_HEAD_DECAY)
@@ -379,28 +985,42 @@ extern "C" int gdn_decay_prefill(int32_t n_seqs, const int32_t* seq_len,
   if (!o && !S_final)
     return fail(GDN_EINVAL,
                 "gdn_decay_prefill: neither states nor outputs are wanted");
-  DecayArgs p = {q, k, v, g, S_init, S_final, o, scale, 1, n_seqs, h_v, h_k,
-                 d_v, 0, (flags & GDN_FLAG_HEAD_DECAY) ? 1 : 0};
-  rc = check_pointers(fn, p, in_dtype);
+  ChunkArgs p = {{q, k, v, g, S_init, S_final, o, scale, 1, n_seqs, h_v, h_k,
+                  d_v, 0, (flags & GDN_FLAG_HEAD_DECAY) ? 1 : 0},
+                 d_k, nullptr, nullptr};
+  rc = check_pointers(fn, p.a, in_dtype);
   if (rc != GDN_OK) return rc;
-  const size_t need =
-      gdn_decay_prefill_workspace_bytes(n_seqs, seq_len, h_v, h_k, d_k, d_v);
+  const size_t need = workspace_bytes(tab, h_v, d_k, d_v);
   if (need > 0 && (!workspace || ws_bytes < need))
     return fail(GDN_EWORKSPACE, "gdn_decay_prefill: workspace too small");
   if (need > 0 && misaligned(workspace, 16))
     return fail(GDN_EINVAL,
                 "gdn_decay_prefill: pointers must be 16-byte aligned");
   if (tokens == 0 && !S_final) return GDN_OK;
-  const double units = (double)n_seqs * h_v * ((d_v + kStepCols - 1) / kStepCols);
-  if (units > (double)INT_MAX)
+  const int w = block_cols(d_v), segs = tab.first[n_seqs];
+  const double scan = ((double)d_k * d_v + 255) / 256;
+  if ((double)segs * h_v * ((d_v + w - 1) / w) > (double)INT_MAX ||
+      (double)n_seqs * h_v * scan > (double)INT_MAX)
     return fail(GDN_EINVAL, "gdn_decay_prefill: grid too large");
-  const long blocks = step_blocks((long)n_seqs * h_v, d_v);
-  const hipError_t e =
-      by_shape(d_k, d_v, in_dtype, [&](auto dk, auto t, auto v4) {
-        return launch(prompt_chain_kernel<decltype(dk)::value, decltype(t),
-                                          decltype(v4)::value>,
-                      dim3((unsigned)blocks), dim3(256), (hipStream_t)stream,
-                      p, seq);
-      });
+  hipStream_t st = (hipStream_t)stream;
+  const bool vec = d_v % (in_dtype == GDN_BF16 ? 8 : 4) == 0;
+  hipError_t e = hipSuccess;
+  if (segs > n_seqs) {
+    p.slots = (float*)workspace;
+    p.decay = (float*)((char*)workspace +
+                       (slots_bytes(tab, h_v, d_k, d_v) + 255) / 256 * 256);
+    e = launch_chunks<kLocal>(d_k, d_v, in_dtype, vec,
+                              (long)(segs - n_seqs) * h_v, st, p, tab, 0);
+    if (e == hipSuccess)
+      e = launch(segment_scan_kernel,
+                 dim3((unsigned)((((long)d_k * d_v + 255) / 256) * h_v *
+                                 n_seqs)),
+                 dim3(256), st, p, tab);
+  }
+  // without outputs only the last segments are left to run
+  if (e == hipSuccess)
+    e = launch_chunks<kOutput>(d_k, d_v, in_dtype, vec,
+                               (long)(o ? segs : n_seqs) * h_v, st, p, tab,
+                               o ? 0 : 1);
   return gdn::hip_status(e, "gdn_decay_prefill launch");
 }
