@@ -207,9 +207,10 @@ __global__ __launch_bounds__(256) void step_kernel(DecayArgs p,
 //   o_t = scale (exp(b_t) S0^T q_t + sum_{s <= t} exp(b_t - b_s)(q_t.k_s) v_s)
 //   S   = exp(B) S0 + sum_s k_s (exp(B - b_s) v_s)^T
 // Four products per chunk: Q K^T, Q S0, P V and K^T W, all on the matrix
-// cores.  bf16 operands enter exactly; f32 ones (S0, P, W) as two bf16 parts,
-// hi + lo, off by at most 2^-18 of each entry: one part alone would put the
-// f32 outputs and states 2^-9 off.  f32 inputs use the f32 matrix cores.
+// cores.  bf16 operands enter exactly, f32 ones (S0, P, W) as three bf16
+// parts whose sum is the f32 value itself (8 of its 24 bits each), so the
+// products are those of f32.  (Two rounded parts left states and outputs
+// 2.5e-6 off, against 1e-7.)  f32 inputs use the f32 matrix cores.
 //
 // The transposed forms are computed (O^T = S0^T Q^T + V^T P^T with
 // P^T = mask(K Q^T)), because then every intermediate is born in the layout
@@ -224,10 +225,9 @@ __global__ __launch_bounds__(256) void step_kernel(DecayArgs p,
 //     two halves).
 //   * a token's decays belong to one lane (column n) of O^T.
 // A workgroup of four waves takes 4 CW columns of d_v of one head; every
-// wave holds its CW columns of the state in registers and never exchanges
-// anything but the staged rows.  (Each wave forms all of K Q^T itself: 40 of
-// its 192 matrix instructions per chunk, against a barrier and an LDS round
-// trip of P in two parts.)
+// wave holds its CW columns of the state in registers.  P is formed once per
+// workgroup, its tiles shared out over the waves, and handed on through LDS
+// as finished operands while the waves multiply the state.
 //
 // Long sequences are cut into segments so that a launch fills the GPU: a
 // first pass forms each segment's own state (from zero) and decay, a scan
@@ -248,8 +248,9 @@ struct Op;
 template <>
 struct Op<uint16_t> {
   typedef u32x4 Raw;
+  static constexpr int kParts = 3;
   struct Wide {
-    u32x4 hi, lo;
+    u32x4 part[kParts];
   };
   static __device__ __forceinline__ f32x4 mul(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -257,25 +258,30 @@ struct Op<uint16_t> {
         0);
   }
   static __device__ __forceinline__ f32x4 mul(const Wide& a, u32x4 b, f32x4 c) {
-    return mul(a.hi, b, mul(a.lo, b, c));
+#pragma unroll
+    for (int i = kParts - 1; i >= 0; --i) c = mul(a.part[i], b, c);
+    return c;
   }
   static __device__ __forceinline__ f32x4 mul(u32x4 a, const Wide& b, f32x4 c) {
-    return mul(a, b.hi, mul(a, b.lo, c));
+#pragma unroll
+    for (int i = kParts - 1; i >= 0; --i) c = mul(a, b.part[i], c);
+    return c;
   }
-  // x = hi + lo, each rounded to nearest even.
+  // x as the sum of its upper 8 bits, the next 8 and the last 8: the high
+  // halves of x, of x minus the first part, and of what is left then.
   static __device__ __forceinline__ Wide wide(f32x4 x, f32x4 y) {
     Wide w;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const f32x2 v = i < 2 ? f32x2{x[2 * i], x[2 * i + 1]}
-                            : f32x2{y[2 * i - 4], y[2 * i - 3]};
-      const uint32_t h =
-          __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
-      const f32x2 r = {v[0] - __uint_as_float(h << 16),
-                       v[1] - __uint_as_float(h & 0xffff0000u)};
-      w.hi[i] = h;
-      w.lo[i] =
-          __builtin_bit_cast(uint32_t, __builtin_convertvector(r, bf16x2));
+      float a = i < 2 ? x[2 * i] : y[2 * i - 4];
+      float b = i < 2 ? x[2 * i + 1] : y[2 * i - 3];
+#pragma unroll
+      for (int part = 0; part < kParts; ++part) {
+        const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+        w.part[part][i] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+        a -= __uint_as_float(ua & 0xffff0000u);
+        b -= __uint_as_float(ub & 0xffff0000u);
+      }
     }
     return w;
   }
@@ -295,12 +301,12 @@ struct Op<uint16_t> {
   static __device__ __forceinline__ u32x4 row(const uint16_t* p) {
     return *reinterpret_cast<const u32x4*>(p);
   }
-  // Column reads.  Lane l of 16 l' + i receives rows r .. r + 3 (first half
-  // of the slots) and r + 16 .. r + 19 (second) with r = 4 (l / 16), at the
-  // column given by `col(i)`, i = l % 16.  The transposing LDS read hands
-  // lane i entry i % 4 of the 8 bytes addressed by lane 4 e + i / 4 of its
-  // 16 as its entry e: the lane addresses row r + (i / 4), entries
-  // col0 + step * (i % 4) .. + 3.
+  // Column reads.  Lane 16 g + i receives rows 4 g .. 4 g + 3 (first half of
+  // the slots) and 16 + 4 g .. 16 + 4 g + 3 (second) of column
+  // col0 + step * (i / 4) + i % 4.  The transposing LDS read hands lane i of
+  // 16 entry i % 4 of the 8 bytes addressed by lane 4 e + i / 4 of them as
+  // its entry e, so lane i addresses row 4 g + i / 4, entries
+  // col0 + step * (i % 4) and the three after it.
   static __device__ __forceinline__ u32x4 column(const uint16_t* tile,
                                                  int pitch, int col0,
                                                  int step, int lane) {
@@ -318,30 +324,32 @@ struct Op<uint16_t> {
 
 template <>
 struct Op<float> {
+  static constexpr int kParts = 2;  // slots 0..3 and 4..7
   struct Raw {
-    f32x4 x, y;
+    u32x4 part[kParts];
+    __device__ __forceinline__ float at(int e) const {
+      return __uint_as_float(part[e / 4][e % 4]);
+    }
   };
   typedef Raw Wide;
   static __device__ __forceinline__ f32x4 mul(const Raw& a, const Raw& b,
                                               f32x4 c) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x[e], b.x[e], c, 0, 0, 0);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.y[e], b.y[e], c, 0, 0, 0);
+    for (int e = 0; e < 8; ++e)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.at(e), b.at(e), c, 0, 0, 0);
     return c;
   }
   static __device__ __forceinline__ Raw wide(f32x4 x, f32x4 y) {
-    return {x, y};
+    return {__builtin_bit_cast(u32x4, x), __builtin_bit_cast(u32x4, y)};
   }
   static __device__ __forceinline__ Raw scaled(const Raw& a, f32x4 s0,
                                                f32x4 s1) {
-    return {a.x * s0, a.y * s1};
+    return wide(__builtin_bit_cast(f32x4, a.part[0]) * s0,
+                __builtin_bit_cast(f32x4, a.part[1]) * s1);
   }
   static __device__ __forceinline__ Raw row(const float* p) {
-    return {reinterpret_cast<const f32x4*>(p)[0],
-            reinterpret_cast<const f32x4*>(p)[1]};
+    return {reinterpret_cast<const u32x4*>(p)[0],
+            reinterpret_cast<const u32x4*>(p)[1]};
   }
   static __device__ __forceinline__ Raw column(const float* tile, int pitch,
                                                int col0, int step, int lane) {
@@ -351,8 +359,8 @@ struct Op<float> {
     Raw r;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      r.x[e] = p[e * pitch];
-      r.y[e] = p[(16 + e) * pitch];
+      r.part[0][e] = __float_as_uint(p[e * pitch]);
+      r.part[1][e] = __float_as_uint(p[(16 + e) * pitch]);
     }
     return r;
   }
@@ -432,48 +440,66 @@ __device__ __forceinline__ double set_gates(Gates& G, float g, int lane) {
 }
 
 // 64 token rows of W entries of a tensor in transit from memory to LDS: each
-// thread holds pieces of 16 bytes.
-template <typename TIn, int W>
+// thread holds pieces of 16 bytes, kRows rows apart at one column.  The loads
+// go through a buffer resource that ends with the last valid row, so that
+// rows past it read as zero without a branch; columns past the row's n
+// entries are sent out of range too.  VEC: rows are 16-byte aligned and n is
+// a multiple of the piece; else entry by entry.
+constexpr int kBufWord3 = 0x00020000;  // raw buffer resource
+constexpr int kOutOfRange = 0x7fffffff;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p,
+                                                            int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes,
+                                           kBufWord3);
+}
+
+template <typename TIn, int W, bool VEC>
 struct Transit {
   static constexpr int kPer = 16 / sizeof(TIn);  // entries per piece
-  static constexpr int kPieces = kChunk * W / kPer / 256;
+  static constexpr int kRows = 256 * kPer / W;
+  static constexpr int kPieces = kChunk / kRows;
   static constexpr int kPitch = W + kPer;
   u32x4 r[kPieces];
-  // Rows base[t * stride], entries 0 .. n - 1; rows from `rows` on and
-  // entries past n read as zero.  VEC: rows are 16-byte aligned and n is a
-  // multiple of kPer.
-  template <bool VEC>
-  __device__ __forceinline__ void load(const TIn* __restrict__ base,
-                                       long stride, int rows, int n) {
+  int first, step, n;  // byte offset of the thread's first piece, row step
+
+  __device__ __forceinline__ void init(long stride, int n_) {
+    const int t = threadIdx.x / (W / kPer), c = threadIdx.x % (W / kPer) * kPer;
+    n = n_;
+    step = (int)(kRows * stride * (long)sizeof(TIn));
+    first = c < n ? (int)((t * stride + c) * (long)sizeof(TIn)) : kOutOfRange;
+  }
+  // base: the chunk's first row; rows: its valid ones.
+  __device__ __forceinline__ void load(const TIn* base, long stride, int rows) {
+    const auto rs = buffer_of(
+        base, (int)(((rows < kChunk ? rows : kChunk) - 1) * stride + n) *
+                  (int)sizeof(TIn));
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int p = threadIdx.x + 256 * i;
-      const int t = p / (W / kPer), c = p % (W / kPer) * kPer;
-      r[i] = u32x4{0, 0, 0, 0};
-      if (t < rows) {
-        const TIn* src = base + t * stride + c;
-        if constexpr (VEC) {
-          if (c < n) r[i] = *reinterpret_cast<const u32x4*>(src);
-        } else {
+      const int off = first == kOutOfRange ? first : first + i * step;
+      if constexpr (VEC) {
+        r[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
+      } else {
+        const int c = threadIdx.x % (W / kPer) * kPer;
+        r[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
-          for (int e = 0; e < kPer; ++e)
-            if (c + e < n) {
-              if constexpr (sizeof(TIn) == 4)
-                r[i][e] = __float_as_uint((float)src[e]);
-              else
-                r[i][e / 2] |= (uint32_t)src[e] << (16 * (e & 1));
-            }
+        for (int e = 0; e < kPer; ++e) {
+          const int at = c + e < n ? off + e * (int)sizeof(TIn) : kOutOfRange;
+          if constexpr (sizeof(TIn) == 4)
+            r[i][e] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0);
+          else
+            r[i][e / 2] |= (uint32_t)(uint16_t)
+                               __builtin_amdgcn_raw_buffer_load_b16(rs, at, 0, 0)
+                           << (16 * (e & 1));
         }
       }
     }
   }
   __device__ __forceinline__ void store(TIn* tile) const {
+    const int t = threadIdx.x / (W / kPer), c = threadIdx.x % (W / kPer) * kPer;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int p = threadIdx.x + 256 * i;
-      const int t = p / (W / kPer), c = p % (W / kPer) * kPer;
-      *reinterpret_cast<u32x4*>(tile + t * kPitch + c) = r[i];
-    }
+    for (int i = 0; i < kPieces; ++i)
+      *reinterpret_cast<u32x4*>(tile + (t + i * kRows) * kPitch + c) = r[i];
   }
 };
 
@@ -481,18 +507,28 @@ struct Transit {
 // outputs and final states from the segments' start states (kOutput).
 enum { kLocal = 0, kOutput = 1 };
 
+// P^T in operand form: fragment (j, x) holds the token columns 16 j .. and
+// the token rows 32 x .. 32 x + 31 (x <= j / 2), in this order; wave w makes
+// the fragments kOwn[w] .. kOwn[w + 1] - 1.
+constexpr int kFrags = 6;
+constexpr int kFragJ[kFrags] = {0, 1, 2, 2, 3, 3};
+constexpr int kFragX[kFrags] = {0, 0, 0, 1, 0, 1};
+constexpr int kOwn[5] = {0, 2, 4, 5, 6};
+constexpr int frag_of(int j, int x) { return j < 2 ? j : 2 * j - 2 + x; }
+
 template <int DK, int CW, typename TIn, int MODE, bool VEC>
-__global__ __launch_bounds__(256, 2) void chunk_kernel(ChunkArgs p,
-                                                       SegTable tab,
-                                                       int last_only) {
+__global__ __launch_bounds__(256, sizeof(TIn) == 2 ? 2 : 1)
+void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
   typedef Op<TIn> O;
   typedef typename O::Raw Raw;
+  typedef typename O::Wide Wide;
   constexpr int KS = DK / 32, CT = CW / 16, W = 4 * CW;
-  typedef Transit<TIn, DK> KT;
-  typedef Transit<TIn, W> VT;
+  typedef Transit<TIn, DK, true> KT;
+  typedef Transit<TIn, W, VEC> VT;
   __shared__ __attribute__((aligned(16))) TIn Ks[kChunk * KT::kPitch];
   __shared__ __attribute__((aligned(16))) TIn Qs[MODE == kOutput ? kChunk * KT::kPitch : 8];
   __shared__ __attribute__((aligned(16))) TIn Vs[kChunk * VT::kPitch];
+  __shared__ u32x4 Ps[MODE == kOutput ? kFrags : 1][O::kParts][64];
   __shared__ __attribute__((aligned(16))) Gates G;
 
   const DecayArgs& a = p.a;
@@ -527,18 +563,18 @@ __global__ __launch_bounds__(256, 2) void chunk_kernel(ChunkArgs p,
   const int T = rest < tab.seg ? (int)rest : tab.seg;
   const bool last = nth == n_seg - 1;
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = gdn::uniform(tid >> 6);
   const int n = lane & 15, g4 = lane >> 4;
   const int hk = h / (a.h_v / a.h_k);
   const int col = cb * W, wcol = wave * CW;  // of d_v; of the block
   const int cols = a.d_v - col < W ? a.d_v - col : W;
   const long ks = (long)a.h_k * p.d_k, vs = (long)a.h_v * a.d_v;
-  const TIn* __restrict__ K = (const TIn*)a.k + tok0 * ks + (long)hk * p.d_k;
-  const TIn* __restrict__ Q = (const TIn*)a.q + tok0 * ks + (long)hk * p.d_k;
-  const TIn* __restrict__ V = (const TIn*)a.v + tok0 * vs + (long)h * a.d_v + col;
+  const TIn* K = (const TIn*)a.k + tok0 * ks + (long)hk * p.d_k;
+  const TIn* Q = (const TIn*)a.q + tok0 * ks + (long)hk * p.d_k;
+  const TIn* V = (const TIn*)a.v + tok0 * vs + (long)h * a.d_v + col;
   const float* __restrict__ g = a.per_head ? a.g + h : a.g + tok0 * a.h_v + h;
   const long gs = a.per_head ? 0 : a.h_v;
-  float* __restrict__ out =
+  float* out =
       MODE == kOutput && a.o ? a.o + tok0 * vs + (long)h * a.d_v + col : nullptr;
 
   // state entry (32 ks + 8 g4 + 4 a + e, column 16 ct + n): st[ct][ks][a][e]
@@ -566,15 +602,18 @@ __global__ __launch_bounds__(256, 2) void chunk_kernel(ChunkArgs p,
 
   KT kt, qt;
   VT vt;
+  kt.init(ks, p.d_k);
+  qt.init(ks, p.d_k);
+  vt.init(vs, cols);
   float gate = 0.f;
   double total = 0.0;
   auto fetch = [&](int t0) {
     const int rows = T - t0;
-    kt.template load<true>(K + t0 * ks, ks, rows, p.d_k);
+    kt.load(K + t0 * ks, ks, rows);
     if constexpr (MODE == kOutput) {
-      if (out) qt.template load<true>(Q + t0 * ks, ks, rows, p.d_k);
+      if (out) qt.load(Q + t0 * ks, ks, rows);
     }
-    vt.template load<VEC>(V + t0 * vs, vs, rows, cols);
+    vt.load(V + t0 * vs, vs, rows);
     gate = lane < rows ? g[(t0 + lane) * gs] : 0.f;
   };
   auto place = [&]() {
@@ -594,6 +633,72 @@ __global__ __launch_bounds__(256, 2) void chunk_kernel(ChunkArgs p,
     __syncthreads();
     const bool more = t0 + kChunk < T;
     if (more) fetch(t0 + kChunk);
+    f32x4 acc[CT][4];
+    if (out) {
+      // this wave's fragments of P^T
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        if (wave != w) continue;
+#pragma unroll
+        for (int f = kOwn[w]; f < kOwn[w + 1]; ++f) {
+          const int j = kFragJ[f], x = kFragX[f], t = 16 * j + n;
+          f32x4 pt[2];
+          pt[0] = pt[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            const Raw qf = O::row(Qs + t * KT::kPitch + 32 * i + 8 * g4);
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              if (2 * x + y <= j)
+                pt[y] = O::mul(O::row(Ks + (32 * x + 16 * y + n) * KT::kPitch +
+                                      32 * i + 8 * g4),
+                               qf, pt[y]);
+          }
+          const float2 bt = G.b[t];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            if (2 * x + y > j) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int sr = 32 * x + 16 * y + 4 * g4 + e;
+              const float2 bs = G.b[sr];
+              const float w2 = __builtin_amdgcn_exp2f((bt.x - bs.x) +
+                                                      (bt.y - bs.y));
+              pt[y][e] = 2 * x + y < j || sr <= t ? pt[y][e] * w2 : 0.f;
+            }
+          }
+          const Wide pw = O::wide(pt[0], pt[1]);
+#pragma unroll
+          for (int i = 0; i < O::kParts; ++i) Ps[f][i][lane] = pw.part[i];
+        }
+      }
+      // O^T of the state: tokens 16 j + n, columns 16 ct + 4 g4 + e
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[ct][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        Wide sw[CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+          sw[ct] = O::wide(st[ct][i][0], st[ct][i][1]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const Raw qf = O::row(Qs + (16 * j + n) * KT::kPitch + 32 * i + 8 * g4);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct)
+            acc[ct][j] = O::mul(sw[ct], qf, acc[ct][j]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float in = G.in[16 * j + n];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) acc[ct][j] *= in;
+      }
+      __syncthreads();  // P^T is complete
+    }
     Raw vf[2][CT];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
@@ -601,81 +706,36 @@ __global__ __launch_bounds__(256, 2) void chunk_kernel(ChunkArgs p,
       for (int ct = 0; ct < CT; ++ct)
         vf[x][ct] = O::column(Vs + 32 * x * VT::kPitch, VT::kPitch,
                               wcol + 16 * ct, 4, lane);
-    if constexpr (MODE == kOutput) {
-      if (out) {
-        // O^T of the state: tokens 16 j + n, columns 16 ct + 4 g4 + e
-        f32x4 acc[CT][4];
+    if (out) {
+      const auto rs = buffer_of(
+          out + t0 * vs,
+          (int)(((T - t0 < kChunk ? T - t0 : kChunk) - 1) * vs + cols) * 4);
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
+      for (int j = 0; j < 4; ++j) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[ct][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int x = 0; x <= j / 2; ++x) {
+          Wide pw;
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          typename O::Wide sw[CT];
+          for (int i = 0; i < O::kParts; ++i)
+            pw.part[i] = Ps[frag_of(j, x)][i][lane];
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct)
-            sw[ct] = O::wide(st[ct][i][0], st[ct][i][1]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const Raw qf =
-                O::row(Qs + (16 * j + n) * KT::kPitch + 32 * i + 8 * g4);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-              acc[ct][j] = O::mul(sw[ct], qf, acc[ct][j]);
-          }
+            acc[ct][j] = O::mul(vf[x][ct], pw, acc[ct][j]);
         }
+        // rows past the last one fall behind the resource's end
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = 16 * j + n;
-          const float in = G.in[t];
-          const float2 bt = G.b[t];
+        for (int ct = 0; ct < CT; ++ct) {
+          const int c = wcol + 16 * ct + 4 * g4;
+          const int off = (int)((16 * j + n) * vs + c) * 4;
+          const u32x4 y = __builtin_bit_cast(u32x4, acc[ct][j] * a.scale);
+          if constexpr (VEC) {
+            __builtin_amdgcn_raw_buffer_store_b128(
+                y, rs, c < cols ? off : kOutOfRange, 0, 0);
+          } else {
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct) acc[ct][j] *= in;
-          // P^T of the tokens s of blocks 0 .. j
-          f32x4 pt[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) pt[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int x = 0; x < KS; ++x) {
-            const Raw qf =
-                O::row(Qs + (16 * j + n) * KT::kPitch + 32 * x + 8 * g4);
-#pragma unroll
-            for (int i = 0; i <= j; ++i)
-              pt[i] = O::mul(
-                  O::row(Ks + (16 * i + n) * KT::kPitch + 32 * x + 8 * g4), qf,
-                  pt[i]);
-          }
-#pragma unroll
-          for (int i = 0; i <= j; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int sr = 16 * i + 4 * g4 + e;
-              const float2 bs = G.b[sr];
-              const float w = __builtin_amdgcn_exp2f((bt.x - bs.x) +
-                                                     (bt.y - bs.y));
-              pt[i][e] = sr <= t ? pt[i][e] * w : 0.f;
-            }
-#pragma unroll
-          for (int x = 0; x <= j / 2; ++x) {
-            const typename O::Wide pw = O::wide(pt[2 * x], pt[2 * x + 1]);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-              acc[ct][j] = O::mul(vf[x][ct], pw, acc[ct][j]);
-          }
-          if (t0 + t < T) {
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-              const int c = wcol + 16 * ct + 4 * g4;
-              float* dst = out + (t0 + t) * vs + c;
-              const f32x4 y = acc[ct][j] * a.scale;
-              if constexpr (VEC) {
-                if (c < cols) *reinterpret_cast<f32x4*>(dst) = y;
-              } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (c + e < cols) dst[e] = y[e];
-              }
-            }
+            for (int e = 0; e < 4; ++e)
+              __builtin_amdgcn_raw_buffer_store_b32(
+                  y[e], rs, c + e < cols ? off + 4 * e : kOutOfRange, 0, 0);
           }
         }
       }
@@ -693,7 +753,7 @@ __global__ __launch_bounds__(256, 2) void chunk_kernel(ChunkArgs p,
       const f32x4 w0 = *reinterpret_cast<const f32x4*>(&G.out[32 * x + 4 * g4]);
       const f32x4 w1 =
           *reinterpret_cast<const f32x4*>(&G.out[32 * x + 16 + 4 * g4]);
-      typename O::Wide ww[CT];
+      Wide ww[CT];
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) ww[ct] = O::scaled(vf[x][ct], w0, w1);
 #pragma unroll
@@ -779,8 +839,10 @@ __global__ __launch_bounds__(256) void segment_scan_kernel(ChunkArgs p,
 // ---------------------------------------------------------------- host side
 static int check_heads(const char* fn, int h_v, int h_k, int d_k, int d_v) {
   char msg[128];
+  // (64 token rows of a tensor are addressed with 31 bits)
   if (h_v < 1 || h_k < 1 || h_v % h_k != 0 || d_k < 1 || d_v < 1 ||
-      d_v > 1024) {
+      d_v > 1024 || (double)h_v * d_v * 4 * 64 > (double)INT_MAX / 2 ||
+      (double)h_k * d_k * 4 * 64 > (double)INT_MAX / 2) {
     snprintf(msg, sizeof(msg), "%s: sizes out of range", fn);
     return fail(GDN_EINVAL, msg);
   }
