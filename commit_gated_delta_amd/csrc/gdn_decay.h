@@ -240,6 +240,31 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+// Staged rows in LDS.  bf16: W entries a row, its 16-byte pieces permuted by
+// an XOR with the row such that both ways of reading them are free of bank
+// conflicts: a piece of eight neighbouring rows (fragments along the row),
+// and 64 bytes of four neighbouring rows (transposed fragments).  A row of
+// fewer than 16 pieces shares its 256 bytes with the next ones.  Permuted
+// row numbers repeat every 16 rows, so a lane computes its offsets once.
+// f32: rows one piece apart from a multiple of the banks.
+template <typename TIn, int W>
+struct Tile {
+  static constexpr int kPer = 16 / sizeof(TIn);  // entries per piece
+  static constexpr int kPieces = W / kPer;
+  static constexpr bool kSwizzled = sizeof(TIn) == 2;
+  static constexpr int kPitch = kSwizzled ? W : W + kPer;
+  static constexpr int kSize = kChunk * kPitch;
+  // Entry offset of piece p of row r.
+  static __device__ __forceinline__ int at(int r, int p) {
+    if constexpr (kSwizzled) {
+      if constexpr (kPieces == 16) p ^= (r & 3) << 2 | (r >> 2 & 3);
+      else if constexpr (kPieces == 8) p ^= (r >> 1 & 1) << 2 | (r >> 2 & 3);
+      else p ^= r >> 2 & 3;
+    }
+    return r * kPitch + p * kPer;
+  }
+};
+
 // Operand fragments of eight k-slots.  Raw: inputs as they are; Wide: f32
 // values.
 template <typename TIn>
@@ -297,22 +322,26 @@ struct Op<uint16_t> {
     }
     return wide(x, y);
   }
-  // Eight consecutive entries of a staged row.
-  static __device__ __forceinline__ u32x4 row(const uint16_t* p) {
-    return *reinterpret_cast<const u32x4*>(p);
+  // Entries 8 p .. 8 p + 7 of row r0 + r (r0 a multiple of 16).
+  template <typename TL>
+  static __device__ __forceinline__ u32x4 row(const uint16_t* tile, int r0,
+                                              int r, int p) {
+    return *reinterpret_cast<const u32x4*>(tile + TL::at(r, p) +
+                                           r0 * TL::kPitch);
   }
   // Column reads.  Lane 16 g + i receives rows 4 g .. 4 g + 3 (first half of
-  // the slots) and 16 + 4 g .. 16 + 4 g + 3 (second) of column
-  // col0 + step * (i / 4) + i % 4.  The transposing LDS read hands lane i of
-  // 16 entry i % 4 of the 8 bytes addressed by lane 4 e + i / 4 of them as
-  // its entry e, so lane i addresses row 4 g + i / 4, entries
-  // col0 + step * (i % 4) and the three after it.
-  static __device__ __forceinline__ u32x4 column(const uint16_t* tile,
-                                                 int pitch, int col0,
-                                                 int step, int lane) {
-    const uint16_t* p = tile + (4 * (lane >> 4) + ((lane & 15) >> 2)) * pitch +
-                        col0 + step * (lane & 3);
-    const uint2 a = tr(p), b = tr(p + 16 * pitch);
+  // the slots) and 16 + 4 g .. 16 + 4 g + 3 (second), counted from row r0 (a
+  // multiple of 32), of column col0 + step * (i / 4) + i % 4.  The
+  // transposing LDS read hands lane i of 16 entry i % 4 of the 8 bytes
+  // addressed by lane 4 e + i / 4 of them as its entry e, so lane i addresses
+  // row 4 g + i / 4, entries col0 + step * (i % 4) and the three after it.
+  template <typename TL>
+  static __device__ __forceinline__ u32x4 column(const uint16_t* tile, int r0,
+                                                 int col0, int step, int lane) {
+    const int r = 4 * (lane >> 4) + ((lane & 15) >> 2);
+    const int c = col0 + step * (lane & 3);
+    const uint16_t* p = tile + TL::at(r, c >> 3) + (c & 7) + r0 * TL::kPitch;
+    const uint2 a = tr(p), b = tr(p + 16 * TL::kPitch);
     return u32x4{a.x, a.y, b.x, b.y};
   }
   static __device__ __forceinline__ uint2 tr(const uint16_t* p) {
@@ -347,20 +376,24 @@ struct Op<float> {
     return wide(__builtin_bit_cast(f32x4, a.part[0]) * s0,
                 __builtin_bit_cast(f32x4, a.part[1]) * s1);
   }
-  static __device__ __forceinline__ Raw row(const float* p) {
-    return {reinterpret_cast<const u32x4*>(p)[0],
-            reinterpret_cast<const u32x4*>(p)[1]};
+  template <typename TL>
+  static __device__ __forceinline__ Raw row(const float* tile, int r0, int r,
+                                            int p) {
+    const u32x4* at = reinterpret_cast<const u32x4*>(
+        tile + (r0 + r) * TL::kPitch + 8 * p);
+    return {at[0], at[1]};
   }
-  static __device__ __forceinline__ Raw column(const float* tile, int pitch,
+  template <typename TL>
+  static __device__ __forceinline__ Raw column(const float* tile, int r0,
                                                int col0, int step, int lane) {
     const int i = lane & 15;
-    const float* p =
-        tile + 4 * (lane >> 4) * pitch + col0 + step * (i >> 2) + (i & 3);
+    const float* p = tile + (r0 + 4 * (lane >> 4)) * TL::kPitch + col0 +
+                     step * (i >> 2) + (i & 3);
     Raw r;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      r.part[0][e] = __float_as_uint(p[e * pitch]);
-      r.part[1][e] = __float_as_uint(p[(16 + e) * pitch]);
+      r.part[0][e] = __float_as_uint(p[e * TL::kPitch]);
+      r.part[1][e] = __float_as_uint(p[(16 + e) * TL::kPitch]);
     }
     return r;
   }
@@ -446,7 +479,7 @@ __device__ __forceinline__ double set_gates(Gates& G, float g, int lane) {
 // entries are sent out of range too.  VEC: rows are 16-byte aligned and n is
 // a multiple of the piece; else entry by entry.
 constexpr int kBufWord3 = 0x00020000;  // raw buffer resource
-constexpr int kOutOfRange = 0x7fffffff;
+constexpr int kOutOfRange = 1 << 30;  // (64 rows are at most as long)
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p,
                                                             int bytes) {
@@ -456,10 +489,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p,
 
 template <typename TIn, int W, bool VEC>
 struct Transit {
-  static constexpr int kPer = 16 / sizeof(TIn);  // entries per piece
+  typedef gdnd::Tile<TIn, W> Tile;
+  static constexpr int kPer = Tile::kPer;
   static constexpr int kRows = 256 * kPer / W;
   static constexpr int kPieces = kChunk / kRows;
-  static constexpr int kPitch = W + kPer;
+  static_assert(!Tile::kSwizzled || kRows % 16 == 0,
+                "the permutation repeats every 16 rows");
   u32x4 r[kPieces];
   int first, step, n;  // byte offset of the thread's first piece, row step
 
@@ -469,37 +504,41 @@ struct Transit {
     step = (int)(kRows * stride * (long)sizeof(TIn));
     first = c < n ? (int)((t * stride + c) * (long)sizeof(TIn)) : kOutOfRange;
   }
-  // base: the chunk's first row; rows: its valid ones.
+  // base: the chunk's first row; rows: its valid ones.  A resource per piece,
+  // so that the pieces share one offset register.
   __device__ __forceinline__ void load(const TIn* base, long stride, int rows) {
-    const auto rs = buffer_of(
-        base, (int)(((rows < kChunk ? rows : kChunk) - 1) * stride + n) *
-                  (int)sizeof(TIn));
+    int bytes = (int)(((rows < kChunk ? rows : kChunk) - 1) * stride + n) *
+                (int)sizeof(TIn);
+    const char* at = (const char*)base;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int off = first == kOutOfRange ? first : first + i * step;
+      const auto rs = buffer_of(at, bytes > 0 ? bytes : 0);
+      at += step;
+      bytes -= step;
       if constexpr (VEC) {
-        r[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
+        r[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, first, 0, 0);
       } else {
         const int c = threadIdx.x % (W / kPer) * kPer;
         r[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-          const int at = c + e < n ? off + e * (int)sizeof(TIn) : kOutOfRange;
+          const int off = c + e < n ? first + e * (int)sizeof(TIn) : kOutOfRange;
           if constexpr (sizeof(TIn) == 4)
-            r[i][e] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0);
+            r[i][e] = __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0);
           else
             r[i][e / 2] |= (uint32_t)(uint16_t)
-                               __builtin_amdgcn_raw_buffer_load_b16(rs, at, 0, 0)
+                               __builtin_amdgcn_raw_buffer_load_b16(rs, off, 0, 0)
                            << (16 * (e & 1));
         }
       }
     }
   }
   __device__ __forceinline__ void store(TIn* tile) const {
-    const int t = threadIdx.x / (W / kPer), c = threadIdx.x % (W / kPer) * kPer;
+    const int t = threadIdx.x / (W / kPer), p = threadIdx.x % (W / kPer);
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
-      *reinterpret_cast<u32x4*>(tile + (t + i * kRows) * kPitch + c) = r[i];
+      *reinterpret_cast<u32x4*>(tile + Tile::at(t, p) +
+                                i * kRows * Tile::kPitch) = r[i];
   }
 };
 
@@ -525,9 +564,11 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
   constexpr int KS = DK / 32, CT = CW / 16, W = 4 * CW;
   typedef Transit<TIn, DK, true> KT;
   typedef Transit<TIn, W, VEC> VT;
-  __shared__ __attribute__((aligned(16))) TIn Ks[kChunk * KT::kPitch];
-  __shared__ __attribute__((aligned(16))) TIn Qs[MODE == kOutput ? kChunk * KT::kPitch : 8];
-  __shared__ __attribute__((aligned(16))) TIn Vs[kChunk * VT::kPitch];
+  typedef typename KT::Tile KL;
+  typedef typename VT::Tile VL;
+  __shared__ __attribute__((aligned(16))) TIn Ks[KL::kSize];
+  __shared__ __attribute__((aligned(16))) TIn Qs[MODE == kOutput ? KL::kSize : 8];
+  __shared__ __attribute__((aligned(16))) TIn Vs[VL::kSize];
   __shared__ u32x4 Ps[MODE == kOutput ? kFrags : 1][O::kParts][64];
   __shared__ __attribute__((aligned(16))) Gates G;
 
@@ -586,19 +627,27 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
     else if (n_seg == 1 && a.s_in)
       from = a.s_in + ((long)s * a.h_v + h) * p.d_k * a.d_v;
   }
+  // (rows past d_k lie behind the resource's end)
+  const int state_bytes = (int)((long)p.d_k * a.d_v - col) * 4;
+  const auto state_at = [&](int l, int ct, int i, int x, int e) {
+    const int c = wcol + 16 * ct + (l & 15);
+    return c < cols ? ((32 * i + 8 * (l >> 4) + 4 * x + e) * a.d_v + c) * 4
+                    : kOutOfRange;
+  };
+  {
+    const auto rs = buffer_of(from ? from + col : nullptr, from ? state_bytes : 0);
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct)
+    for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-    for (int i = 0; i < KS; ++i)
+      for (int i = 0; i < KS; ++i)
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = 32 * i + 8 * g4 + 4 * x + e, c = wcol + 16 * ct + n;
-          st[ct][i][x][e] = from && j < p.d_k && c < cols
-                                ? from[(long)j * a.d_v + col + c]
-                                : 0.f;
-        }
+          for (int e = 0; e < 4; ++e)
+            st[ct][i][x][e] =
+                __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                    rs, state_at(lane, ct, i, x, e), 0, 0));
+  }
 
   KT kt, qt;
   VT vt;
@@ -646,13 +695,13 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
           pt[0] = pt[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int i = 0; i < KS; ++i) {
-            const Raw qf = O::row(Qs + t * KT::kPitch + 32 * i + 8 * g4);
+            const Raw qf = O::template row<KL>(Qs, 16 * j, n, 4 * i + g4);
 #pragma unroll
             for (int y = 0; y < 2; ++y)
               if (2 * x + y <= j)
-                pt[y] = O::mul(O::row(Ks + (32 * x + 16 * y + n) * KT::kPitch +
-                                      32 * i + 8 * g4),
-                               qf, pt[y]);
+                pt[y] = O::mul(
+                    O::template row<KL>(Ks, 32 * x + 16 * y, n, 4 * i + g4),
+                    qf, pt[y]);
           }
           const float2 bt = G.b[t];
 #pragma unroll
@@ -685,7 +734,7 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
           sw[ct] = O::wide(st[ct][i][0], st[ct][i][1]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const Raw qf = O::row(Qs + (16 * j + n) * KT::kPitch + 32 * i + 8 * g4);
+          const Raw qf = O::template row<KL>(Qs, 16 * j, n, 4 * i + g4);
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct)
             acc[ct][j] = O::mul(sw[ct], qf, acc[ct][j]);
@@ -704,12 +753,11 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
-        vf[x][ct] = O::column(Vs + 32 * x * VT::kPitch, VT::kPitch,
-                              wcol + 16 * ct, 4, lane);
+        vf[x][ct] =
+            O::template column<VL>(Vs, 32 * x, wcol + 16 * ct, 4, lane);
     if (out) {
-      const auto rs = buffer_of(
-          out + t0 * vs,
-          (int)(((T - t0 < kChunk ? T - t0 : kChunk) - 1) * vs + cols) * 4);
+      int bytes =
+          (int)(((T - t0 < kChunk ? T - t0 : kChunk) - 1) * vs + cols) * 4;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -723,10 +771,12 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
             acc[ct][j] = O::mul(vf[x][ct], pw, acc[ct][j]);
         }
         // rows past the last one fall behind the resource's end
+        const auto rs = buffer_of(out + (t0 + 16 * j) * vs, bytes > 0 ? bytes : 0);
+        bytes -= (int)(16 * vs * 4);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           const int c = wcol + 16 * ct + 4 * g4;
-          const int off = (int)((16 * j + n) * vs + c) * 4;
+          const int off = (int)(n * vs + c) * 4;
           const u32x4 y = __builtin_bit_cast(u32x4, acc[ct][j] * a.scale);
           if constexpr (VEC) {
             __builtin_amdgcn_raw_buffer_store_b128(
@@ -760,8 +810,8 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
       for (int i = 0; i < KS; ++i)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const Raw kf = O::column(Ks + 32 * x * KT::kPitch, KT::kPitch,
-                                   32 * i + 4 * y, 8, lane);
+          const Raw kf =
+              O::template column<KL>(Ks, 32 * x, 32 * i + 4 * y, 8, lane);
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct)
             st[ct][i][y] = O::mul(kf, ww[ct], st[ct][i][y]);
@@ -780,6 +830,11 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
     to = a.s_out + ((long)s * a.h_v + h) * p.d_k * a.d_v;
   }
   if (to) {
+    // the offsets are computed anew: kept from the load at the kernel's start
+    // they would cost 64 registers through the whole loop
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    const auto rs = buffer_of(to + col, state_bytes);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
@@ -787,11 +842,10 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = 32 * i + 8 * g4 + 4 * x + e, c = wcol + 16 * ct + n;
-            if (j < p.d_k && c < cols)
-              to[(long)j * a.d_v + col + c] = st[ct][i][x][e];
-          }
+          for (int e = 0; e < 4; ++e)
+            __builtin_amdgcn_raw_buffer_store_b32(
+                __float_as_uint(st[ct][i][x][e]), rs,
+                state_at(l, ct, i, x, e), 0, 0);
   }
 }
 
