@@ -7,6 +7,7 @@
 #include <cmath>
 
 #include "gdn.h"
+#include "gdn_mfma_op.h"
 #include "gdn_window_common.h"
 
 namespace gdnk {
@@ -15,13 +16,18 @@ using gdn::fail;
 using gdn::launch;
 using gdn::misaligned;
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+using gdn::op::f32x4;
+using gdn::op::Op;
+using gdn::op::Tile;
+using gdn::op::u32x4;
 
 struct KvArgs {
   const void *k, *v;  // the caches
   const int* table;
   const int* kv_len;
   int lanes, t_max, h_q, h_kv, page, n_pages, max_pages;
+  uint32_t page_mul;  // pos / page = (umulhi(pos, page_mul) + pos) >> page_shift
+  int page_shift;
 };
 
 // Positions that lane n's cache holds.
@@ -32,72 +38,469 @@ __device__ __forceinline__ int lane_len(const KvArgs& a, int n) {
 
 // First element of position pos's row of key-value head h, or -1 when its
 // page is outside the cache.
+__device__ __forceinline__ int page_of(const KvArgs& a, int pos) {
+  return (int)((__umulhi((uint32_t)pos, a.page_mul) + (uint32_t)pos) >>
+               a.page_shift);
+}
+__device__ __forceinline__ long row_in(const KvArgs& a, int page, int h,
+                                       int row, int d) {
+  if ((unsigned)page >= (unsigned)a.n_pages) return -1;
+  return (((long)page * a.h_kv + h) * a.page + row) * d;
+}
 __device__ __forceinline__ long row_of(const KvArgs& a, int n, int h, int pos,
                                        int d) {
-  const int page = a.table[(long)n * a.max_pages + pos / a.page];
-  if ((unsigned)page >= (unsigned)a.n_pages) return -1;
-  return (((long)page * a.h_kv + h) * a.page + pos % a.page) * d;
+  const int nth = page_of(a, pos);
+  return row_in(a, a.table[(long)n * a.max_pages + nth], h, pos - nth * a.page,
+                d);
 }
 
-__device__ __forceinline__ float elem(const uint16_t* p, long i) {
-  return __uint_as_float((uint32_t)p[i] << 16);
-}
-__device__ __forceinline__ float elem(const float* p, long i) { return p[i]; }
+// --------------------------------------------------------- splitting the work
+// A lane's positions are taken in units of kUnit, and the units of all lanes
+// are shared out in splits of equally many, about `target` of them, whatever
+// the lengths (which only the device knows).  Splits are numbered lane by
+// lane; the grid holds the most there can be, target + lanes, and those past
+// the last one end at once.  Partial results of lanes with more than one
+// split have a slot each, at most 2 * target of them.
+constexpr int kUnit = 128;
 
-// One wave per (lane, token, query head): 64 positions at a time, a lane per
-// position for the scores, a lane per D/64 columns for the values.
-template <int D, typename T>
-__global__ __launch_bounds__(64) void attend_kernel(KvArgs a,
-                                                    gdn::LaneTable tl,
-                                                    const T* __restrict__ q,
-                                                    float* __restrict__ o,
-                                                    float scale) {
-  __shared__ float qs[D];
-  __shared__ float ps[64];
-  __shared__ long rows[64];
-  const int lane = threadIdx.x;
-  const int h = blockIdx.x % a.h_q, nt = blockIdx.x / a.h_q;
-  const int n = nt / a.t_max, t = nt % a.t_max;
-  const int T_n = tl.v[n];
-  if (t >= T_n) return;
-  const long qo = (long)blockIdx.x * D;
-  const int hk = h / (a.h_q / a.h_kv);
-  for (int i = lane; i < D; i += 64) qs[i] = elem(q, qo + i);
-  __syncthreads();
-  const int end = lane_len(a, n) - T_n + t + 1;
-  float m = -INFINITY, l = 0.f, acc[D / 64] = {};
-  for (int p0 = 0; p0 < end; p0 += 64) {
-    const int pos = p0 + lane;
-    const long row = pos < end ? row_of(a, n, hk, pos, D) : -1;
-    float s = -INFINITY;
-    if (row >= 0) {
-      s = 0.f;
-      for (int i = 0; i < D; ++i)
-        s = __builtin_fmaf(qs[i], elem((const T*)a.k, row + i), s);
-      s *= scale;
+struct Split {
+  int lane;    // -1: no such split
+  int len;     // positions of the lane
+  int nth, n;  // this split among the lane's
+  int units;   // units per split
+  int slot;    // slot of the lane's first split
+};
+
+__device__ __forceinline__ int wave_scan_int(int x) {  // inclusive
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
+  return x;
+}
+
+// The split `item`, or with of_lane the first split of lane `item`.  Every
+// wave works it out for itself, 64 lanes at a time.
+__device__ __forceinline__ Split find_split(const KvArgs& a,
+                                            const gdn::LaneTable& tl, int item,
+                                            int target, bool of_lane) {
+  const int l = threadIdx.x & 63;
+  int len[GDN_MAX_LANES / 64], u[GDN_MAX_LANES / 64], all = 0;
+#pragma unroll
+  for (int c = 0; c < GDN_MAX_LANES / 64; ++c) {
+    const int n = 64 * c + l;
+    const bool on = n < a.lanes && tl.v[n < a.lanes ? n : 0] > 0;
+    len[c] = on ? lane_len(a, n) : 0;
+    u[c] = (len[c] + kUnit - 1) / kUnit;
+    if (on && u[c] == 0) u[c] = 1;  // its outputs are zeros
+    all += u[c];
+  }
+  all = __builtin_amdgcn_readlane(wave_scan_int(all), 63);
+  Split s;
+  s.units = (all + target - 1) / target;
+  if (s.units < 1) s.units = 1;
+  s.lane = -1;
+  int before = 0, slots = 0;
+#pragma unroll
+  for (int c = 0; c < GDN_MAX_LANES / 64; ++c) {
+    if (64 * c >= a.lanes || s.lane >= 0) continue;
+    const int n = (u[c] + s.units - 1) / s.units, several = n > 1 ? n : 0;
+    const int upto = wave_scan_int(n) + before;
+    const int slots_upto = wave_scan_int(several) + slots;
+    const bool mine = of_lane ? 64 * c + l == item : upto > item;
+    const uint64_t hit = __ballot(mine);
+    if (hit) {
+      const int w = __builtin_ctzll(hit);
+      s.lane = 64 * c + w;
+      s.len = __builtin_amdgcn_readlane(len[c], w);
+      s.n = __builtin_amdgcn_readlane(n, w);
+      s.nth = of_lane ? 0 : item - (__builtin_amdgcn_readlane(upto, w) - s.n);
+      s.slot = __builtin_amdgcn_readlane(slots_upto - several, w);
     }
-    float tile = s;
-    for (int x = 1; x < 64; x *= 2) tile = fmaxf(tile, __shfl_xor(tile, x));
-    const float m2 = fmaxf(m, tile);
-    const float keep = m == -INFINITY ? 0.f : expf(m - m2);
-    const float e = row >= 0 ? expf(s - m2) : 0.f;
-    l = l * keep + gdn::wave_sum(e);
-    m = m2;
-    __syncthreads();
-    ps[lane] = e;
-    rows[lane] = row;
-    __syncthreads();
-    for (int c = 0; c < D / 64; ++c) acc[c] *= keep;
-    for (int j = 0; j < 64; ++j) {
-      if (rows[j] < 0) continue;
-      for (int c = 0; c < D / 64; ++c)
-        acc[c] = __builtin_fmaf(ps[j],
-                                elem((const T*)a.v, rows[j] + 64 * c + lane),
-                                acc[c]);
+    before = __builtin_amdgcn_readlane(upto, 63);
+    slots = __builtin_amdgcn_readlane(slots_upto, 63);
+  }
+  return s;
+}
+
+// ------------------------------------------------------------------ attention
+struct AttendArgs {
+  KvArgs kv;
+  const void* q;
+  float* o;
+  float* part_o;  // [slots][h_kv][rows][d]
+  float* part_ml; // [slots][h_kv][rows][2]: maximum, sum
+  float scale;    // of the scores, times log2 e
+  int target, rows, groups;  // rows = t_max * h_q / h_kv; row groups of them
+};
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// The rows of a key-value head (token t and query head h' of its group are
+// row t * group + h') are taken 16 RT WR at a time by a workgroup of four
+// waves: WR waves side by side in the rows, 4 / WR sharing out the split's
+// positions, 32 at a step.  Per step a wave forms S^T = K Q^T (rows
+// positions, columns rows of q), whose result layout is at once the B operand
+// of O^T = V^T P^T; V passes through LDS for the transposed read.  In O^T and
+// S^T a row of q is one lane column, so the running maximum m and sum l of
+// the softmax and the rescaling of O are per lane.  m is raised only when a
+// score is more than 2^8 above it, which keeps the exchange between lanes
+// out of nearly every step and costs f32 no precision; l stays apart per
+// lane group until the end.  P enters as three exact bf16 parts (see
+// gdn_mfma_op.h).  The next step's K rows are loaded when this step's scores
+// are done and its V rows when V is in LDS, page numbers a step earlier.
+template <int D, typename T, int RT, int WR>
+__global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs p,
+                                                        gdn::LaneTable tl) {
+  typedef Op<T> O;
+  typedef typename O::Raw Raw;
+  typedef typename O::Wide Wide;
+  typedef Tile<T, D> TL;
+  constexpr int KS = D / 32, CT = D / 16, WP = 4 / WR, kRows = 16 * RT * WR;
+  constexpr int kPieces = sizeof(Raw) / 16;  // 16-byte loads per fragment
+  constexpr float kSlack = 8.f;
+  constexpr int kTileBytes = 32 * TL::kPitch * (int)sizeof(T);
+  constexpr int kMergeBytes = WP > 1 ? WR * 16 * RT * D * 4 : 0;
+  constexpr int kPool = 4 * kTileBytes > kMergeBytes ? 4 * kTileBytes : kMergeBytes;
+  __shared__ __attribute__((aligned(16))) T Qs[kRows * TL::kPitch];
+  __shared__ __attribute__((aligned(16))) char pool[kPool];
+  __shared__ float ml[4][2][16 * RT];
+  const KvArgs& a = p.kv;
+  const int per_item = a.h_kv * p.groups;
+  const Split s = find_split(a, tl, blockIdx.x / per_item, p.target, false);
+  if (s.lane < 0) return;
+  const int hk = blockIdx.x % per_item / p.groups;
+  const int row0 = blockIdx.x % p.groups * kRows;
+  const int group = a.h_q / a.h_kv, T_n = tl.v[s.lane];
+  const int rows = T_n * group;
+  if (row0 >= rows) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = gdn::uniform(tid >> 6);
+  const int n = lane & 15, g4 = lane >> 4;
+  const int wr = wave % WR, wp = wave / WR;
+
+  // q rows of the workgroup (zeros past the last)
+  {
+    constexpr int kPer = TL::kPer;
+    for (int i = tid; i < kRows * TL::kPieces; i += 256) {
+      const int r = i / TL::kPieces, c = i % TL::kPieces;
+      u32x4 x = {0, 0, 0, 0};
+      if (row0 + r < rows) {
+        const int t = (row0 + r) / group, h = hk * group + (row0 + r) % group;
+        x = *reinterpret_cast<const u32x4*>(
+            (const T*)p.q +
+            (((long)s.lane * a.t_max + t) * a.h_q + h) * D + c * kPer);
+      }
+      *reinterpret_cast<u32x4*>(Qs + TL::at(r, c)) = x;
     }
   }
-  for (int c = 0; c < D / 64; ++c)
-    o[qo + 64 * c + lane] = l > 0.f ? acc[c] / l : 0.f;
+  __syncthreads();
+
+  const int begin = s.nth * s.units * kUnit;
+  const int stop = begin + s.units * kUnit < s.len ? begin + s.units * kUnit : s.len;
+  const int steps = (stop - begin + 31) / 32;
+  // first position that some row of the window does not see
+  const int open = s.len - T_n + 1;
+  int end[RT];  // positions that the lane's row sees
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int row = row0 + (wr * RT + r) * 16 + n;
+    end[r] = row < rows ? s.len - T_n + row / group + 1 : 0;
+  }
+  T* Vs = reinterpret_cast<T*>(pool + wave * kTileBytes);
+  const T* kc = (const T*)a.k + 8 * g4;
+  const T* vc = (const T*)a.v + 8 * g4;
+  const int* table = a.table + (long)s.lane * a.max_pages;
+
+  f32x4 acc[RT][CT];
+  float m[RT], l[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+#pragma unroll
+    for (int c = 0; c < CT; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // position of half h of a step's rows in this lane
+  auto pos_of = [&](int step, int h) { return begin + 32 * step + 16 * h + n; };
+  int page[2];    // page numbers of the step after the next
+  bool there[2];  // whether the rows of the step in hand are
+  long at[2];     // and where
+  auto look_up = [&](int step) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int pos = pos_of(step, h);
+      page[h] = pos < stop ? table[page_of(a, pos)] : -1;
+    }
+  };
+  auto place = [&](int step) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int pos = pos_of(step, h);
+      const long row = row_in(a, page[h], hk, pos - page_of(a, pos) * a.page, D);
+      there[h] = row >= 0;
+      at[h] = there[h] ? row : 0;  // (any row of the cache will do)
+    }
+  };
+  u32x4 kr[2][KS][kPieces], vr[2][KS][kPieces];
+  auto fetch = [&](const T* c, u32x4 (&r)[2][KS][kPieces]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int x = 0; x < kPieces; ++x)
+          r[h][i][x] =
+              *reinterpret_cast<const u32x4*>(c + at[h] + 32 * i + 4 * x);
+  };
+
+  if (wp < steps) {
+    look_up(wp);
+    place(wp);
+    fetch(kc, kr);
+    fetch(vc, vr);
+    look_up(wp + WP);
+  }
+  for (int step = wp; step < steps; step += WP) {
+    const bool here[2] = {there[0], there[1]};
+    // scores
+    f32x4 sc[RT][2];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) sc[r][0] = sc[r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const Raw qf = O::template row<TL>(Qs, 16 * (wr * RT + r), n, 4 * i + g4);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          Raw kf;
+          __builtin_memcpy(&kf, kr[h][i], sizeof(Raw));
+          sc[r][h] = O::mul(kf, qf, sc[r][h]);
+        }
+      }
+    const int next = step + WP;
+    if (next < steps) {
+      place(next);
+      fetch(kc, kr);
+      look_up(next + WP);
+    }
+    // softmax
+    const int p0 = begin + 32 * step;
+    const bool whole =
+        p0 + 32 <= (open < stop ? open : stop) && __all(here[0] && here[1]);
+    uint64_t ok = 0;  // bit of position i of the step: its row is there
+    if (!whole)
+      ok = (__ballot(here[0]) & 0xffffull) | (__ballot(here[1]) & 0xffffull) << 16;
+    bool raise = false;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = sc[r][h][e] * p.scale;
+          if (!whole) {
+            const int i = 16 * h + 4 * g4 + e;
+            if (!(ok >> i & 1) || p0 + i >= end[r]) x = -INFINITY;
+          }
+          sc[r][h][e] = x;
+          raise |= x > m[r] + kSlack;
+        }
+    if (__any(raise)) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        float top = m[r];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[r][h][e]);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float keep =
+            m[r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[r] - top);
+        m[r] = top;
+        l[r] *= keep;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[r][c] *= keep;
+      }
+    }
+    Wide pw[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const float ref = m[r] == -INFINITY ? 0.f : m[r];
+      f32x4 e2[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          e2[h][e] = __builtin_amdgcn_exp2f(sc[r][h][e] - ref);
+          l[r] += e2[h][e];
+        }
+      pw[r] = O::wide(e2[0], e2[1]);
+    }
+    // V through LDS.  Rows that are not there count as zeros.
+    if (!whole) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (!here[h])
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int x = 0; x < kPieces; ++x) vr[h][i][x] = u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int x = 0; x < kPieces; ++x)
+          *reinterpret_cast<u32x4*>(
+              Vs + TL::at(n, kPieces * (4 * i + g4) + x) + 16 * h * TL::kPitch) =
+              vr[h][i][x];
+    if (next < steps) fetch(vc, vr);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      const Raw vf = O::template column<TL>(Vs, 0, 16 * c, 4, lane);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[r][c] = O::mul(vf, pw[r], acc[r][c]);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    l[r] += __shfl_xor(l[r], 16);
+    l[r] += __shfl_xor(l[r], 32);
+  }
+  // the waves that shared out the positions
+  float* sum = reinterpret_cast<float*>(pool) + wr * 16 * RT * D;
+  if constexpr (WP > 1) {
+    if (g4 == 0)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        ml[wave][0][16 * r + n] = m[r];
+        ml[wave][1][16 * r + n] = l[r];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      float top = -INFINITY, tot = 0.f;
+#pragma unroll
+      for (int w = 0; w < WP; ++w)
+        top = fmaxf(top, ml[w * WR + wr][0][16 * r + n]);
+#pragma unroll
+      for (int w = 0; w < WP; ++w) {
+        const float mw = ml[w * WR + wr][0][16 * r + n];
+        tot += mw == -INFINITY ? 0.f
+                               : ml[w * WR + wr][1][16 * r + n] *
+                                     __builtin_amdgcn_exp2f(mw - top);
+      }
+      const float keep =
+          m[r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[r] - top);
+      m[r] = top;
+      l[r] = tot;
+#pragma unroll
+      for (int c = 0; c < CT; ++c) acc[r][c] *= keep;
+    }
+    for (int w = WP - 1; w >= 0; --w) {
+      if (wp == w) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            f32x4* x = reinterpret_cast<f32x4*>(
+                sum + (16 * r + n) * D + 16 * c + 4 * g4);
+            if (w == WP - 1) *x = acc[r][c];
+            else if (w > 0) *x += acc[r][c];
+            else acc[r][c] += *x;
+          }
+      }
+      __syncthreads();
+    }
+    if (wp > 0) return;
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int row = row0 + (wr * RT + r) * 16 + n;
+    if (row >= rows) continue;
+    float* dst;
+    if (s.n == 1) {
+      const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+#pragma unroll
+      for (int c = 0; c < CT; ++c) acc[r][c] *= inv;
+      dst = p.o + (((long)s.lane * a.t_max + row / group) * a.h_q + hk * group +
+                   row % group) * D;
+    } else {
+      const long at_row = ((long)(s.slot + s.nth) * a.h_kv + hk) * p.rows + row;
+      if (g4 == 0) {
+        p.part_ml[2 * at_row] = m[r];
+        p.part_ml[2 * at_row + 1] = l[r];
+      }
+      dst = p.part_o + at_row * D;
+    }
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+      *reinterpret_cast<f32x4*>(dst + 16 * c + 4 * g4) = acc[r][c];
+  }
+}
+
+// Joins the splits of a lane: a wave per row of q, D / 64 columns per lane.
+template <int D>
+__global__ __launch_bounds__(256) void join_kernel(AttendArgs p,
+                                                   gdn::LaneTable tl) {
+  const KvArgs& a = p.kv;
+  const int per_lane = a.h_kv * p.rows;
+  const long item = (long)blockIdx.x * 4 + threadIdx.x / 64;
+  const int n = gdn::uniform((int)(item / per_lane));
+  if (n >= a.lanes) return;
+  const int hk = gdn::uniform((int)(item % per_lane) / p.rows);
+  const int row = gdn::uniform((int)(item % p.rows));
+  const int group = a.h_q / a.h_kv;
+  if (row >= tl.v[n] * group) return;
+  const Split s = find_split(a, tl, n, p.target, true);
+  if (s.n < 2) return;
+  const int lane = threadIdx.x & 63;
+  const long first = ((long)s.slot * a.h_kv + hk) * p.rows + row;
+  const long step = (long)a.h_kv * p.rows;
+  float m = -INFINITY;
+  for (int i = lane; i < s.n; i += 64) m = fmaxf(m, p.part_ml[2 * (first + i * step)]);
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
+  float l = 0.f, acc[D / 64] = {};
+  constexpr int kAhead = 4;
+  for (int i = 0; i < s.n; i += kAhead) {
+    float ms[kAhead], ls[kAhead], o[kAhead][D / 64];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const long at = first + (i + u < s.n ? i + u : i) * step;
+      ms[u] = p.part_ml[2 * at];
+      ls[u] = p.part_ml[2 * at + 1];
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) o[u][c] = p.part_o[at * D + 64 * c + lane];
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (i + u >= s.n || ms[u] == -INFINITY) continue;
+      const float w = __builtin_amdgcn_exp2f(ms[u] - m);
+      l = __builtin_fmaf(w, ls[u], l);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        acc[c] = __builtin_fmaf(w, o[u][c], acc[c]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  float* dst = p.o + (((long)n * a.t_max + row / group) * a.h_q + hk * group +
+                      row % group) * D;
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) dst[64 * c + lane] = acc[c] * inv;
 }
 
 // One 16-byte piece of a key and of a value row per thread.
@@ -135,6 +538,7 @@ static int check_kv_dims(const char* fn, const gdn_kv_dims* p) {
       d.d < 1 || d.page_size < 1 || d.n_pages < 1 || d.max_pages < 1 ||
       (double)d.max_pages * d.page_size >= (double)(1 << 30) ||
       (double)d.n_lanes * d.t_max * d.h_q * 32 > (double)INT_MAX ||
+      (double)d.n_lanes * d.h_q * 1024 > (double)INT_MAX ||
       (double)d.n_pages * d.page_size * d.h_kv > 9.0e15) {
     snprintf(msg, sizeof(msg), "%s: dims out of range", fn);
     return fail(GDN_EINVAL, msg);
@@ -164,26 +568,83 @@ static int check_lanes(const char* fn, const gdn_kv_dims& d,
 
 static KvArgs kv_args(const gdn_kv_dims& d, const void* k, const void* v,
                       const int32_t* table, const int32_t* kv_len) {
-  return {k,     v,         table,   kv_len,    d.n_lanes, d.t_max,
-          d.h_q, d.h_kv, d.page_size, d.n_pages, d.max_pages};
+  KvArgs a = {k,     v,      table,       kv_len,    d.n_lanes,   d.t_max,
+              d.h_q, d.h_kv, d.page_size, d.n_pages, d.max_pages, 0u, 0};
+  // division by the page size for positions below 2^30 (with 2^s >= page,
+  // multiplier floor(2^32 (2^s - page) / page) + 1)
+  while ((1l << a.page_shift) < d.page_size) ++a.page_shift;
+  a.page_mul = (uint32_t)(((uint64_t)((1l << a.page_shift) - d.page_size) << 32) /
+                              (uint64_t)d.page_size +
+                          1);
+  return a;
+}
+
+// How a call is spread: rows of q per workgroup, row groups, splits.  About
+// kTarget workgroups in all (four per CU, what its registers and LDS hold),
+// few rows leaving more of them to the positions.
+constexpr int kTarget = 1024;
+
+struct Shape {
+  int rows, rt, wr, groups, target, slots;
+};
+// f32 rows of 256 leave LDS for the tiles of one row block only; that means
+// more row groups and at most as many slots, so the bf16 shape's workspace
+// does for both.
+static Shape shape_of(const gdn_kv_dims& d, bool f32) {
+  Shape s;
+  s.rows = d.t_max * (d.h_q / d.h_kv);
+  s.rt = s.rows > 16 && d.d < 256 ? 2 : 1;
+  const int tiles = (s.rows + 16 * s.rt - 1) / (16 * s.rt);
+  s.wr = f32 && d.d == 256 ? 1 : tiles > 2 ? 4 : tiles;
+  s.groups = (tiles + s.wr - 1) / s.wr;
+  s.target = kTarget / (d.h_kv * s.groups);
+  if (s.target < 1) s.target = 1;
+  s.slots = 2 * s.target;
+  return s;
+}
+static size_t attend_bytes(const gdn_kv_dims& d) {
+  const Shape s = shape_of(d, false);
+  const size_t n = (size_t)s.slots * d.h_kv * s.rows;
+  return n * (d.d + 2) * sizeof(float);
+}
+
+template <int D, typename T>
+static hipError_t attend(const gdn_kv_dims& d, const Shape& s,
+                         const AttendArgs& p, const gdn::LaneTable& tl,
+                         hipStream_t st) {
+  const dim3 grid(
+      (unsigned)((long)(s.target + d.n_lanes) * d.h_kv * s.groups));
+  auto go = [&](auto rt, auto wr) {
+    return launch(attend_kernel<D, T, decltype(rt)::value, decltype(wr)::value>,
+                  grid, dim3(256), st, p, tl);
+  };
+  auto of_wr = [&](auto rt) {
+    if (s.wr == 1) return go(rt, std::integral_constant<int, 1>{});
+    if (s.wr == 2) return go(rt, std::integral_constant<int, 2>{});
+    return go(rt, std::integral_constant<int, 4>{});
+  };
+  hipError_t e = hipSuccess;
+  if constexpr (D < 256)
+    e = s.rt == 2 ? of_wr(std::integral_constant<int, 2>{})
+                  : of_wr(std::integral_constant<int, 1>{});
+  else if constexpr (sizeof(T) == 4)
+    e = go(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+  else
+    e = of_wr(std::integral_constant<int, 1>{});
+  // a cache of one unit per lane has nothing to join
+  if (e != hipSuccess || (long)d.max_pages * d.page_size <= kUnit) return e;
+  const long rows = (long)d.n_lanes * d.h_kv * s.rows;
+  return launch(join_kernel<D>, dim3((unsigned)((rows + 3) / 4)), dim3(256), st,
+                p, tl);
 }
 
 template <typename T>
-static hipError_t attend(const gdn_kv_dims& d, const KvArgs& a,
-                         const gdn::LaneTable& tl, const void* q, float* o,
-                         float scale, hipStream_t st) {
-  const dim3 grid((unsigned)((long)d.n_lanes * d.t_max * d.h_q));
-  switch (d.d) {
-    case 64:
-      return launch(attend_kernel<64, T>, grid, dim3(64), st, a, tl,
-                    (const T*)q, o, scale);
-    case 128:
-      return launch(attend_kernel<128, T>, grid, dim3(64), st, a, tl,
-                    (const T*)q, o, scale);
-    default:
-      return launch(attend_kernel<256, T>, grid, dim3(64), st, a, tl,
-                    (const T*)q, o, scale);
-  }
+static hipError_t attend(const gdn_kv_dims& d, const Shape& s,
+                         const AttendArgs& p, const gdn::LaneTable& tl,
+                         hipStream_t st) {
+  if (d.d == 64) return attend<64, T>(d, s, p, tl, st);
+  if (d.d == 128) return attend<128, T>(d, s, p, tl, st);
+  return attend<256, T>(d, s, p, tl, st);
 }
 
 }  // namespace gdnk
@@ -192,7 +653,7 @@ extern "C" size_t gdn_paged_attention_workspace_bytes(const gdn_kv_dims* dims) {
   if (gdnk::check_kv_dims("gdn_paged_attention_workspace_bytes", dims) !=
       GDN_OK)
     return 0;
-  return 0;
+  return gdnk::attend_bytes(*dims);
 }
 
 extern "C" int gdn_paged_attention(const gdn_kv_dims* dims,
@@ -223,11 +684,21 @@ extern "C" int gdn_paged_attention(const gdn_kv_dims* dims,
   rc = check_lanes(fn, *dims, t_lane, tl, any);
   if (rc != GDN_OK) return rc;
   if (!any) return GDN_OK;
-  const KvArgs a = kv_args(*dims, k_cache, v_cache, page_table, kv_len);
+  const Shape s = shape_of(*dims, dtype == GDN_F32);
+  AttendArgs p;
+  p.kv = kv_args(*dims, k_cache, v_cache, page_table, kv_len);
+  p.q = q;
+  p.o = o;
+  p.part_o = (float*)workspace;
+  p.part_ml = p.part_o + (size_t)s.slots * dims->h_kv * s.rows * dims->d;
+  p.scale = scale * kLog2e;
+  p.target = s.target;
+  p.rows = s.rows;
+  p.groups = s.groups;
   const hipError_t e =
       dtype == GDN_BF16
-          ? attend<uint16_t>(*dims, a, tl, q, o, scale, (hipStream_t)stream)
-          : attend<float>(*dims, a, tl, q, o, scale, (hipStream_t)stream);
+          ? attend<uint16_t>(*dims, s, p, tl, (hipStream_t)stream)
+          : attend<float>(*dims, s, p, tl, (hipStream_t)stream);
   return gdn::hip_status(e, "gdn_paged_attention launch");
 }
 
