@@ -10,6 +10,7 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 
 #include "gdn.h"
@@ -22,9 +23,10 @@ using gdn::launch;
 using gdn::misaligned;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // What a slice of a row leaves behind: its largest logit, and Z and W of the
-// slice with that as m (W in units of log 2).
+// slice with that as m (W in units of the logits).
 struct Part {
   float m, z, w;
   int n;  // alternatives listed
@@ -55,7 +57,6 @@ __device__ __forceinline__ float logit_at(const float* p, long i) {
 
 constexpr int kThreads = 256;
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.693147180559945309417f;
 
 // Larger logits have larger keys; -0 and 0 have the same.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -96,13 +97,14 @@ struct RowSums {
   float m, lz, entropy;
   bool bad, empty;
 };
-__device__ __forceinline__ RowSums row_sums(float m, float z, float w) {
+__device__ __forceinline__ RowSums row_sums(float m, float z, float w,
+                                            float it) {
   RowSums r;
   r.bad = !(m < INFINITY) || z != z;
   r.empty = !r.bad && m == -INFINITY;
   r.m = m;
   r.lz = logf(z);
-  r.entropy = r.bad ? NAN : r.empty ? 0.f : r.lz - w * kLn2 / z;
+  r.entropy = r.bad ? NAN : r.empty ? 0.f : r.lz - w * it / z;
   return r;
 }
 __device__ __forceinline__ float log_p(const ScoreArgs& p, const RowSums& r,
@@ -129,28 +131,137 @@ __device__ __forceinline__ void write_top(const ScoreArgs& p, long row,
   p.top_logprobs[row * p.n_top + place] = log_p(p, r, x);
 }
 
-// One workgroup per slice of a row: 16 V bytes a thread, read once into
-// registers; everything else works on those.
-//
-// Alternatives: with n lanes of a wave each holding a logit of at least tau,
-// the wave's n-th largest is at least tau too.  So tau, the n-th largest of a
-// wave's 64 lane maxima (by a binary search over its key bits, counting
-// lanes), rules out nearly every logit; the largest tau of the four waves is
-// used.  What is above tau, and of what equals it the n lowest ids of each
-// wave, goes to a list in LDS (about n entries, rarely more), whose entries
-// then count the ones before them.  Should more be above tau than the list
-// holds (its logits would have to sit in a few lanes), the n largest are
-// taken one by one.
-//
-// What bounds it: the read of the row; the exponentials and comparisons come
-// to about two thirds of its time.
 constexpr int kList = 512;
 constexpr int kStrict = kList - 4 * GDN_MAX_TOP;  // room for those above tau
 
+// The n largest of a slice when more than the list holds is at least tau (or
+// tau is -inf, where entries that stand for no logit look the same).
+template <typename TIn, int V, typename Put>
+__device__ __forceinline__ void pick_tied(
+    const ScoreArgs& p, const float (&val)[V][16 / sizeof(TIn)], uint32_t tau,
+    int first, int skew, int& listed, uint32_t* list_key, int* list_id,
+    Put&& put) {
+  constexpr int E = 16 / sizeof(TIn);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  auto id_of = [&](int c, int e) {
+    return (first + c * kThreads) * E - skew + e;
+  };
+  __syncthreads();
+  if (tid == 0) listed = 0;
+  __syncthreads();
+  int ties = 0;  // of this wave so far
+#pragma unroll
+  for (int c = 0; c < V; ++c) {
+    int equal = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const uint32_t k = key_of(val[c][e]);
+      if (k > tau) {
+        const int slot = atomicAdd(&listed, 1);
+        if (slot < kStrict) {
+          list_key[slot] = k;
+          list_id[slot] = id_of(c, e);
+        }
+      }
+      equal += k == tau && (unsigned)id_of(c, e) < (unsigned)p.vocab;
+    }
+    if (ties < p.n_top && __any(equal > 0)) {
+      // the n lowest ids of the wave's ties, behind the entries above tau
+      int place = ties + wave_prefix(equal);
+      ties = __builtin_amdgcn_readlane(place + equal, 63);
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (key_of(val[c][e]) == tau &&
+            (unsigned)id_of(c, e) < (unsigned)p.vocab) {
+          if (place < p.n_top)
+            list_id[kStrict + wave * GDN_MAX_TOP + place] = id_of(c, e);
+          ++place;
+        }
+    }
+  }
+  for (int i = ties + lane; i < GDN_MAX_TOP; i += 64)
+    list_id[kStrict + wave * GDN_MAX_TOP + i] = -1;
+  if (lane < GDN_MAX_TOP) {
+    list_key[kStrict + wave * GDN_MAX_TOP + lane] = tau;
+    if (lane >= p.n_top) list_id[kStrict + wave * GDN_MAX_TOP + lane] = -1;
+  }
+  __syncthreads();
+  const int strict = listed;
+  if (strict <= kStrict) {
+    // every entry counts those before it: the ones above tau, and if they
+    // are fewer than n the ties
+    const int span = strict < p.n_top ? kList - kStrict : 0;
+    for (int i = tid; i < strict + span; i += kThreads) {
+      const int at_i = i < strict ? i : kStrict + i - strict;
+      const uint32_t key = list_key[at_i];
+      const int id = list_id[at_i];
+      if (id < 0) continue;
+      int place = 0;
+#pragma unroll 4
+      for (int j = 0; j < strict; ++j) {
+        const uint32_t k = list_key[j];
+        place += k > key || (k == key && list_id[j] < id);
+      }
+      if (i >= strict)
+#pragma unroll 4
+        for (int j = kStrict; j < kList; ++j)
+          place += (unsigned)list_id[j] < (unsigned)id;
+      if (place < p.n_top) put(place, key, id);
+    }
+    return;
+  }
+  uint32_t last = 0xffffffffu;
+  int last_id = -1;
+  for (int place = 0; place < p.n_top; ++place) {
+    uint32_t best = 0;
+    int id = INT_MAX;
+#pragma unroll
+    for (int c = 0; c < V; ++c)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t k = key_of(val[c][e]);
+        const int i = id_of(c, e);
+        const bool after = k < last || (k == last && i > last_id);
+        if (after && (unsigned)i < (unsigned)p.vocab &&
+            (k > best || (k == best && i < id))) {
+          best = k;
+          id = i;
+        }
+      }
+    __syncthreads();
+    list_key[tid] = best;
+    list_id[tid] = id;
+    __syncthreads();
+#pragma unroll 4
+    for (int j = 0; j < kThreads; ++j)
+      if (list_key[j] > best || (list_key[j] == best && list_id[j] < id)) {
+        best = list_key[j];
+        id = list_id[j];
+      }
+    last = best;
+    last_id = id;
+    if (tid == 0) put(place, best, id);
+  }
+}
+
+// One workgroup per slice of a row: 16 V bytes a thread, read once into
+// registers; everything else works on those.
+//
+// Alternatives: with n threads each holding a logit of at least tau, the n-th
+// largest of the slice is at least tau too.  So tau, the n-th largest of the
+// 256 thread maxima cut to the upper half of its key (by a binary search over
+// those bits, counting threads; every wave for itself), rules out nearly every
+// logit.  What is at least tau goes to a list in LDS (about n entries, rarely
+// more), whose entries then count the ones before them.  If that is more than
+// the list holds (many equal logits), what is above tau and, of what equals
+// it, the n lowest ids of each wave are listed instead; and if even what is
+// above tau is too much (it would have to sit in a few lanes), the n largest
+// are taken one by one.
 template <typename TIn, int V, bool TOP>
-__global__ __launch_bounds__(kThreads) void slice_kernel(ScoreArgs p) {
+__global__ __launch_bounds__(kThreads, 4) void slice_kernel(ScoreArgs p) {
   constexpr int E = 16 / sizeof(TIn);  // logits per vector
-  __shared__ float wave_m[4], wave_tau[4], sums[2][4];
+  __shared__ __attribute__((aligned(16))) float own_of[kThreads];
+  __shared__ float sums[2][4];
   __shared__ uint32_t list_key[TOP ? kList : 1];
   __shared__ int list_id[TOP ? kList : 1];
   __shared__ int listed;
@@ -185,41 +296,48 @@ __global__ __launch_bounds__(kThreads) void slice_kernel(ScoreArgs p) {
         }
     }
   }
-  auto at = [&](int c, int e) {
-    if constexpr (sizeof(TIn) == 4) return __uint_as_float(raw[c][e]);
-    else
-      return __uint_as_float(e & 1 ? raw[c][e / 2] & 0xffff0000u
-                                   : raw[c][e / 2] << 16);
-  };
+  float val[V][E];
+#pragma unroll
+  for (int c = 0; c < V; ++c)
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if constexpr (sizeof(TIn) == 4) val[c][e] = __uint_as_float(raw[c][e]);
+      else
+        val[c][e] = __uint_as_float(e & 1 ? raw[c][e / 2] & 0xffff0000u
+                                          : raw[c][e / 2] << 16);
   auto id_of = [&](int c, int e) {
     return (first + c * kThreads) * E - skew + e;
   };
 
-  float own = -INFINITY;
+  float top[V], own = -INFINITY;
 #pragma unroll
-  for (int c = 0; c < V; ++c)
+  for (int c = 0; c < V; ++c) {
+    top[c] = val[c][0];
 #pragma unroll
-    for (int e = 0; e < E; ++e) own = fmaxf(own, at(c, e));
-  const float wm = wave_max(own);
-  if (lane == 0) wave_m[wave] = wm;
-  if constexpr (TOP) {
-    const uint32_t key = key_of(own);
-    uint32_t tau = 0;
-#pragma unroll
-    for (int b = 31; b >= (sizeof(TIn) == 2 ? 16 : 0); --b) {
-      const uint32_t t = tau | 1u << b;
-      if (__popcll(__ballot(key >= t)) >= p.n_top) tau = t;
-    }
-    // (the lower key half of a negative bf16 logit is all ones)
-    if (sizeof(TIn) == 2 && !(tau >> 31)) tau |= 0xffffu;
-    if (lane == 0) wave_tau[wave] = __uint_as_float(tau);
-    if (tid == 0) listed = 0;
+    for (int e = 1; e < E; ++e) top[c] = fmaxf(top[c], val[c][e]);
+    own = fmaxf(own, top[c]);
   }
+  own_of[tid] = own;
+  if (TOP && tid == 0) listed = 0;
   __syncthreads();
+  const f32x4 of4 = *reinterpret_cast<const f32x4*>(&own_of[4 * lane]);
   const float m =
-      fmaxf(fmaxf(wave_m[0], wave_m[1]), fmaxf(wave_m[2], wave_m[3]));
+      wave_max(fmaxf(fmaxf(of4[0], of4[1]), fmaxf(of4[2], of4[3])));
+  uint32_t keys[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) keys[i] = key_of(of4[i]);
+  auto search = [&](uint32_t tau, int from, int to) {
+    for (int b = from; b >= to; --b) {
+      const uint32_t t = tau | 1u << b;
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n += __popcll(__ballot(keys[i] >= t));
+      if (n >= p.n_top) tau = t;
+    }
+    return tau;
+  };
 
-  // sums
+  // sums (W in units of the logits)
   {
     const float ref = m == -INFINITY ? 0.f : m, s = p.it * kLog2e;
     float z = 0.f, w = 0.f;
@@ -227,10 +345,12 @@ __global__ __launch_bounds__(kThreads) void slice_kernel(ScoreArgs p) {
     for (int c = 0; c < V; ++c)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float d = (at(c, e) - ref) * s;
-        const float q = __builtin_amdgcn_exp2f(d);
+        // (0 times the d of a -inf has to be 0; a NaN stays one)
+        const float d =
+            __builtin_elementwise_maximum(val[c][e] - ref, -FLT_MAX);
+        const float q = __builtin_amdgcn_exp2f(d * s);
         z += q;
-        w = __builtin_fmaf(q, fmaxf(d, -1e30f), w);  // 0, not NaN, for -inf
+        w = __builtin_fmaf(q, d, w);
       }
     z = gdn::wave_sum(z);
     w = gdn::wave_sum(w);
@@ -240,71 +360,31 @@ __global__ __launch_bounds__(kThreads) void slice_kernel(ScoreArgs p) {
     }
   }
 
+  uint32_t tau = 0;
   if constexpr (TOP) {
-    uint32_t tau = 0;
+    tau = search(0, 31, 16);
+    const float least = __uint_as_float(tau >> 31 ? tau & 0x7fffffffu : ~tau);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t t = __float_as_uint(wave_tau[i]);
-      tau = t > tau ? t : tau;
-    }
-    // keys above tau, and equal to it
-    int ties = 0;  // of this wave so far
-    const bool some = __any(key_of(own) >= tau);
-    if (some) {
+    for (int c = 0; c < V; ++c) {
+      if (top[c] >= least) {
 #pragma unroll
-      for (int c = 0; c < V; ++c) {
-        int equal = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const uint32_t k = key_of(at(c, e));
-          equal += k == tau;
-          const uint64_t hits = __ballot(k > tau);
-          if (hits) {
-            int base = 0;
-            if (lane == __builtin_ctzll(hits))
-              base = atomicAdd(&listed, __popcll(hits));
-            base = __builtin_amdgcn_readlane(base, __builtin_ctzll(hits));
-            const int slot =
-                base + __builtin_amdgcn_mbcnt_hi(
-                           (uint32_t)(hits >> 32),
-                           __builtin_amdgcn_mbcnt_lo((uint32_t)hits, 0));
-            if (k > tau && slot < kStrict) {
-              list_key[slot] = k;
+        for (int e = 0; e < E; ++e)
+          if (val[c][e] >= least) {
+            const int slot = atomicAdd(&listed, 1);
+            if (slot < kList) {
+              list_key[slot] = key_of(val[c][e]);
               list_id[slot] = id_of(c, e);
             }
           }
-        }
-        if (ties < p.n_top && __any(equal > 0)) {
-          // the n lowest ids of the wave's ties, behind the strict entries
-          equal = 0;
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            equal += key_of(at(c, e)) == tau &&
-                     (unsigned)id_of(c, e) < (unsigned)p.vocab;
-          int place = ties + wave_prefix(equal);
-          ties += __builtin_amdgcn_readlane(place - ties + equal, 63);
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (key_of(at(c, e)) == tau &&
-                (unsigned)id_of(c, e) < (unsigned)p.vocab) {
-              if (place < p.n_top)
-                list_id[kStrict + wave * GDN_MAX_TOP + place] = id_of(c, e);
-              ++place;
-            }
-        }
       }
     }
-    if (ties > p.n_top) ties = p.n_top;
-    for (int i = ties + lane; i < GDN_MAX_TOP; i += 64)
-      list_id[kStrict + wave * GDN_MAX_TOP + i] = -1;
-    if (lane < GDN_MAX_TOP) list_key[kStrict + wave * GDN_MAX_TOP + lane] = tau;
   }
   __syncthreads();
   const float z = (sums[0][0] + sums[0][1]) + (sums[0][2] + sums[0][3]);
   const float w = (sums[1][0] + sums[1][1]) + (sums[1][2] + sums[1][3]);
   const bool alone = p.slices == 1;
   const long part = row * p.slices + slice;
-  const RowSums r = row_sums(m, z, w);
+  const RowSums r = row_sums(m, z, w, p.it);
   if (tid == 0) {
     if (alone) write_row<TIn>(p, row, r);
     else p.parts[part] = {m, z, w, 0};
@@ -320,58 +400,22 @@ __global__ __launch_bounds__(kThreads) void slice_kernel(ScoreArgs p) {
         p.ids[part * p.n_top + place] = id;
       }
     };
-    const int strict = listed;
-    if (strict <= kStrict) {
-      // every entry counts those before it: the strict ones, and if they are
-      // fewer than n the ties
-      const int span = strict < p.n_top ? kList - kStrict : 0;
-      for (int i = tid; i < strict + span; i += kThreads) {
-        const int at_i = i < strict ? i : kStrict + i - strict;
-        const uint32_t key = list_key[at_i];
-        const int id = list_id[at_i];
-        if (id < 0) continue;
+    const int entries = listed;
+    if (entries <= kList && tau > key_of(-INFINITY)) {
+      for (int i = tid; i < entries; i += kThreads) {
+        const uint32_t key = list_key[i];
+        const int id = list_id[i];
         int place = 0;
-        for (int j = 0; j < strict; ++j) {
+#pragma unroll 4
+        for (int j = 0; j < entries; ++j) {
           const uint32_t k = list_key[j];
           place += k > key || (k == key && list_id[j] < id);
         }
-        if (i >= strict)
-          for (int j = kStrict; j < kList; ++j)
-            place += (unsigned)list_id[j] < (unsigned)id;
         if (place < p.n_top) put(place, key, id);
       }
     } else {
-      uint32_t last = 0xffffffffu;
-      int last_id = -1;
-      for (int place = 0; place < p.n_top; ++place) {
-        uint32_t best = 0;
-        int id = INT_MAX;
-#pragma unroll
-        for (int c = 0; c < V; ++c)
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const uint32_t k = key_of(at(c, e));
-            const int i = id_of(c, e);
-            const bool after = k < last || (k == last && i > last_id);
-            if (after && (unsigned)i < (unsigned)p.vocab &&
-                (k > best || (k == best && i < id))) {
-              best = k;
-              id = i;
-            }
-          }
-        __syncthreads();
-        list_key[tid] = best;
-        list_id[tid] = id;
-        __syncthreads();
-        for (int j = 0; j < kThreads; ++j)
-          if (list_key[j] > best || (list_key[j] == best && list_id[j] < id)) {
-            best = list_key[j];
-            id = list_id[j];
-          }
-        last = best;
-        last_id = id;
-        if (tid == 0) put(place, best, id);
-      }
+      tau = search(tau, 15, 0);
+      pick_tied<TIn, V>(p, val, tau, first, skew, listed, list_key, list_id, put);
     }
     // a slice of fewer logits than n
     if (!alone && tid == 0) {
@@ -389,6 +433,24 @@ __global__ __launch_bounds__(kThreads) void slice_kernel(ScoreArgs p) {
 // taking the largest head of the slices' lists n times.  A lane keeps the
 // lists of K consecutive slices, so that equal logits are met lowest id
 // first.
+constexpr int kJoinList = 2048;
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_max_key(uint32_t x) {
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL,
+                                                           ROWS, 0xf, false);
+  return o > x ? o : x;
+}
+__device__ __forceinline__ uint32_t wave_max_key(uint32_t x) {
+  x = dpp_max_key<0x111, 0xf>(x);
+  x = dpp_max_key<0x112, 0xf>(x);
+  x = dpp_max_key<0x114, 0xf>(x);
+  x = dpp_max_key<0x118, 0xf>(x);
+  x = dpp_max_key<0x142, 0xa>(x);
+  x = dpp_max_key<0x143, 0xc>(x);
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+
 template <typename TIn>
 __global__ __launch_bounds__(64) void join_kernel(ScoreArgs p) {
   const int lane = threadIdx.x;
@@ -405,42 +467,62 @@ __global__ __launch_bounds__(64) void join_kernel(ScoreArgs p) {
   for (int i = lane; i < p.slices; i += 64) {
     const Part q = parts[i];
     if (q.m == -INFINITY) continue;
-    const float d = (q.m - m) * p.it * kLog2e, f = __builtin_amdgcn_exp2f(d);
+    const float d = q.m - m, f = __builtin_amdgcn_exp2f(d * (p.it * kLog2e));
     z = __builtin_fmaf(f, q.z, z);
-    w = __builtin_fmaf(f, __builtin_fmaf(fmaxf(d, -1e30f), q.z, q.w), w);
+    w = __builtin_fmaf(f, __builtin_fmaf(d, q.z, q.w), w);
   }
   z = gdn::wave_sum(z);
   w = gdn::wave_sum(w);
   if (__any(bad)) z = NAN;
-  const RowSums r = row_sums(m, z, w);
+  const RowSums r = row_sums(m, z, w, p.it);
   if (lane == 0) write_row<TIn>(p, row, r);
   if (p.n_top == 0) return;
 
-  const int K = (p.slices + 63) / 64;
-  const float* values = p.values + row * p.slices * p.n_top;
-  const int* ids = p.ids + row * p.slices * p.n_top;
+  // the lists, in LDS when they fit
+  __shared__ float lds_values[kJoinList];
+  __shared__ int lds_ids[kJoinList];
+  const int K = (p.slices + 63) / 64, all = p.slices * p.n_top;
+  const float* values = p.values + row * all;
+  const int* ids = p.ids + row * all;
+  if (all <= kJoinList) {
+    for (int i = lane; i < all; i += 64) {
+      lds_values[i] = values[i];
+      lds_ids[i] = ids[i];
+    }
+    __syncthreads();
+    values = lds_values;
+    ids = lds_ids;
+  }
   uint32_t last = 0xffffffffu;
   int last_id = -1;
-  // heads of the lane's lists: what comes after (last, last_id) in each
+  // head of the lane's lists: the first of what comes after (last, last_id)
   uint32_t key = 0;  // 0: none left
   float value = 0.f;
-  int id = 0, from = 0, taken = 0;
+  int id = 0, taken = 0;
+  const int mine = K == 1 && lane < p.slices ? parts[lane].n : 0;
   auto head = [&]() {
     key = 0;
+    if (K == 1) {  // one list, taken in order
+      if (taken < mine) {
+        value = values[lane * p.n_top + taken];
+        id = ids[lane * p.n_top + taken];
+        key = key_of(value);
+      }
+      return;
+    }
     for (int k = 0; k < K; ++k) {
       const int s = lane * K + k;
       if (s >= p.slices) break;
       const int n = parts[s].n;
-      for (int i = K == 1 ? taken : 0; i < n; ++i) {
-        const float v = values[(long)s * p.n_top + i];
+      for (int i = 0; i < n; ++i) {
+        const float v = values[s * p.n_top + i];
         const uint32_t q = key_of(v);
-        const int j = ids[(long)s * p.n_top + i];
+        const int j = ids[s * p.n_top + i];
         if (q > last || (q == last && j <= last_id)) continue;
         if (q > key) {
           key = q;
           value = v;
           id = j;
-          from = s;
         }
         break;
       }
@@ -448,15 +530,10 @@ __global__ __launch_bounds__(64) void join_kernel(ScoreArgs p) {
   };
   head();
   for (int place = 0; place < p.n_top; ++place) {
-    uint32_t best = key;
-#pragma unroll
-    for (int x = 1; x < 64; x *= 2) {
-      const uint32_t o = __shfl_xor(best, x);
-      best = o > best ? o : best;
-    }
+    const uint32_t best = wave_max_key(key);
     const int win = __builtin_ctzll(__ballot(key == best));
     last = best;
-    last_id = __shfl(id, win);
+    last_id = __builtin_amdgcn_readlane(id, win);
     if (lane == win) {
       write_top(p, row, r, place, value, id);
       ++taken;
@@ -470,16 +547,17 @@ static bool sizes_ok(int32_t n_rows, int32_t vocab, int32_t n_top) {
          n_top <= vocab;
 }
 
-// Vectors per thread of a slice: eight, or two when eight would leave most
-// of the CUs without a slice.
+// Vectors per thread of a slice: 32 logits a thread, or 8 when that would
+// leave most of the CUs without a slice.
 static int vectors_for(int32_t n_rows, int32_t vocab, int size) {
-  const long per = (long)kThreads * 8 * 16 / size;
-  return n_rows * ((vocab + per - 1) / per) < 256 ? 2 : 8;
+  const long per = (long)kThreads * 32;
+  return (n_rows * ((vocab + per - 1) / per) < 256 ? 8 : 32) * size / 16;
 }
-// (one more vector than the vocabulary fills: rows may start inside one)
-static int slices_for(int32_t vocab, int size, int v) {
+// aligned: every row starts with a vector; else it may reach into one more
+// than it fills.
+static int slices_for(int32_t vocab, int size, int v, bool aligned) {
   const int per_line = 16 / size;
-  const long lines = ((long)vocab + per_line - 1) / per_line + 1;
+  const long lines = ((long)vocab + per_line - 1) / per_line + (aligned ? 0 : 1);
   return (int)((lines + kThreads * v - 1) / (kThreads * v));
 }
 static size_t round16(size_t n) { return (n + 15) / 16 * 16; }
@@ -493,12 +571,13 @@ static hipError_t run(const ScoreArgs& p, int v, hipStream_t st) {
   const dim3 grid((unsigned)((long)p.rows * p.slices)), block(kThreads);
   const bool top = p.n_top > 0;
   hipError_t e;
-  if (v == 8)
-    e = top ? launch(slice_kernel<TIn, 8, true>, grid, block, st, p)
-            : launch(slice_kernel<TIn, 8, false>, grid, block, st, p);
+  constexpr int kMany = 32 * sizeof(TIn) / 16, kFew = 8 * sizeof(TIn) / 16;
+  if (v == kMany)
+    e = top ? launch(slice_kernel<TIn, kMany, true>, grid, block, st, p)
+            : launch(slice_kernel<TIn, kMany, false>, grid, block, st, p);
   else
-    e = top ? launch(slice_kernel<TIn, 2, true>, grid, block, st, p)
-            : launch(slice_kernel<TIn, 2, false>, grid, block, st, p);
+    e = top ? launch(slice_kernel<TIn, kFew, true>, grid, block, st, p)
+            : launch(slice_kernel<TIn, kFew, false>, grid, block, st, p);
   if (e != hipSuccess || p.slices == 1) return e;
   return launch(join_kernel<TIn>, dim3((unsigned)p.rows), dim3(64), st, p);
 }
@@ -514,7 +593,7 @@ extern "C" size_t gdn_token_scores_workspace_bytes(int32_t n_rows,
   size_t need = 0;
   for (int size = 2; size <= 4; size += 2) {
     const int v = vectors_for(n_rows, vocab, size);
-    const size_t n = bytes_for(n_rows, slices_for(vocab, size, v), n_top);
+    const size_t n = bytes_for(n_rows, slices_for(vocab, size, v, false), n_top);
     if (n > need) need = n;
   }
   return need;
@@ -553,7 +632,10 @@ extern "C" int gdn_token_scores(int32_t n_rows, int32_t vocab,
   const int v = vectors_for(n_rows, vocab, size);
   ScoreArgs p = {logits, tokens, logprob, entropy, top_ids, top_logprobs,
                  row_stride, n_rows, vocab, n_top, inv_temperature,
-                 slices_for(vocab, size, v), nullptr, nullptr, nullptr};
+                 slices_for(vocab, size, v,
+                            !misaligned(logits, 16) &&
+                                (n_rows == 1 || row_stride * size % 16 == 0)),
+                 nullptr, nullptr, nullptr};
   if ((double)n_rows * p.slices > (double)INT_MAX)
     return fail(GDN_EINVAL, "gdn_token_scores: grid too large");
   const size_t n = (size_t)n_rows * p.slices;
