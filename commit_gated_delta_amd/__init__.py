@@ -396,35 +396,61 @@ def prefill_chunked_noalloc(n_seqs, seq_len, h_v, h_k, d_k, d_v, q, k, v,
 
 # The entry points below also check the tensors they are given: the kernels
 # index them by the sizes alone, so a wrong element type, a view that is not
-# contiguous, too few elements or another device is refused here.
-def _tensor(t, name, dtype, numel):
-    if (t.dtype is not dtype or not t.is_contiguous() or t.numel() < numel
-            or not t.is_cuda):
-        raise ValueError(
-            "%s: expected a contiguous device tensor of %s with %d elements, "
-            "got %s %s on %s%s" % (name, dtype, numel, t.dtype,
-                                   tuple(t.shape), t.device,
-                                   "" if t.is_contiguous() else
-                                   ", not contiguous"))
-    return t.data_ptr()
+# contiguous, too few elements or another device than the current one is
+# refused here.  They are called once per layer and token, so the checks and
+# the stream look-up are kept to about 2 us.
+import torch  # noqa: E402  (loaded with the library already)
+
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
+_CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
 
 
-def _optional(t, name, dtype, numel):
-    return None if t is None else _tensor(t, name, dtype, numel)
+def _tensor(t, name, dtype, numel, device):
+    if (t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+            and t.numel() >= numel):
+        return t.data_ptr()
+    raise ValueError(
+        "%s: expected a contiguous tensor of %s with %d elements on the "
+        "current device (cuda:%d), got %s %s on %s%s" % (
+            name, dtype, numel, device, t.dtype, tuple(t.shape), t.device,
+            "" if t.is_contiguous() else ", not contiguous"))
 
 
-def _one_device(*tensors):
-    import torch
-    at = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != at:
-            raise ValueError("a tensor is on %s, the current device is cuda:%d"
-                             % (t.device, at))
+def _optional(t, name, dtype, numel, device):
+    return None if t is None else _tensor(t, name, dtype, numel, device)
 
 
-def _floats():
-    import torch
-    return torch.float32, torch.int32, torch.uint8
+def _workspace(t, device):
+    """Address and size in bytes of a workspace (a uint8 tensor or None)."""
+    if t is None:
+        return None, 0
+    return _tensor(t, "workspace", _U8, 0, device), t.numel()
+
+
+def _code(dtype):
+    try:
+        return _CODES[dtype]
+    except KeyError:
+        raise TypeError("expected bfloat16 or float32, got %s" % dtype) from None
+
+
+def _lanes(t_lane, n):
+    if len(t_lane) != n:
+        raise ValueError("expected %d per-lane values, got %d"
+                         % (n, len(t_lane)))
+    return (ctypes.c_int32 * n)(*t_lane)
+
+
+def _stream_on(stream, device):
+    """As _stream, without making a Stream object for the current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if isinstance(stream, int):
+        return stream
+    if stream.device_index != device:
+        raise ValueError("the stream is on cuda:%d, the current device is "
+                         "cuda:%d" % (stream.device_index, device))
+    return stream.cuda_stream
 
 
 def decay_step(dims: Dims, t_lane, q, k, v, g, S, o, scale=1.0,
@@ -432,36 +458,29 @@ def decay_step(dims: Dims, t_lane, q, k, v, g, S, o, scale=1.0,
                raw_status=False):
     """gdn_decay_step on torch tensors.  keep_state=True is the verify of a
     window, o=None (q may be None then) with t_lane = m its commit."""
-    f32, _, _ = _floats()
-    lanes = _int_array(t_lane, dims.n_lanes)
-    kind = k.dtype
-    code = _dtype_code(k)
-    rows = dims.n_layers * dims.n_lanes * dims.t_max
-    nk, nv = rows * dims.h_k * dims.d_k, rows * dims.h_v * dims.d_v
-    ng = dims.n_layers * dims.h_v if head_decay else rows * dims.h_v
-    ns = dims.n_layers * dims.n_lanes * dims.h_v * dims.d_k * dims.d_v
-    _one_device(q, k, v, g, S, o)
+    kind, lanes = k.dtype, _lanes(t_lane, dims.n_lanes)
+    code, dev = _code(kind), torch.cuda.current_device()
+    h_v, states = dims.h_v, dims.n_layers * dims.n_lanes
+    rows = states * dims.t_max
+    nk, nv = rows * dims.h_k * dims.d_k, rows * h_v * dims.d_v
     st = lib.gdn_decay_step(
-        ctypes.byref(dims), lanes, _optional(q, "q", kind, nk),
-        _tensor(k, "k", kind, nk), _tensor(v, "v", kind, nv), code,
-        _tensor(g, "g", f32, ng), _tensor(S, "S", f32, ns),
-        _optional(o, "o", f32, nv), float(scale),
+        ctypes.byref(dims), lanes, _optional(q, "q", kind, nk, dev),
+        _tensor(k, "k", kind, nk, dev), _tensor(v, "v", kind, nv, dev), code,
+        _tensor(g, "g", _F32,
+                dims.n_layers * h_v if head_decay else rows * h_v, dev),
+        _tensor(S, "S", _F32, states * h_v * dims.d_k * dims.d_v, dev),
+        _optional(o, "o", _F32, nv, dev), scale,
         (GDN_FLAG_HEAD_DECAY if head_decay else 0) |
-        (GDN_FLAG_KEEP_STATE if keep_state else 0), _stream(stream))
+        (GDN_FLAG_KEEP_STATE if keep_state else 0), _stream_on(stream, dev))
     if raw_status:
         return st
     _check(st, "gdn_decay_step")
 
 
-def _lengths(seq_len):
-    vals = [int(x) for x in seq_len]
-    return len(vals), (ctypes.c_int32 * max(len(vals), 1))(*vals), sum(vals)
-
-
 def decay_prefill_workspace_bytes(seq_len, h_v, h_k, d_k, d_v) -> int:
-    n, arr, _ = _lengths(seq_len)
-    return int(lib.gdn_decay_prefill_workspace_bytes(n, arr, h_v, h_k, d_k,
-                                                     d_v))
+    n = len(seq_len)
+    return int(lib.gdn_decay_prefill_workspace_bytes(
+        n, _lanes(seq_len, n), h_v, h_k, d_k, d_v))
 
 
 def decay_prefill(seq_len, h_v, h_k, d_k, d_v, q, k, v, g, S_init, S_final, o,
@@ -469,21 +488,19 @@ def decay_prefill(seq_len, h_v, h_k, d_k, d_v, q, k, v, g, S_init, S_final, o,
                   raw_status=False):
     """gdn_decay_prefill on torch tensors; seq_len lists the lengths of the
     packed sequences."""
-    f32, _, u8 = _floats()
-    n, arr, tokens = _lengths(seq_len)
-    kind = k.dtype
-    code = _dtype_code(k)
+    n, tokens, kind = len(seq_len), sum(seq_len), k.dtype
+    code, dev = _code(kind), torch.cuda.current_device()
     nk, nv, ns = tokens * h_k * d_k, tokens * h_v * d_v, n * h_v * d_k * d_v
-    ws_bytes = 0 if workspace is None else workspace.numel()
-    _one_device(q, k, v, g, S_init, S_final, o, workspace)
+    ws, ws_bytes = _workspace(workspace, dev)
     st = lib.gdn_decay_prefill(
-        n, arr, h_v, h_k, d_k, d_v, _optional(q, "q", kind, nk),
-        _tensor(k, "k", kind, nk), _tensor(v, "v", kind, nv), code,
-        _tensor(g, "g", f32, h_v if head_decay else tokens * h_v),
-        _optional(S_init, "S_init", f32, ns),
-        _optional(S_final, "S_final", f32, ns), _optional(o, "o", f32, nv),
-        _optional(workspace, "workspace", u8, 0), ws_bytes, float(scale),
-        GDN_FLAG_HEAD_DECAY if head_decay else 0, _stream(stream))
+        n, _lanes(seq_len, n), h_v, h_k, d_k, d_v,
+        _optional(q, "q", kind, nk, dev), _tensor(k, "k", kind, nk, dev),
+        _tensor(v, "v", kind, nv, dev), code,
+        _tensor(g, "g", _F32, h_v if head_decay else tokens * h_v, dev),
+        _optional(S_init, "S_init", _F32, ns, dev),
+        _optional(S_final, "S_final", _F32, ns, dev),
+        _optional(o, "o", _F32, nv, dev), ws, ws_bytes, scale,
+        GDN_FLAG_HEAD_DECAY if head_decay else 0, _stream_on(stream, dev))
     if raw_status:
         return st
     _check(st, "gdn_decay_prefill")
@@ -497,22 +514,19 @@ def paged_attention(dims: KvDims, t_lane, q, k_cache, v_cache, page_table,
                     kv_len, o, workspace, scale=1.0, stream=None,
                     raw_status=False):
     """gdn_paged_attention on torch tensors."""
-    f32, i32, u8 = _floats()
-    lanes = _int_array(t_lane, dims.n_lanes)
-    kind = q.dtype
-    code = _dtype_code(q)
-    nq = dims.n_lanes * dims.t_max * dims.h_q * dims.d
-    nc = dims.n_pages * dims.h_kv * dims.page_size * dims.d
-    ws_bytes = 0 if workspace is None else workspace.numel()
-    _one_device(q, k_cache, v_cache, page_table, kv_len, o, workspace)
+    n, d, kind = dims.n_lanes, dims.d, q.dtype
+    lanes, code, dev = _lanes(t_lane, n), _code(kind), torch.cuda.current_device()
+    nq = n * dims.t_max * dims.h_q * d
+    nc = dims.n_pages * dims.h_kv * dims.page_size * d
+    ws, ws_bytes = _workspace(workspace, dev)
     st = lib.gdn_paged_attention(
-        ctypes.byref(dims), lanes, _tensor(q, "q", kind, nq),
-        _tensor(k_cache, "k_cache", kind, nc),
-        _tensor(v_cache, "v_cache", kind, nc), code,
-        _tensor(page_table, "page_table", i32, dims.n_lanes * dims.max_pages),
-        _tensor(kv_len, "kv_len", i32, dims.n_lanes),
-        _tensor(o, "o", f32, nq), _optional(workspace, "workspace", u8, 0),
-        ws_bytes, float(scale), _stream(stream))
+        ctypes.byref(dims), lanes, _tensor(q, "q", kind, nq, dev),
+        _tensor(k_cache, "k_cache", kind, nc, dev),
+        _tensor(v_cache, "v_cache", kind, nc, dev), code,
+        _tensor(page_table, "page_table", _I32, n * dims.max_pages, dev),
+        _tensor(kv_len, "kv_len", _I32, n, dev),
+        _tensor(o, "o", _F32, nq, dev), ws, ws_bytes, scale,
+        _stream_on(stream, dev))
     if raw_status:
         return st
     _check(st, "gdn_paged_attention")
@@ -521,20 +535,16 @@ def paged_attention(dims: KvDims, t_lane, q, k_cache, v_cache, page_table,
 def kv_append(dims: KvDims, t_lane, k, v, k_cache, v_cache, page_table,
               kv_len, stream=None, raw_status=False):
     """gdn_kv_append on torch tensors."""
-    _, i32, _ = _floats()
-    lanes = _int_array(t_lane, dims.n_lanes)
-    kind = k.dtype
-    code = _dtype_code(k)
-    nr = dims.n_lanes * dims.t_max * dims.h_kv * dims.d
-    nc = dims.n_pages * dims.h_kv * dims.page_size * dims.d
-    _one_device(k, v, k_cache, v_cache, page_table, kv_len)
+    n, kind, row = dims.n_lanes, k.dtype, dims.h_kv * dims.d
+    lanes, code, dev = _lanes(t_lane, n), _code(kind), torch.cuda.current_device()
+    nr, nc = n * dims.t_max * row, dims.n_pages * dims.page_size * row
     st = lib.gdn_kv_append(
-        ctypes.byref(dims), lanes, _tensor(k, "k", kind, nr),
-        _tensor(v, "v", kind, nr), code,
-        _tensor(k_cache, "k_cache", kind, nc),
-        _tensor(v_cache, "v_cache", kind, nc),
-        _tensor(page_table, "page_table", i32, dims.n_lanes * dims.max_pages),
-        _tensor(kv_len, "kv_len", i32, dims.n_lanes), _stream(stream))
+        ctypes.byref(dims), lanes, _tensor(k, "k", kind, nr, dev),
+        _tensor(v, "v", kind, nr, dev), code,
+        _tensor(k_cache, "k_cache", kind, nc, dev),
+        _tensor(v_cache, "v_cache", kind, nc, dev),
+        _tensor(page_table, "page_table", _I32, n * dims.max_pages, dev),
+        _tensor(kv_len, "kv_len", _I32, n, dev), _stream_on(stream, dev))
     if raw_status:
         return st
     _check(st, "gdn_kv_append")
@@ -549,25 +559,24 @@ def token_scores(logits, tokens, n_top, logprob, entropy, top_ids,
                  raw_status=False):
     """gdn_token_scores on torch tensors.  logits is [n_rows, vocab] with
     contiguous rows (their stride may be larger than vocab)."""
-    f32, i32, u8 = _floats()
-    code = _dtype_code(logits)
-    if logits.dim() != 2 or not logits.is_cuda or (
-            logits.size(1) > 1 and logits.stride(1) != 1):
-        raise ValueError("logits: expected a device tensor [n_rows, vocab] "
-                         "with contiguous rows")
+    code, dev = _code(logits.dtype), torch.cuda.current_device()
     rows, vocab = logits.shape
-    stride = logits.stride(0) if rows > 1 else vocab
-    ws_bytes = 0 if workspace is None else workspace.numel()
-    _one_device(logits, tokens, logprob, entropy, top_ids, top_logprobs,
-                workspace)
+    stride, unit = logits.stride()
+    if logits.get_device() != dev or (vocab > 1 and unit != 1) or (
+            rows > 1 and stride < vocab):
+        raise ValueError("logits: expected a tensor [n_rows, vocab] with "
+                         "contiguous rows on the current device (cuda:%d), "
+                         "got strides %s on %s" % (dev, logits.stride(),
+                                                   logits.device))
+    ws, ws_bytes = _workspace(workspace, dev)
     st = lib.gdn_token_scores(
-        rows, vocab, stride, logits.data_ptr(), code,
-        _optional(tokens, "tokens", i32, rows), n_top, float(inv_temperature),
-        _optional(logprob, "logprob", f32, rows),
-        _optional(entropy, "entropy", f32, rows),
-        _optional(top_ids, "top_ids", i32, rows * n_top),
-        _optional(top_logprobs, "top_logprobs", f32, rows * n_top),
-        _optional(workspace, "workspace", u8, 0), ws_bytes, _stream(stream))
+        rows, vocab, stride if rows > 1 else vocab, logits.data_ptr(), code,
+        _optional(tokens, "tokens", _I32, rows, dev), n_top, inv_temperature,
+        _optional(logprob, "logprob", _F32, rows, dev),
+        _optional(entropy, "entropy", _F32, rows, dev),
+        _optional(top_ids, "top_ids", _I32, rows * n_top, dev),
+        _optional(top_logprobs, "top_logprobs", _F32, rows * n_top, dev),
+        ws, ws_bytes, _stream_on(stream, dev))
     if raw_status:
         return st
     _check(st, "gdn_token_scores")

@@ -177,21 +177,16 @@ def test_scores_refusals():
 
 # ------------------------------------------------------------------ binding
 def test_binding_refuses_tensors_that_do_not_fit():
-    """Host tensors, and lists of the wrong length (torch reports no device
-    here, so no call gets further)."""
     z = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t)
-    f = lambda *s: z(*s, t=torch.float32)
-    dims = gdn.Dims.of(1, 2, 4, 2, 16, 16, 1)
     with pytest.raises(ValueError):
-        gdn.decay_step(dims, [1], z(2, 2, 16), z(2, 2, 16), z(2, 4, 16),
-                       f(2, 4), f(2, 4, 16, 16), f(2, 4, 16), stream=0)
-    kind = torch.float64
+        gdn._lanes([1], 2)
     with pytest.raises(TypeError):
-        gdn.decay_step(dims, [1, 1], z(2, 2, 16, t=kind), z(2, 2, 16, t=kind),
-                       z(2, 4, 16, t=kind), f(2, 4), f(2, 4, 16, 16),
-                       f(2, 4, 16), stream=0)
-    for t in (f(5), z(4, 2)[:, 0], z(3)):     # type, order, size
+        gdn._code(torch.float64)
+    for t in (z(5, t=torch.float32), z(4, 2)[:, 0], z(3)):   # type, order, size
         with pytest.raises(ValueError):
-            gdn._tensor(t, "x", torch.bfloat16, 4)
-    with pytest.raises(ValueError):           # not on a device
-        gdn._tensor(z(4), "x", torch.bfloat16, 4)
+            gdn._tensor(t, "x", torch.bfloat16, 4, -1)
+    with pytest.raises(ValueError):                          # not on a device
+        gdn._tensor(z(4), "x", torch.bfloat16, 4, 0)
+    x = z(4)     # (a host tensor's device number is -1)
+    assert gdn._tensor(x, "x", torch.bfloat16, 4, -1) == x.data_ptr()
+    assert gdn._optional(None, "x", torch.bfloat16, 4, 0) is None
