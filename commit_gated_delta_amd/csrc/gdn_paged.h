@@ -138,90 +138,258 @@ struct AttendArgs {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// The rows of a key-value head (token t and query head h' of its group are
-// row t * group + h') are taken 16 RT WR at a time by a workgroup of four
-// waves: WR waves side by side in the rows, 4 / WR sharing out the split's
-// positions, 32 at a step.  Per step a wave forms S^T = K Q^T (rows
-// positions, columns rows of q), whose result layout is at once the B operand
-// of O^T = V^T P^T; V passes through LDS for the transposed read.  In O^T and
-// S^T a row of q is one lane column, so the running maximum m and sum l of
-// the softmax and the rescaling of O are per lane.  m is raised only when a
-// score is more than 2^8 above it, which keeps the exchange between lanes
-// out of nearly every step and costs f32 no precision; l stays apart per
-// lane group until the end.  P enters as three exact bf16 parts (see
-// gdn_mfma_op.h).  The next step's K rows are loaded when this step's scores
-// are done and its V rows when V is in LDS, page numbers a step earlier.
-template <int D, typename T, int RT, int WR>
-__global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs p,
-                                                        gdn::LaneTable tl) {
+__device__ __forceinline__ float elem(const uint16_t* p, long i) {
+  return __uint_as_float((uint32_t)p[i] << 16);
+}
+__device__ __forceinline__ float elem(const float* p, long i) { return p[i]; }
+
+// The rows of a key-value head are those of q that read it: token t and query
+// head h' of its group are row t * group + h'.  Per step of 32 positions a
+// wave forms S^T = K Q^T for 16 RT rows, whose result layout (lane column =
+// row of q) is at once the B operand of O^T = V^T P^T; V passes through LDS
+// for the transposed read.  So the running maximum m and sum l of the softmax
+// and the rescaling of O are per lane.  m is raised only when a score is more
+// than 2^8 above it, which keeps the exchange between lanes out of nearly
+// every step and costs f32 no precision; l stays apart per lane group until
+// the end.  P enters as three exact bf16 parts (gdn_mfma_op.h).
+//
+// Two kernels share this.  For up to 32 rows (16 at D = 256) the four waves
+// of attend_kernel share out the positions and each loads its own: the work
+// is reading the cache.  For more rows those of rows_kernel take 16 RT rows
+// each of the same positions, staged once for all four.
+constexpr float kSlack = 8.f;
+
+// Scores, softmax state and outputs of a wave.
+template <int D, typename T, int RT>
+struct Rows {
   typedef Op<T> O;
   typedef typename O::Raw Raw;
   typedef typename O::Wide Wide;
   typedef Tile<T, D> TL;
-  constexpr int KS = D / 32, CT = D / 16, WP = 4 / WR, kRows = 16 * RT * WR;
-  constexpr int kPieces = sizeof(Raw) / 16;  // 16-byte loads per fragment
-  constexpr float kSlack = 8.f;
-  constexpr int kTileBytes = 32 * TL::kPitch * (int)sizeof(T);
-  constexpr int kMergeBytes = WP > 1 ? WR * 16 * RT * D * 4 : 0;
-  constexpr int kPool = 4 * kTileBytes > kMergeBytes ? 4 * kTileBytes : kMergeBytes;
-  __shared__ __attribute__((aligned(16))) T Qs[kRows * TL::kPitch];
-  __shared__ __attribute__((aligned(16))) char pool[kPool];
-  __shared__ float ml[4][2][16 * RT];
-  const KvArgs& a = p.kv;
-  const int per_item = a.h_kv * p.groups;
-  const Split s = find_split(a, tl, blockIdx.x / per_item, p.target, false);
-  if (s.lane < 0) return;
-  const int hk = blockIdx.x % per_item / p.groups;
-  const int row0 = blockIdx.x % p.groups * kRows;
-  const int group = a.h_q / a.h_kv, T_n = tl.v[s.lane];
-  const int rows = T_n * group;
-  if (row0 >= rows) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = gdn::uniform(tid >> 6);
-  const int n = lane & 15, g4 = lane >> 4;
-  const int wr = wave % WR, wp = wave / WR;
+  static constexpr int KS = D / 32, CT = D / 16;
+  f32x4 acc[RT][CT], sc[RT][2];
+  float m[RT], l[RT];
+  int end[RT];  // positions that the lane's rows see
 
-  // q rows of the workgroup (zeros past the last)
-  {
-    constexpr int kPer = TL::kPer;
-    for (int i = tid; i < kRows * TL::kPieces; i += 256) {
-      const int r = i / TL::kPieces, c = i % TL::kPieces;
-      u32x4 x = {0, 0, 0, 0};
-      if (row0 + r < rows) {
-        const int t = (row0 + r) / group, h = hk * group + (row0 + r) % group;
-        x = *reinterpret_cast<const u32x4*>(
-            (const T*)p.q +
-            (((long)s.lane * a.t_max + t) * a.h_q + h) * D + c * kPer);
-      }
-      *reinterpret_cast<u32x4*>(Qs + TL::at(r, c)) = x;
+  __device__ __forceinline__ void init(int row0, int rows, int len, int T_n,
+                                       int group) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const int row = row0 + 16 * r + (threadIdx.x & 15);
+      end[r] = row < rows ? len - T_n + row / group + 1 : 0;
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int c = 0; c < CT; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
   }
-  __syncthreads();
+  // Scores of positions p0 .. p0 + 31 -> sc = exp2(x - m), raising m when
+  // needed.  Unless all rows see all of them (whole), bit i of ok says that
+  // position p0 + i is in the cache.
+  __device__ __forceinline__ void softmax(float scale, bool whole, uint32_t ok,
+                                          int p0) {
+    const int g4 = (threadIdx.x & 63) >> 4;
+    bool raise = false;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = sc[r][h][e] * scale;
+          if (!whole) {
+            const int i = 16 * h + 4 * g4 + e;
+            if (!(ok >> i & 1) || p0 + i >= end[r]) x = -INFINITY;
+          }
+          sc[r][h][e] = x;
+          raise |= x > m[r] + kSlack;
+        }
+    if (__any(raise)) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        float top = m[r];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[r][h][e]);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float keep =
+            m[r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[r] - top);
+        m[r] = top;
+        l[r] *= keep;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[r][c] *= keep;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const float ref = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sc[r][h][e] = __builtin_amdgcn_exp2f(sc[r][h][e] - ref);
+          l[r] += sc[r][h][e];
+        }
+    }
+  }
+  // O^T += V^T P^T with V rows r0 .. r0 + 31 of the tile.
+  __device__ __forceinline__ void values(const T* Vs, int r0) {
+    Wide pw[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) pw[r] = O::wide(sc[r][0], sc[r][1]);
+    constexpr int kTwo = CT % 2 == 0 ? 2 : 1;
+#pragma unroll
+    for (int c = 0; c < CT; c += kTwo) {
+      Raw vf[kTwo];
+#pragma unroll
+      for (int y = 0; y < kTwo; ++y)
+        vf[y] = O::template column<TL>(Vs, r0, 16 * (c + y), 4,
+                                       threadIdx.x & 63);
+#pragma unroll
+      for (int i = 0; i < O::kSteps; ++i)
+#pragma unroll
+        for (int y = 0; y < kTwo; ++y)
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            acc[r][c + y] = O::step(i, vf[y], pw[r], acc[r][c + y]);
+    }
+  }
+  // What infinities and NaN in V at positions from .. stop - 1 of a step add
+  // to the rows that see them; `values` took them as zeros, as they have to
+  // count for the rows that do not.  (p is 0 for those, and 0 times NaN is
+  // not.)  Rarely needed and slow.
+  __device__ __forceinline__ void special(const KvArgs& a, int n, int hk,
+                                          int p0, int from, int stop) {
+    const int lane = threadIdx.x & 63, g4 = lane >> 4;
+#pragma unroll 1
+    for (int pos = from; pos < stop; ++pos) {
+      const long row = row_of(a, n, hk, pos, D);
+      if (row < 0) continue;
+      const int i = pos - p0;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        float p = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = __shfl(sc[r][h][e], 16 * ((i & 15) >> 2) + (lane & 15));
+            if (h == i >> 4 && e == (i & 3)) p = x;
+          }
+        if (pos >= end[r]) continue;
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v = elem((const T*)a.v, row + 16 * c + 4 * g4 + e);
+            if (!(fabsf(v) < INFINITY)) acc[r][c][e] += p * v;
+          }
+      }
+    }
+  }
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      l[r] += __shfl_xor(l[r], 16);
+      l[r] += __shfl_xor(l[r], 32);
+    }
+  }
+};
 
+// Whether a dword of V holds an infinity or a NaN, and the dword with those
+// as zeros.
+template <typename T>
+__device__ __forceinline__ bool clear_special(uint32_t& w) {
+  if constexpr (sizeof(T) == 4) {
+    const bool s = (w & 0x7f800000u) == 0x7f800000u;
+    if (s) w = 0;
+    return s;
+  } else {
+    const bool lo = (w & 0x7f80u) == 0x7f80u;
+    const bool hi = (w & 0x7f800000u) == 0x7f800000u;
+    if (lo) w &= 0xffff0000u;
+    if (hi) w &= 0xffffu;
+    return lo || hi;
+  }
+}
+
+// q rows row0 .. row0 + n - 1 of a key-value head (zeros past the last).
+template <int D, typename T>
+__device__ __forceinline__ void stage_q(T* Qs, const AttendArgs& p, int lane,
+                                        int hk, int row0, int n, int rows) {
+  typedef Tile<T, D> TL;
+  const int group = p.kv.h_q / p.kv.h_kv;
+  for (int i = threadIdx.x; i < n * TL::kPieces; i += 256) {
+    const int r = i / TL::kPieces, c = i % TL::kPieces;
+    u32x4 x = {0, 0, 0, 0};
+    if (row0 + r < rows) {
+      const int t = (row0 + r) / group, h = hk * group + (row0 + r) % group;
+      x = *reinterpret_cast<const u32x4*>(
+          (const T*)p.q +
+          (((long)lane * p.kv.t_max + t) * p.kv.h_q + h) * D + c * TL::kPer);
+    }
+    *reinterpret_cast<u32x4*>(Qs + TL::at(r, c)) = x;
+  }
+}
+
+// Where a row's result goes: o, when the lane has one split, or the split's
+// slot (unnormalised, with its m and l).
+__device__ __forceinline__ float* row_out(const AttendArgs& p, const Split& s,
+                                          int hk, int row, int d, float m,
+                                          float l, bool first, float& scale) {
+  const KvArgs& a = p.kv;
+  const int group = a.h_q / a.h_kv;
+  if (s.n == 1) {
+    scale = l == 0.f ? 0.f : 1.f / l;
+    return p.o + (((long)s.lane * a.t_max + row / group) * a.h_q + hk * group +
+                  row % group) * d;
+  }
+  const long at = ((long)(s.slot + s.nth) * a.h_kv + hk) * p.rows + row;
+  if (first) {
+    p.part_ml[2 * at] = m;
+    p.part_ml[2 * at + 1] = l;
+  }
+  scale = 1.f;
+  return p.part_o + at * d;
+}
+
+// Few rows: four waves share out a split's positions, 32 at a step.  The next
+// step's K rows are loaded when this step's scores are done and its V rows
+// when V is in LDS, page numbers a step earlier.
+template <int D, typename T, int RT>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_kernel(
+    AttendArgs p, gdn::LaneTable tl) {
+  typedef Rows<D, T, RT> R;
+  typedef typename R::O O;
+  typedef typename R::Raw Raw;
+  typedef typename R::TL TL;
+  constexpr int KS = R::KS, CT = R::CT, kRows = 16 * RT;
+  constexpr int kPieces = sizeof(Raw) / 16;  // 16-byte loads per fragment
+  constexpr int kTileBytes = 32 * TL::kPitch * (int)sizeof(T);
+  constexpr int kSumPitch = D + 4;  // (rows on different banks)
+  constexpr int kSumBytes = kRows * kSumPitch * 4;
+  constexpr int kPer = kTileBytes > kSumBytes ? kTileBytes : kSumBytes;
+  __shared__ __attribute__((aligned(16))) T Qs[kRows * TL::kPitch];
+  __shared__ __attribute__((aligned(16))) char pool[4 * kPer];
+  __shared__ float ml[4][2][kRows];
+  const KvArgs& a = p.kv;
+  const Split s = find_split(a, tl, blockIdx.x / a.h_kv, p.target, false);
+  if (s.lane < 0) return;
+  const int hk = blockIdx.x % a.h_kv;
+  const int group = a.h_q / a.h_kv, T_n = tl.v[s.lane];
+  const int rows = T_n * group;
+  const int tid = threadIdx.x, lane = tid & 63, wave = gdn::uniform(tid >> 6);
+  const int n = lane & 15, g4 = lane >> 4;
   const int begin = s.nth * s.units * kUnit;
   const int stop = begin + s.units * kUnit < s.len ? begin + s.units * kUnit : s.len;
   const int steps = (stop - begin + 31) / 32;
-  // first position that some row of the window does not see
-  const int open = s.len - T_n + 1;
-  int end[RT];  // positions that the lane's row sees
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int row = row0 + (wr * RT + r) * 16 + n;
-    end[r] = row < rows ? s.len - T_n + row / group + 1 : 0;
-  }
-  T* Vs = reinterpret_cast<T*>(pool + wave * kTileBytes);
+  const int open = s.len - T_n + 1;  // first position that some row cannot see
+  T* Vs = reinterpret_cast<T*>(pool + wave * kPer);
   const T* kc = (const T*)a.k + 8 * g4;
   const T* vc = (const T*)a.v + 8 * g4;
   const int* table = a.table + (long)s.lane * a.max_pages;
-
-  f32x4 acc[RT][CT];
-  float m[RT], l[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    m[r] = -INFINITY;
-    l[r] = 0.f;
-#pragma unroll
-    for (int c = 0; c < CT; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
 
   // position of half h of a step's rows in this lane
   auto pos_of = [&](int step, int h) { return begin + 32 * step + 16 * h + n; };
@@ -256,199 +424,270 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs p,
               *reinterpret_cast<const u32x4*>(c + at[h] + 32 * i + 4 * x);
   };
 
-  if (wp < steps) {
-    look_up(wp);
-    place(wp);
+  if (wave < steps) look_up(wave);
+  stage_q<D, T>(Qs, p, s.lane, hk, 0, kRows, rows);
+  if (wave < steps) {
+    place(wave);
     fetch(kc, kr);
     fetch(vc, vr);
-    look_up(wp + WP);
+    look_up(wave + 4);
   }
-  for (int step = wp; step < steps; step += WP) {
+  R x;
+  x.init(0, rows, s.len, T_n, group);
+  __syncthreads();
+  for (int step = wave; step < steps; step += 4) {
     const bool here[2] = {there[0], there[1]};
-    // scores
-    f32x4 sc[RT][2];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) sc[r][0] = sc[r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < RT; ++r)
+      x.sc[r][0] = x.sc[r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < KS; ++i)
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        const Raw qf = O::template row<TL>(Qs, 16 * (wr * RT + r), n, 4 * i + g4);
+        const Raw qf = O::template row<TL>(Qs, 16 * r, n, 4 * i + g4);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           Raw kf;
           __builtin_memcpy(&kf, kr[h][i], sizeof(Raw));
-          sc[r][h] = O::mul(kf, qf, sc[r][h]);
+          x.sc[r][h] = O::mul(kf, qf, x.sc[r][h]);
         }
       }
-    const int next = step + WP;
+    const int next = step + 4;
     if (next < steps) {
       place(next);
       fetch(kc, kr);
-      look_up(next + WP);
+      look_up(next + 4);
     }
-    // softmax
     const int p0 = begin + 32 * step;
     const bool whole =
         p0 + 32 <= (open < stop ? open : stop) && __all(here[0] && here[1]);
-    uint64_t ok = 0;  // bit of position i of the step: its row is there
+    uint32_t ok = 0;  // bit of position i of the step: its row is there
     if (!whole)
-      ok = (__ballot(here[0]) & 0xffffull) | (__ballot(here[1]) & 0xffffull) << 16;
-    bool raise = false;
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = sc[r][h][e] * p.scale;
-          if (!whole) {
-            const int i = 16 * h + 4 * g4 + e;
-            if (!(ok >> i & 1) || p0 + i >= end[r]) x = -INFINITY;
-          }
-          sc[r][h][e] = x;
-          raise |= x > m[r] + kSlack;
-        }
-    if (__any(raise)) {
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        float top = m[r];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[r][h][e]);
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float keep =
-            m[r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[r] - top);
-        m[r] = top;
-        l[r] *= keep;
-#pragma unroll
-        for (int c = 0; c < CT; ++c) acc[r][c] *= keep;
-      }
-    }
-    Wide pw[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const float ref = m[r] == -INFINITY ? 0.f : m[r];
-      f32x4 e2[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          e2[h][e] = __builtin_amdgcn_exp2f(sc[r][h][e] - ref);
-          l[r] += e2[h][e];
-        }
-      pw[r] = O::wide(e2[0], e2[1]);
-    }
+      ok = ((uint32_t)__ballot(here[0]) & 0xffffu) |
+           ((uint32_t)__ballot(here[1]) & 0xffffu) << 16;
+    x.softmax(p.scale, whole, ok, p0);
     // V through LDS.  Rows that are not there count as zeros.
+    bool odd = false;
     if (!whole) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        if (!here[h])
 #pragma unroll
-          for (int i = 0; i < KS; ++i)
+        for (int i = 0; i < KS; ++i)
 #pragma unroll
-            for (int x = 0; x < kPieces; ++x) vr[h][i][x] = u32x4{0, 0, 0, 0};
+          for (int y = 0; y < kPieces; ++y) {
+            if (!here[h]) vr[h][i][y] = u32x4{0, 0, 0, 0};
+            if (pos_of(step, h) >= open)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t w = vr[h][i][y][e];
+                odd |= clear_special<T>(w);
+                vr[h][i][y][e] = w;
+              }
+          }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < KS; ++i)
 #pragma unroll
-        for (int x = 0; x < kPieces; ++x)
+        for (int y = 0; y < kPieces; ++y)
           *reinterpret_cast<u32x4*>(
-              Vs + TL::at(n, kPieces * (4 * i + g4) + x) + 16 * h * TL::kPitch) =
-              vr[h][i][x];
+              Vs + TL::at(n, kPieces * (4 * i + g4) + y) + 16 * h * TL::kPitch) =
+              vr[h][i][y];
     if (next < steps) fetch(vc, vr);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      const Raw vf = O::template column<TL>(Vs, 0, 16 * c, 4, lane);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) acc[r][c] = O::mul(vf, pw[r], acc[r][c]);
-    }
+    x.values(Vs, 0);
+    if (__any(odd))
+      x.special(a, s.lane, hk, p0, p0 > open ? p0 : open,
+                p0 + 32 < stop ? p0 + 32 : stop);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
 
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    l[r] += __shfl_xor(l[r], 16);
-    l[r] += __shfl_xor(l[r], 32);
-  }
-  // the waves that shared out the positions
-  float* sum = reinterpret_cast<float*>(pool) + wr * 16 * RT * D;
-  if constexpr (WP > 1) {
-    if (g4 == 0)
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        ml[wave][0][16 * r + n] = m[r];
-        ml[wave][1][16 * r + n] = l[r];
-      }
-    __syncthreads();
+  // the four waves' results: each scaled to the common maximum, written to
+  // LDS and added up by all threads
+  x.finish();
+  if (g4 == 0)
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      float top = -INFINITY, tot = 0.f;
-#pragma unroll
-      for (int w = 0; w < WP; ++w)
-        top = fmaxf(top, ml[w * WR + wr][0][16 * r + n]);
-#pragma unroll
-      for (int w = 0; w < WP; ++w) {
-        const float mw = ml[w * WR + wr][0][16 * r + n];
-        tot += mw == -INFINITY ? 0.f
-                               : ml[w * WR + wr][1][16 * r + n] *
-                                     __builtin_amdgcn_exp2f(mw - top);
-      }
-      const float keep =
-          m[r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[r] - top);
-      m[r] = top;
-      l[r] = tot;
-#pragma unroll
-      for (int c = 0; c < CT; ++c) acc[r][c] *= keep;
+      ml[wave][0][16 * r + n] = x.m[r];
+      ml[wave][1][16 * r + n] = x.l[r];
     }
-    for (int w = WP - 1; w >= 0; --w) {
-      if (wp == w) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            f32x4* x = reinterpret_cast<f32x4*>(
-                sum + (16 * r + n) * D + 16 * c + 4 * g4);
-            if (w == WP - 1) *x = acc[r][c];
-            else if (w > 0) *x += acc[r][c];
-            else acc[r][c] += *x;
-          }
-      }
-      __syncthreads();
-    }
-    if (wp > 0) return;
-  }
+  __syncthreads();
+  float* sum = reinterpret_cast<float*>(pool + wave * kPer);
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    const int row = row0 + (wr * RT + r) * 16 + n;
-    if (row >= rows) continue;
-    float* dst;
-    if (s.n == 1) {
-      const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+    float top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < CT; ++c) acc[r][c] *= inv;
-      dst = p.o + (((long)s.lane * a.t_max + row / group) * a.h_q + hk * group +
-                   row % group) * D;
-    } else {
-      const long at_row = ((long)(s.slot + s.nth) * a.h_kv + hk) * p.rows + row;
-      if (g4 == 0) {
-        p.part_ml[2 * at_row] = m[r];
-        p.part_ml[2 * at_row + 1] = l[r];
-      }
-      dst = p.part_o + at_row * D;
-    }
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w][0][16 * r + n]);
+    const float keep =
+        x.m[r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x.m[r] - top);
 #pragma unroll
     for (int c = 0; c < CT; ++c)
-      *reinterpret_cast<f32x4*>(dst + 16 * c + 4 * g4) = acc[r][c];
+      *reinterpret_cast<f32x4*>(sum + (16 * r + n) * kSumPitch + 16 * c +
+                                4 * g4) = x.acc[r][c] * keep;
+  }
+  __syncthreads();
+  const int used = rows < kRows ? rows : kRows;
+  for (int i = tid; i < used * (D / 4); i += 256) {
+    const int row = i / (D / 4), c = i % (D / 4) * 4;
+    float top = -INFINITY, tot = 0.f;
+    f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w][0][row]);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float mw = ml[w][0][row];
+      if (mw != -INFINITY || ml[w][1][row] != 0.f)
+        tot += ml[w][1][row] *
+               (mw == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mw - top));
+      y += *reinterpret_cast<const f32x4*>(
+          reinterpret_cast<const float*>(pool + w * kPer) + row * kSumPitch + c);
+    }
+    float f;
+    float* dst = row_out(p, s, hk, row, D, top, tot, c == 0, f);
+    *reinterpret_cast<f32x4*>(dst + c) = y * f;
+  }
+}
+
+// Many rows: the waves take 16 RT rows each, and a tile of positions is
+// staged in LDS for all of them.
+template <int D, typename T, int RT>
+__global__ __launch_bounds__(256, D == 256 || sizeof(T) == 4 ? 1 : 2)
+void rows_kernel(AttendArgs p, gdn::LaneTable tl) {
+  typedef Rows<D, T, RT> R;
+  typedef typename R::O O;
+  typedef typename R::Raw Raw;
+  typedef typename R::TL TL;
+  constexpr int KS = R::KS, CT = R::CT, kRows = 64 * RT;
+  constexpr int kTile = sizeof(T) == 2 ? 64 : 32;  // positions per tile
+  constexpr int kStep = 256 / TL::kPieces;         // rows per piece of a thread
+  constexpr int kN = kTile / kStep;                // pieces of a thread
+  __shared__ __attribute__((aligned(16))) T Qs[kRows * TL::kPitch];
+  __shared__ __attribute__((aligned(16))) T Ks[kTile * TL::kPitch];
+  __shared__ __attribute__((aligned(16))) T Vs[kTile * TL::kPitch];
+  const KvArgs& a = p.kv;
+  const int per_item = a.h_kv * p.groups;
+  const Split s = find_split(a, tl, blockIdx.x / per_item, p.target, false);
+  if (s.lane < 0) return;
+  const int hk = blockIdx.x % per_item / p.groups;
+  const int row0 = blockIdx.x % p.groups * kRows;
+  const int group = a.h_q / a.h_kv, T_n = tl.v[s.lane];
+  const int rows = T_n * group;
+  if (row0 >= rows) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = gdn::uniform(tid >> 6);
+  const int n = lane & 15, g4 = lane >> 4;
+  const int begin = s.nth * s.units * kUnit;
+  const int stop = begin + s.units * kUnit < s.len ? begin + s.units * kUnit : s.len;
+  const int tiles = (stop - begin + kTile - 1) / kTile;
+  const int open = s.len - T_n + 1;
+  const int* table = a.table + (long)s.lane * a.max_pages;
+
+  // lane i of every wave keeps track of row i of a tile
+  int page = -1;        // page number of the row, a tile ahead of its use
+  long at = 0;          // where it is
+  uint64_t ok = 0;      // rows of the tile in transit that are there
+  auto look_up = [&](int tile) {
+    const int pos = begin + tile * kTile + lane % kTile;
+    page = pos < stop ? table[page_of(a, pos)] : -1;
+  };
+  auto place = [&](int tile) {
+    const int pos = begin + tile * kTile + lane % kTile;
+    const long row = row_in(a, page, hk, pos - page_of(a, pos) * a.page, D);
+    ok = __ballot(row >= 0);
+    at = row >= 0 ? row : 0;
+  };
+  u32x4 kr[kN], vr[kN];
+  const int piece = tid % TL::kPieces, r0 = tid / TL::kPieces;
+  auto fetch = [&]() {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int src = r0 + i * kStep;
+      const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)at, src);
+      const uint32_t hi = (uint32_t)__shfl((int)(at >> 32), src);
+      const long off = (long)((uint64_t)hi << 32 | lo) + piece * TL::kPer;
+      kr[i] = *reinterpret_cast<const u32x4*>((const T*)a.k + off);
+      vr[i] = *reinterpret_cast<const u32x4*>((const T*)a.v + off);
+    }
+  };
+  if (tiles > 0) look_up(0);
+  stage_q<D, T>(Qs, p, s.lane, hk, row0, kRows, rows);
+  if (tiles > 0) {
+    place(0);
+    fetch();
+    look_up(1);
+  }
+  R x;
+  x.init(row0 + 16 * RT * wave, rows, s.len, T_n, group);
+  for (int tile = 0; tile < tiles; ++tile) {
+    const int t0 = begin + tile * kTile;
+    const uint64_t here = ok;
+    const bool whole = t0 + kTile <= (open < stop ? open : stop) && here == ~0ull;
+    bool odd = false;
+    __syncthreads();  // the tile before has been read
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int r = r0 + i * kStep;
+      if (!whole) {
+        if (!(here >> r & 1)) vr[i] = u32x4{0, 0, 0, 0};
+        if (t0 + r >= open)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w = vr[i][e];
+            odd |= clear_special<T>(w);
+            vr[i][e] = w;
+          }
+      }
+      *reinterpret_cast<u32x4*>(Ks + TL::at(r, piece)) = kr[i];
+      *reinterpret_cast<u32x4*>(Vs + TL::at(r, piece)) = vr[i];
+    }
+    if (whole) __syncthreads();
+    else odd = __syncthreads_or(odd);
+    if (tile + 1 < tiles) {
+      place(tile + 1);
+      fetch();
+      look_up(tile + 2);
+    }
+    if (row0 + 16 * RT * wave >= rows) continue;
+#pragma unroll
+    for (int half = 0; half < kTile / 32; ++half) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        x.sc[r][0] = x.sc[r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        Raw kf[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          kf[h] = O::template row<TL>(Ks, 32 * half + 16 * h, n, 4 * i + g4);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const Raw qf = O::template row<TL>(Qs, 16 * (RT * wave + r), n, 4 * i + g4);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) x.sc[r][h] = O::mul(kf[h], qf, x.sc[r][h]);
+        }
+      }
+      const int p0 = t0 + 32 * half;
+      x.softmax(p.scale, whole, (uint32_t)(here >> (32 * half)), p0);
+      x.values(Vs, 32 * half);
+      if (odd)
+        x.special(a, s.lane, hk, p0, p0 > open ? p0 : open,
+                  p0 + 32 < stop ? p0 + 32 : stop);
+    }
+  }
+  x.finish();
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int row = row0 + 16 * (RT * wave + r) + n;
+    if (row >= rows) continue;
+    float f;
+    float* dst = row_out(p, s, hk, row, D, x.m[r], x.l[r], g4 == 0, f);
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+      *reinterpret_cast<f32x4*>(dst + 16 * c + 4 * g4) = x.acc[r][c] * f;
   }
 }
 
@@ -488,7 +727,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs p,
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      if (i + u >= s.n || ms[u] == -INFINITY) continue;
+      if (i + u >= s.n || (ms[u] == -INFINITY && ls[u] == 0.f)) continue;
       const float w = __builtin_amdgcn_exp2f(ms[u] - m);
       l = __builtin_fmaf(w, ls[u], l);
 #pragma unroll
@@ -579,31 +818,28 @@ static KvArgs kv_args(const gdn_kv_dims& d, const void* k, const void* v,
   return a;
 }
 
-// How a call is spread: rows of q per workgroup, row groups, splits.  About
-// kTarget workgroups in all (four per CU, what its registers and LDS hold),
-// few rows leaving more of them to the positions.
+// How a call is spread: few rows of q (attend_kernel) or many in groups of
+// 64 rt (rows_kernel), and the splits.  About kTarget workgroups in all, two
+// rounds of what the CUs hold.
 constexpr int kTarget = 1024;
 
 struct Shape {
-  int rows, rt, wr, groups, target, slots;
+  int rows, rt, groups, target, slots;
+  bool few;
 };
-// f32 rows of 256 leave LDS for the tiles of one row block only; that means
-// more row groups and at most as many slots, so the bf16 shape's workspace
-// does for both.
-static Shape shape_of(const gdn_kv_dims& d, bool f32) {
+static Shape shape_of(const gdn_kv_dims& d) {
   Shape s;
   s.rows = d.t_max * (d.h_q / d.h_kv);
-  s.rt = s.rows > 16 && d.d < 256 ? 2 : 1;
-  const int tiles = (s.rows + 16 * s.rt - 1) / (16 * s.rt);
-  s.wr = f32 && d.d == 256 ? 1 : tiles > 2 ? 4 : tiles;
-  s.groups = (tiles + s.wr - 1) / s.wr;
+  s.few = s.rows <= (d.d < 256 ? 32 : 16);
+  s.rt = d.d < 256 && s.rows > (s.few ? 16 : 64) ? 2 : 1;
+  s.groups = s.few ? 1 : (s.rows + 64 * s.rt - 1) / (64 * s.rt);
   s.target = kTarget / (d.h_kv * s.groups);
   if (s.target < 1) s.target = 1;
   s.slots = 2 * s.target;
   return s;
 }
 static size_t attend_bytes(const gdn_kv_dims& d) {
-  const Shape s = shape_of(d, false);
+  const Shape s = shape_of(d);
   const size_t n = (size_t)s.slots * d.h_kv * s.rows;
   return n * (d.d + 2) * sizeof(float);
 }
@@ -614,23 +850,18 @@ static hipError_t attend(const gdn_kv_dims& d, const Shape& s,
                          hipStream_t st) {
   const dim3 grid(
       (unsigned)((long)(s.target + d.n_lanes) * d.h_kv * s.groups));
-  auto go = [&](auto rt, auto wr) {
-    return launch(attend_kernel<D, T, decltype(rt)::value, decltype(wr)::value>,
-                  grid, dim3(256), st, p, tl);
-  };
-  auto of_wr = [&](auto rt) {
-    if (s.wr == 1) return go(rt, std::integral_constant<int, 1>{});
-    if (s.wr == 2) return go(rt, std::integral_constant<int, 2>{});
-    return go(rt, std::integral_constant<int, 4>{});
-  };
-  hipError_t e = hipSuccess;
-  if constexpr (D < 256)
-    e = s.rt == 2 ? of_wr(std::integral_constant<int, 2>{})
-                  : of_wr(std::integral_constant<int, 1>{});
-  else if constexpr (sizeof(T) == 4)
-    e = go(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-  else
-    e = of_wr(std::integral_constant<int, 1>{});
+  hipError_t e;
+  if constexpr (D < 256) {
+    if (s.few)
+      e = s.rt == 2 ? launch(attend_kernel<D, T, 2>, grid, dim3(256), st, p, tl)
+                    : launch(attend_kernel<D, T, 1>, grid, dim3(256), st, p, tl);
+    else
+      e = s.rt == 2 ? launch(rows_kernel<D, T, 2>, grid, dim3(256), st, p, tl)
+                    : launch(rows_kernel<D, T, 1>, grid, dim3(256), st, p, tl);
+  } else {
+    e = s.few ? launch(attend_kernel<D, T, 1>, grid, dim3(256), st, p, tl)
+              : launch(rows_kernel<D, T, 1>, grid, dim3(256), st, p, tl);
+  }
   // a cache of one unit per lane has nothing to join
   if (e != hipSuccess || (long)d.max_pages * d.page_size <= kUnit) return e;
   const long rows = (long)d.n_lanes * d.h_kv * s.rows;
@@ -684,7 +915,7 @@ extern "C" int gdn_paged_attention(const gdn_kv_dims* dims,
   rc = check_lanes(fn, *dims, t_lane, tl, any);
   if (rc != GDN_OK) return rc;
   if (!any) return GDN_OK;
-  const Shape s = shape_of(*dims, dtype == GDN_F32);
+  const Shape s = shape_of(*dims);
   AttendArgs p;
   p.kv = kv_args(*dims, k_cache, v_cache, page_table, kv_len);
   p.q = q;

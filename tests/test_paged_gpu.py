@@ -124,6 +124,36 @@ def test_bad_page_numbers_are_masked():
     assert (o[1, :3] == 0).all()
 
 
+@pytest.mark.parametrize("T,h_q,d,kind", [(4, 4, 128, "bf16"), (16, 16, 128, "bf16"),
+                                          (3, 2, 64, "f32"), (40, 2, 256, "bf16")])
+def test_later_tokens_of_a_window_do_not_matter(T, h_q, d, kind):
+    """A draft token's key and value rows hold infinities and NaN: the tokens
+    before it are as if they did not, it and the ones after it see them."""
+    bad = T // 2
+    x = _case([T, 1], [300, 77], h_q, 2, d, 16, kind)
+    pos = 300 - T + bad
+    page, row = int(x["table"][0, pos // 16]), pos % 16
+    clean = _run(x, [T, 1], 0.1)
+    x["v"][page, 0, row, ::3] = math.inf
+    x["v"][page, 0, row, 1::3] = math.nan
+    x["k"][page, 1, row] = math.nan
+    o = _run(x, [T, 1], 0.1)
+    assert torch.equal(o[0, :bad], clean[0, :bad]) and torch.equal(o[1], clean[1])
+    first, second = o[0, bad:, :h_q // 2], o[0, bad:, h_q // 2:]
+    assert (first[..., ::3] == math.inf).all()
+    assert torch.isnan(first[..., 1::3]).all()
+    assert torch.equal(first[..., 2::3], clean[0, bad:, :h_q // 2][..., 2::3])
+    assert torch.isnan(second).all()
+
+
+def test_nan_in_the_cache_reaches_the_rows_that_see_it():
+    x = _case([1, 2], [3000, 77], 4, 2, 128, 16, "bf16")
+    x["k"][int(x["table"][0, 3]), 0, 5] = math.nan
+    o = _run(x, [1, 2], 0.1)
+    assert torch.isnan(o[0, 0, :2]).all() and torch.isfinite(o[0, 0, 2:]).all()
+    assert torch.isfinite(o[1]).all()
+
+
 def test_shared_pages():
     """Two lanes with a common prefix, and a page twice in one lane."""
     x = _case([1, 1], [64, 64], 4, 2, 128, 16, "bf16")
