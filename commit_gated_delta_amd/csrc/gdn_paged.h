@@ -58,9 +58,10 @@ __device__ __forceinline__ long row_of(const KvArgs& a, int n, int h, int pos,
 // A lane's positions are taken in units of kUnit, and the units of all lanes
 // are shared out in splits of equally many, about `target` of them, whatever
 // the lengths (which only the device knows).  Splits are numbered lane by
-// lane; the grid holds the most there can be, target + lanes, and those past
-// the last one end at once.  Partial results of lanes with more than one
-// split have a slot each, at most 2 * target of them.
+// lane; the grid holds the most there can be, target + lanes (each lane's
+// last split may be a short one), and those past the last one end at once.
+// Partial results of lanes with more than one split have a slot each, at most
+// 2 * target of them.
 constexpr int kUnit = 128;
 
 struct Split {
@@ -819,12 +820,18 @@ static KvArgs kv_args(const gdn_kv_dims& d, const void* k, const void* v,
 }
 
 // How a call is spread: few rows of q (attend_kernel) or many in groups of
-// 64 rt (rows_kernel), and the splits.  About kTarget workgroups in all, two
-// rounds of what the CUs hold.
-constexpr int kTarget = 1024;
+// 64 rt (rows_kernel), and the splits: kFewBlocks and kRowsBlocks workgroups
+// in all, short last splits included, and no more than the page tables have
+// units.  Measured, for 32 lanes x 8 heads x 16k..32k positions, one token:
+// 780, 618, 588, 584 us with 512, 1024, 1536, 2048 workgroups (more of them
+// even out the memory's latency); for 8 lanes x 4 heads x 8k..16k, 128 rows:
+// 121, 93, 117, 110 us with 256, 512, 768, 1024 (two a CU run at once, and
+// every split of 128 rows leaves 64 KiB to join).
+constexpr int kFewBlocks = 2048;
+constexpr int kRowsBlocks = 512;
 
 struct Shape {
-  int rows, rt, groups, target, slots;
+  int rows, rt, groups, target, items, slots;
   bool few;
 };
 static Shape shape_of(const gdn_kv_dims& d) {
@@ -833,9 +840,13 @@ static Shape shape_of(const gdn_kv_dims& d) {
   s.few = s.rows <= (d.d < 256 ? 32 : 16);
   s.rt = d.d < 256 && s.rows > (s.few ? 16 : 64) ? 2 : 1;
   s.groups = s.few ? 1 : (s.rows + 64 * s.rt - 1) / (64 * s.rt);
-  s.target = kTarget / (d.h_kv * s.groups);
+  const int items = (s.few ? kFewBlocks : kRowsBlocks) / (d.h_kv * s.groups);
+  s.target = items - d.n_lanes > items / 2 ? items - d.n_lanes : items / 2;
   if (s.target < 1) s.target = 1;
-  s.slots = 2 * s.target;
+  const long units = ((long)d.max_pages * d.page_size + kUnit - 1) / kUnit;
+  const long most = units * d.n_lanes;
+  s.items = s.target + d.n_lanes < most ? s.target + d.n_lanes : (int)most;
+  s.slots = 2l * s.target < most ? 2 * s.target : (int)most;
   return s;
 }
 static size_t attend_bytes(const gdn_kv_dims& d) {
@@ -848,8 +859,7 @@ template <int D, typename T>
 static hipError_t attend(const gdn_kv_dims& d, const Shape& s,
                          const AttendArgs& p, const gdn::LaneTable& tl,
                          hipStream_t st) {
-  const dim3 grid(
-      (unsigned)((long)(s.target + d.n_lanes) * d.h_kv * s.groups));
+  const dim3 grid((unsigned)((long)s.items * d.h_kv * s.groups));
   hipError_t e;
   if constexpr (D < 256) {
     if (s.few)
