@@ -295,20 +295,32 @@ struct Gates {
   float all;             // exp(B)
 };
 
-__device__ __forceinline__ double set_gates(Gates& G, float g, int lane) {
-  g = g < -1000.f ? -1000.f : g;
-  const double b = wave_scan((double)g * kLog2e);
-  const long bits = __builtin_bit_cast(long, b);
-  const double B = __builtin_bit_cast(
-      double, ((long)__builtin_amdgcn_readlane((int)(bits >> 32), 63) << 32) |
-                  (uint32_t)__builtin_amdgcn_readlane((int)bits, 63));
-  const float hi = (float)b;
-  G.b[lane] = make_float2(hi, (float)(b - (double)hi));
-  G.in[lane] = __builtin_amdgcn_exp2f((float)b);
-  G.out[lane] = __builtin_amdgcn_exp2f((float)(B - b));
-  if (lane == 0) G.all = __builtin_amdgcn_exp2f((float)B);
-  return B;
-}
+// The same of lane's token, before they go to LDS.
+struct GateRegs {
+  float hi, lo, in, out, all;
+  // From the token's gate; the whole sum.
+  __device__ __forceinline__ double make(float g) {
+    g = g < -1000.f ? -1000.f : g;
+    const double b = wave_scan((double)g * kLog2e);
+    const long bits = __builtin_bit_cast(long, b);
+    const double B = __builtin_bit_cast(
+        double,
+        ((long)__builtin_amdgcn_readlane((int)(bits >> 32), 63) << 32) |
+            (uint32_t)__builtin_amdgcn_readlane((int)bits, 63));
+    hi = (float)b;
+    lo = (float)(b - (double)hi);
+    in = __builtin_amdgcn_exp2f(hi);
+    out = __builtin_amdgcn_exp2f((float)(B - b));
+    all = __builtin_amdgcn_exp2f((float)B);
+    return B;
+  }
+  __device__ __forceinline__ void store(Gates& G, int lane) const {
+    G.b[lane] = make_float2(hi, lo);
+    G.in[lane] = in;
+    G.out[lane] = out;
+    if (lane == 0) G.all = all;
+  }
+};
 
 // 64 token rows of W entries of a tensor in transit from memory to LDS: each
 // thread holds pieces of 16 bytes, kRows rows apart at one column.  The loads
@@ -380,9 +392,21 @@ struct Transit {
   }
 };
 
-// What a chunk kernel is for: the states of segments from zero (kLocal), or
-// outputs and final states from the segments' start states (kOutput).
-enum { kLocal = 0, kOutput = 1 };
+// What a chunk kernel is for: states alone (of all segments but the last of
+// each sequence from zero, or with last_only of the last ones from their
+// start states), or outputs and final states of all segments.
+enum { kStates = 0, kOutput = 1 };
+
+// Asks the scheduler to issue the region's matrix instructions one by one
+// with V vector instructions after each, which run while it does.
+template <int M, int V>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
+  }
+}
 
 // P^T in operand form: fragment (j, x) holds the token columns 16 j .. and
 // the token rows 32 x .. 32 x + 31 (x <= j / 2), in this order; wave w makes
@@ -391,7 +415,6 @@ constexpr int kFrags = 6;
 constexpr int kFragJ[kFrags] = {0, 1, 2, 2, 3, 3};
 constexpr int kFragX[kFrags] = {0, 0, 0, 1, 0, 1};
 constexpr int kOwn[5] = {0, 2, 4, 5, 6};
-constexpr int frag_of(int j, int x) { return j < 2 ? j : 2 * j - 2 + x; }
 
 template <int DK, int CW, typename TIn, int MODE, bool VEC>
 __global__ __launch_bounds__(256, sizeof(TIn) == 2 ? 2 : 1)
@@ -404,11 +427,14 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
   typedef Transit<TIn, W, VEC> VT;
   typedef typename KT::Tile KL;
   typedef typename VT::Tile VL;
-  __shared__ __attribute__((aligned(16))) TIn Ks[kChunk * KL::kPitch];
+  // (states alone leave room for a second set of tiles: the next chunk is
+  // placed while this one is read, with one barrier per chunk)
+  constexpr int kSets = MODE == kStates && sizeof(TIn) == 2 ? 2 : 1;
+  __shared__ __attribute__((aligned(16))) TIn Kset[kSets][kChunk * KL::kPitch];
   __shared__ __attribute__((aligned(16))) TIn Qs[MODE == kOutput ? kChunk * KL::kPitch : 8];
-  __shared__ __attribute__((aligned(16))) TIn Vs[kChunk * VL::kPitch];
+  __shared__ __attribute__((aligned(16))) TIn Vset[kSets][kChunk * VL::kPitch];
   __shared__ u32x4 Ps[MODE == kOutput ? kFrags : 1][O::kParts][64];
-  __shared__ __attribute__((aligned(16))) Gates G;
+  __shared__ __attribute__((aligned(16))) Gates Gset[kSets];
 
   const DecayArgs& a = p.a;
   const int ncb = (a.d_v + W - 1) / W;
@@ -417,13 +443,11 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
   item /= ncb;
   const int h = item % a.h_v;
   item /= a.h_v;
-  // the segment: all of them, or (last_only) the last of each sequence, or
-  // (kLocal) all but the last of each sequence
   int s, seg;
   if (last_only) {
     s = item;
     seg = tab.first[s + 1] - 1;
-  } else if (MODE == kLocal) {
+  } else if (MODE == kStates) {
     int lo = 0, hi = tab.n - 1;  // first[s] - s segments lie before sequence s
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
@@ -453,13 +477,12 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
   const TIn* V = (const TIn*)a.v + tok0 * vs + (long)h * a.d_v + col;
   const float* __restrict__ g = a.per_head ? a.g + h : a.g + tok0 * a.h_v + h;
   const long gs = a.per_head ? 0 : a.h_v;
-  float* out =
-      MODE == kOutput && a.o ? a.o + tok0 * vs + (long)h * a.d_v + col : nullptr;
+  float* out = MODE == kOutput ? a.o + tok0 * vs + (long)h * a.d_v + col : nullptr;
 
   // state entry (32 ks + 8 g4 + 4 a + e, column 16 ct + n): st[ct][ks][a][e]
   f32x4 st[CT][KS][2];
   const float* from = nullptr;
-  if constexpr (MODE == kOutput) {
+  if (MODE == kOutput || last_only) {
     if (n_seg > 1 && (nth > 0 || a.s_in))
       from = p.slots + ((long)seg * a.h_v + h) * p.d_k * a.d_v;
     else if (n_seg == 1 && a.s_in)
@@ -494,34 +517,42 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
   vt.init(vs, cols);
   float gate = 0.f;
   double total = 0.0;
+  GateRegs next_gates;
   auto fetch = [&](int t0) {
     const int rows = T - t0;
     kt.load(K + t0 * ks, ks, rows);
-    if constexpr (MODE == kOutput) {
-      if (out) qt.load(Q + t0 * ks, ks, rows);
-    }
     vt.load(V + t0 * vs, vs, rows);
     gate = lane < rows ? g[(t0 + lane) * gs] : 0.f;
   };
-  auto place = [&]() {
-    kt.store(Ks);
-    if constexpr (MODE == kOutput) {
-      if (out) qt.store(Qs);
-    }
-    vt.store(Vs);
-    if (wave == 0) total += set_gates(G, gate, lane);
+  auto fetch_q = [&](int t0) {
+    if constexpr (MODE == kOutput) qt.load(Q + t0 * ks, ks, T - t0);
+  };
+  auto place = [&](int set) {
+    kt.store(Kset[set]);
+    if constexpr (MODE == kOutput) qt.store(Qs);
+    vt.store(Vset[set]);
+    if (wave == 0) next_gates.store(Gset[set], lane);
   };
 
   if (T > 0) {
     fetch(0);
-    place();
+    fetch_q(0);
+    total += next_gates.make(gate);
+    place(0);
   }
+  int set = 0;
   for (int t0 = 0; t0 < T; t0 += kChunk) {
     __syncthreads();
     const bool more = t0 + kChunk < T;
+    const TIn *Ks = Kset[set], *Vs = Vset[set];
+    const Gates& G = Gset[set];
+    // the next chunk's K and V rows now; Q's when the state's operands have
+    // left the registers
+    gate = 0.f;
     if (more) fetch(t0 + kChunk);
     f32x4 acc[CT][4];
-    if (out) {
+    const float all = G.all;
+    if constexpr (MODE == kOutput) {
       // this wave's fragments of P^T
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
@@ -559,25 +590,41 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
           for (int i = 0; i < O::kParts; ++i) Ps[f][i][lane] = pw.part[i];
         }
       }
-      // O^T of the state: tokens 16 j + n, columns 16 ct + 4 g4 + e
+      // O^T of the state: tokens 16 j + n, columns 16 ct + 4 g4 + e.  The
+      // operands of a step of 32 state rows are made while the one before is
+      // multiplied, and a state row is decayed as soon as it has been read.
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[ct][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      Wide sw[2][CT];
+      Raw qf[2][4];
+      auto state_operands = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          qf[i & 1][j] = O::template row<KL>(Qs, 16 * j, n, 4 * i + g4);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          sw[i & 1][ct] = O::wide(st[ct][i][0], st[ct][i][1]);
+          st[ct][i][0] *= all;
+          st[ct][i][1] *= all;
+        }
+      };
+      state_operands(0);
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
-        Wide sw[CT];
+        __builtin_amdgcn_sched_barrier(0);
+        if (i + 1 < KS) state_operands(i + 1);
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          sw[ct] = O::wide(st[ct][i][0], st[ct][i][1]);
+        for (int m = 0; m < O::kSteps; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const Raw qf = O::template row<KL>(Qs, 16 * j, n, 4 * i + g4);
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
-            acc[ct][j] = O::mul(sw[ct], qf, acc[ct][j]);
-        }
+            for (int ct = 0; ct < CT; ++ct)
+              acc[ct][j] = O::step(m, sw[i & 1][ct], qf[i & 1][j], acc[ct][j]);
+        interleave<12 * CT, 4>();
       }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float in = G.in[16 * j + n];
@@ -585,7 +632,15 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
         for (int ct = 0; ct < CT; ++ct) acc[ct][j] *= in;
       }
       __syncthreads();  // P^T is complete
+    } else {
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) st[ct][i][x] *= all;
     }
+    if (more) fetch_q(t0 + kChunk);
     Raw vf[2][CT];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
@@ -593,21 +648,27 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
       for (int ct = 0; ct < CT; ++ct)
         vf[x][ct] =
             O::template column<VL>(Vs, 32 * x, wcol + 16 * ct, 4, lane);
-    if (out) {
+    if constexpr (MODE == kOutput) {
+      Wide pw[2];
+      auto p_operand = [&](int f) {
+#pragma unroll
+        for (int i = 0; i < O::kParts; ++i) pw[f & 1].part[i] = Ps[f][i][lane];
+      };
+      p_operand(0);
+#pragma unroll
+      for (int f = 0; f < kFrags; ++f) {
+        if (f + 1 < kFrags) p_operand(f + 1);
+#pragma unroll
+        for (int m = 0; m < O::kSteps; ++m)
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct)
+            acc[ct][kFragJ[f]] = O::step(m, vf[kFragX[f]][ct], pw[f & 1],
+                                         acc[ct][kFragJ[f]]);
+      }
       int bytes =
           (int)(((T - t0 < kChunk ? T - t0 : kChunk) - 1) * vs + cols) * 4;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-#pragma unroll
-        for (int x = 0; x <= j / 2; ++x) {
-          Wide pw;
-#pragma unroll
-          for (int i = 0; i < O::kParts; ++i)
-            pw.part[i] = Ps[frag_of(j, x)][i][lane];
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
-            acc[ct][j] = O::mul(vf[x][ct], pw, acc[ct][j]);
-        }
         // rows past the last one fall behind the resource's end
         const auto rs = buffer_of(out + (t0 + 16 * j) * vs, bytes > 0 ? bytes : 0);
         bytes -= (int)(16 * vs * 4);
@@ -628,39 +689,49 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
         }
       }
     }
-    // the state after the chunk
-    const float all = G.all;
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-      for (int i = 0; i < KS; ++i)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) st[ct][i][x] *= all;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    // the writes of the chunk's tokens
+    Wide ww[2][CT];
+    Raw kf[2][2];
+    auto write_operands = [&](int x) {
       const f32x4 w0 = *reinterpret_cast<const f32x4*>(&G.out[32 * x + 4 * g4]);
       const f32x4 w1 =
           *reinterpret_cast<const f32x4*>(&G.out[32 * x + 16 + 4 * g4]);
-      Wide ww[CT];
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) ww[ct] = O::scaled(vf[x][ct], w0, w1);
+      for (int ct = 0; ct < CT; ++ct)
+        ww[x][ct] = O::scaled(vf[x][ct], w0, w1);
+    };
+    auto key_operands = [&](int u) {  // u = 32-token step x, 32 state rows i
 #pragma unroll
-      for (int i = 0; i < KS; ++i)
+      for (int y = 0; y < 2; ++y)
+        kf[u & 1][y] = O::template column<KL>(Ks, 32 * (u / KS),
+                                              32 * (u % KS) + 4 * y, 8, lane);
+    };
+    key_operands(0);
+    write_operands(0);
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const Raw kf =
-              O::template column<KL>(Ks, 32 * x, 32 * i + 4 * y, 8, lane);
+    for (int u = 0; u < 2 * KS; ++u) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (u + 1 < 2 * KS) key_operands(u + 1);
+      if (u == KS - 1) write_operands(1);
+      if (u == KS) total += next_gates.make(gate);
+#pragma unroll
+      for (int m = 0; m < O::kSteps; ++m)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct)
-            st[ct][i][y] = O::mul(kf, ww[ct], st[ct][i][y]);
-        }
+            st[ct][u % KS][y] = O::step(m, kf[u & 1][y], ww[u / KS][ct],
+                                        st[ct][u % KS][y]);
+      if (u == KS - 1 || u == KS) interleave<6 * CT, 10>();
     }
-    __syncthreads();
-    if (more) place();
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kSets == 2) set ^= 1;
+    else __syncthreads();
+    if (more) place(set);
   }
 
   float* to = nullptr;
-  if constexpr (MODE == kLocal) {
+  if (MODE == kStates && !last_only) {
     to = p.slots + ((long)(seg + 1) * a.h_v + h) * p.d_k * a.d_v;
     if (tid == 0 && cb == 0)
       p.decay[(long)seg * a.h_v + h] = __builtin_amdgcn_exp2f((float)total);
@@ -963,7 +1034,7 @@ extern "C" int gdn_decay_prefill(int32_t n_seqs, const int32_t* seq_len,
     p.slots = (float*)workspace;
     p.decay = (float*)((char*)workspace +
                        (slots_bytes(tab, h_v, d_k, d_v) + 255) / 256 * 256);
-    e = launch_chunks<kLocal>(d_k, d_v, in_dtype, vec,
+    e = launch_chunks<kStates>(d_k, d_v, in_dtype, vec,
                               (long)(segs - n_seqs) * h_v, st, p, tab, 0);
     if (e == hipSuccess)
       e = launch(segment_scan_kernel,
@@ -972,9 +1043,11 @@ extern "C" int gdn_decay_prefill(int32_t n_seqs, const int32_t* seq_len,
                  dim3(256), st, p, tab);
   }
   // without outputs only the last segments are left to run
-  if (e == hipSuccess)
-    e = launch_chunks<kOutput>(d_k, d_v, in_dtype, vec,
-                               (long)(o ? segs : n_seqs) * h_v, st, p, tab,
-                               o ? 0 : 1);
+  if (e == hipSuccess && o)
+    e = launch_chunks<kOutput>(d_k, d_v, in_dtype, vec, (long)segs * h_v, st,
+                               p, tab, 0);
+  else if (e == hipSuccess)
+    e = launch_chunks<kStates>(d_k, d_v, in_dtype, vec, (long)n_seqs * h_v, st,
+                               p, tab, 1);
   return gdn::hip_status(e, "gdn_decay_prefill launch");
 }
