@@ -534,24 +534,34 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
     if (wave == 0) next_gates.store(Gset[set], lane);
   };
 
+  // A segment's own state is summed from its last chunk to its first, each
+  // chunk's writes decayed by the chunks summed before it: so the rows read
+  // last, which the cache still holds, are those the output pass starts with.
+  // (Such segments are whole chunks.)
+  const bool back = MODE == kStates && !last_only;
+  const int t_step = back ? -kChunk : kChunk;
+  int t0 = back ? T - kChunk : 0;
+  double sum = 0.0;  // of the chunk's gates
   if (T > 0) {
-    fetch(0);
-    fetch_q(0);
-    total += next_gates.make(gate);
+    fetch(t0);
+    fetch_q(t0);
+    sum = next_gates.make(gate);
     place(0);
   }
   int set = 0;
-  for (int t0 = 0; t0 < T; t0 += kChunk) {
+  for (int left = (T + kChunk - 1) / kChunk; left > 0; --left, t0 += t_step) {
     __syncthreads();
-    const bool more = t0 + kChunk < T;
+    const bool more = left > 1;
+    const float since = back ? __builtin_amdgcn_exp2f((float)total) : 1.f;
+    total += sum;
     const TIn *Ks = Kset[set], *Vs = Vset[set];
     const Gates& G = Gset[set];
     // the next chunk's K and V rows now; Q's when the state's operands have
     // left the registers
     gate = 0.f;
-    if (more) fetch(t0 + kChunk);
+    if (more) fetch(t0 + t_step);
     f32x4 acc[CT][4];
-    const float all = G.all;
+    const float all = back ? 1.f : G.all;
     if constexpr (MODE == kOutput) {
       // this wave's fragments of P^T
 #pragma unroll
@@ -698,7 +708,8 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
           *reinterpret_cast<const f32x4*>(&G.out[32 * x + 16 + 4 * g4]);
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
-        ww[x][ct] = O::scaled(vf[x][ct], w0, w1);
+        ww[x][ct] = MODE == kStates ? O::scaled(vf[x][ct], w0 * since, w1 * since)
+                                    : O::scaled(vf[x][ct], w0, w1);
     };
     auto key_operands = [&](int u) {  // u = 32-token step x, 32 state rows i
 #pragma unroll
@@ -713,7 +724,7 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
       __builtin_amdgcn_sched_barrier(0);
       if (u + 1 < 2 * KS) key_operands(u + 1);
       if (u == KS - 1) write_operands(1);
-      if (u == KS) total += next_gates.make(gate);
+      if (u == KS) sum = next_gates.make(gate);
 #pragma unroll
       for (int m = 0; m < O::kSteps; ++m)
 #pragma unroll
