@@ -20,6 +20,7 @@ using gdn::misaligned;
 
 using gdn::op::f32x4;
 using gdn::op::Op;
+using gdn::op::Special;
 using gdn::op::u32x4;
 
 struct DecayArgs {
@@ -128,6 +129,24 @@ __device__ __forceinline__ void store_cols(float* __restrict__ row, int c,
   }
 }
 
+// Sums over the eight row groups (lane bits 3, 4, 5) of four columns: lane
+// halves and quarters trade places, so that each step adds half as many
+// values and a lane ends up with column 2 * bit 4 + bit 5 of its four.
+__device__ __forceinline__ float sum_groups(f32x4 y) {
+  auto fold32 = [](float a, float b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(
+        __float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  };
+  const float a = fold32(y[0], y[1]), b = fold32(y[2], y[3]);
+  const auto r = __builtin_amdgcn_permlane16_swap(
+      __float_as_uint(a), __float_as_uint(b), false, false);
+  const float x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  // rotate the 16 lanes by eight
+  return x + __int_as_float(__builtin_amdgcn_update_dpp(
+                 0, __float_as_int(x), 0x128, 0xf, 0xf, false));
+}
+
 // One head's chain over T tokens.  Pointers are at the first token's row of
 // the head; qs, vs, gs are the token strides.
 template <int DK, typename TIn, bool V4>
@@ -161,14 +180,9 @@ __device__ __forceinline__ void decay_chain(
       for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(qq[i], st[i][e], y[e]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[e] += __shfl_xor(y[e], 8);
-        y[e] += __shfl_xor(y[e], 16);
-        y[e] += __shfl_xor(y[e], 32);
-        y[e] *= scale;
-      }
-      if (lane < 8) store_cols<V4>(o + t * vs, c, dv, y);
+      const float x = sum_groups(y) * scale;
+      const int col = col0 + 4 * (lane & 7) + 2 * (lane >> 4 & 1) + (lane >> 5);
+      if (!(lane & 8) && col < dv) o[t * vs + col] = x;
     }
   }
   if (s_out) {
@@ -415,6 +429,7 @@ constexpr int kFrags = 6;
 constexpr int kFragJ[kFrags] = {0, 1, 2, 2, 3, 3};
 constexpr int kFragX[kFrags] = {0, 0, 0, 1, 0, 1};
 constexpr int kOwn[5] = {0, 2, 4, 5, 6};
+__device__ constexpr int frag_of(int j, int x) { return j < 2 ? j : 2 * j - 2 + x; }
 
 template <int DK, int CW, typename TIn, int MODE, bool VEC>
 __global__ __launch_bounds__(256, sizeof(TIn) == 2 ? 2 : 1)
@@ -435,6 +450,7 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
   __shared__ __attribute__((aligned(16))) TIn Vset[kSets][kChunk * VL::kPitch];
   __shared__ u32x4 Ps[MODE == kOutput ? kFrags : 1][O::kParts][64];
   __shared__ __attribute__((aligned(16))) Gates Gset[kSets];
+  __shared__ int odd_chunk[2];  // whether a chunk's V holds special values
 
   const DecayArgs& a = p.a;
   const int ncb = (a.d_v + W - 1) / W;
@@ -527,7 +543,13 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
   auto fetch_q = [&](int t0) {
     if constexpr (MODE == kOutput) qt.load(Q + t0 * ks, ks, T - t0);
   };
-  auto place = [&](int set) {
+  auto place = [&](int set, int left) {
+    if constexpr (MODE == kOutput) {
+      Special<TIn> odd;
+#pragma unroll
+      for (int i = 0; i < VT::kPieces; ++i) odd.look(vt.r[i]);
+      if (odd.any()) odd_chunk[left & 1] = 1;
+    }
     kt.store(Kset[set]);
     if constexpr (MODE == kOutput) qt.store(Qs);
     vt.store(Vset[set]);
@@ -546,11 +568,16 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
     fetch(t0);
     fetch_q(t0);
     sum = next_gates.make(gate);
-    place(0);
   }
-  int set = 0;
-  for (int left = (T + kChunk - 1) / kChunk; left > 0; --left, t0 += t_step) {
+  int set = 0, left = (T + kChunk - 1) / kChunk;  // chunks left
+  if constexpr (MODE == kOutput) {
+    if (tid == 0) odd_chunk[left & 1] = 0;
     __syncthreads();
+  }
+  if (T > 0) place(0, left);
+  for (; left > 0; --left, t0 += t_step) {
+    __syncthreads();
+    if (MODE == kOutput && tid == 0) odd_chunk[~left & 1] = 0;
     const bool more = left > 1;
     const float since = back ? __builtin_amdgcn_exp2f((float)total) : 1.f;
     total += sum;
@@ -608,11 +635,7 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[ct][j] = f32x4{0.f, 0.f, 0.f, 0.f};
       Wide sw[2][CT];
-      Raw qf[2][4];
       auto state_operands = [&](int i) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          qf[i & 1][j] = O::template row<KL>(Qs, 16 * j, n, 4 * i + g4);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           sw[i & 1][ct] = O::wide(st[ct][i][0], st[ct][i][1]);
@@ -624,6 +647,10 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
         __builtin_amdgcn_sched_barrier(0);
+        Raw qf[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          qf[j] = O::template row<KL>(Qs, 16 * j, n, 4 * i + g4);
         if (i + 1 < KS) state_operands(i + 1);
 #pragma unroll
         for (int m = 0; m < O::kSteps; ++m)
@@ -631,7 +658,7 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
-              acc[ct][j] = O::step(m, sw[i & 1][ct], qf[i & 1][j], acc[ct][j]);
+              acc[ct][j] = O::step(m, sw[i & 1][ct], qf[j], acc[ct][j]);
         interleave<12 * CT, 4>();
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -652,28 +679,62 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
     }
     if (more) fetch_q(t0 + kChunk);
     Raw vf[2][CT];
+    auto value_operands = [&]() {
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-        vf[x][ct] =
-            O::template column<VL>(Vs, 32 * x, wcol + 16 * ct, 4, lane);
+        for (int ct = 0; ct < CT; ++ct)
+          vf[x][ct] =
+              O::template column<VL>(Vs, 32 * x, wcol + 16 * ct, 4, lane);
+    };
+    if constexpr (MODE == kStates) value_operands();
     if constexpr (MODE == kOutput) {
       Wide pw[2];
       auto p_operand = [&](int f) {
 #pragma unroll
         for (int i = 0; i < O::kParts; ++i) pw[f & 1].part[i] = Ps[f][i][lane];
       };
-      p_operand(0);
+      if (!odd_chunk[left & 1]) {
+        value_operands();
+        p_operand(0);
 #pragma unroll
-      for (int f = 0; f < kFrags; ++f) {
-        if (f + 1 < kFrags) p_operand(f + 1);
+        for (int f = 0; f < kFrags; ++f) {
+          if (f + 1 < kFrags) p_operand(f + 1);
 #pragma unroll
-        for (int m = 0; m < O::kSteps; ++m)
+          for (int m = 0; m < O::kSteps; ++m)
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
-            acc[ct][kFragJ[f]] = O::step(m, vf[kFragX[f]][ct], pw[f & 1],
-                                         acc[ct][kFragJ[f]]);
+            for (int ct = 0; ct < CT; ++ct)
+              acc[ct][kFragJ[f]] = O::step(m, vf[kFragX[f]][ct], pw[f & 1],
+                                           acc[ct][kFragJ[f]]);
+        }
+      } else {
+        // an infinity or a NaN in V must not reach the tokens before its own
+        // (the lane's number passes through an empty asm, or what follows
+        // from it is kept in registers through the whole loop)
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        const int lc = wcol + 4 * (l >> 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll 1
+          for (int sr = 0; sr < 16 * j + 16; ++sr) {
+            if (sr > 16 * j + (l & 15)) continue;
+            u32x4 part[O::kParts];
+#pragma unroll
+            for (int i = 0; i < O::kParts; ++i)
+              part[i] = Ps[frag_of(j, sr >> 5)][i][4 * (sr & 12) + (l & 15)];
+            const float pv = O::slot(part, 4 * (sr >> 4 & 1) + (sr & 3));
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int c = lc + 16 * ct + e;
+                acc[ct][j][e] += pv * gdn::op::value_of(
+                    Vs[VL::at(sr, c / VL::kPer) + c % VL::kPer]);
+              }
+          }
+        }
+        value_operands();
       }
       int bytes =
           (int)(((T - t0 < kChunk ? T - t0 : kChunk) - 1) * vs + cols) * 4;
@@ -738,7 +799,7 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (kSets == 2) set ^= 1;
     else __syncthreads();
-    if (more) place(set);
+    if (more) place(set, left - 1);
   }
 
   float* to = nullptr;
@@ -827,10 +888,12 @@ static int check_heads(const char* fn, int h_v, int h_k, int d_k, int d_v) {
   return GDN_OK;
 }
 
-static int check_pointers(const char* fn, const DecayArgs& p, int in_dtype) {
+// (a call without tokens reads no inputs)
+static int check_pointers(const char* fn, const DecayArgs& p, int in_dtype,
+                          bool tokens) {
   char msg[128];
   const char* what = nullptr;
-  if (!p.k || !p.v || !p.g || (p.o && !p.q)) what = "required pointer is NULL";
+  if (tokens && (!p.k || !p.v || !p.g || (p.o && !p.q))) what = "required pointer is NULL";
   else if (in_dtype != GDN_BF16 && in_dtype != GDN_F32) what = "unknown in_dtype";
   else if (misaligned(p.q, 16) || misaligned(p.k, 16) || misaligned(p.v, 16) ||
            misaligned(p.g, 16) || misaligned(p.s_in, 16) ||
@@ -968,7 +1031,7 @@ extern "C" int gdn_decay_step(const gdn_dims* dims, const int32_t* t_lane,
   DecayArgs p = {q, k, v, g, S, keep ? nullptr : S, o, scale, d.n_layers,
                  d.n_lanes, d.h_v, d.h_k, d.d_v, d.t_max,
                  (flags & GDN_FLAG_HEAD_DECAY) ? 1 : 0};
-  rc = check_pointers(fn, p, in_dtype);
+  rc = check_pointers(fn, p, in_dtype, true);
   if (rc != GDN_OK) return rc;
   gdn::LaneTable tl;
   memset(&tl, 0, sizeof(tl));
@@ -1030,7 +1093,7 @@ extern "C" int gdn_decay_prefill(int32_t n_seqs, const int32_t* seq_len,
   ChunkArgs p = {{q, k, v, g, S_init, S_final, o, scale, 1, n_seqs, h_v, h_k,
                   d_v, 0, (flags & GDN_FLAG_HEAD_DECAY) ? 1 : 0},
                  d_k, nullptr, nullptr};
-  rc = check_pointers(fn, p.a, in_dtype);
+  rc = check_pointers(fn, p.a, in_dtype, tokens > 0);
   if (rc != GDN_OK) return rc;
   const size_t need = workspace_bytes(tab, h_v, d_k, d_v);
   if (need > 0 && (!workspace || ws_bytes < need))

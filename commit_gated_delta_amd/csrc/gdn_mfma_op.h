@@ -42,6 +42,40 @@ struct Tile {
   }
 };
 
+// Infinities and NaN among inputs.  A product of the matrix cores takes its
+// masked entries as zeros, and 0 times an infinity or a NaN is a NaN: rows
+// that hold such values are found here and treated apart.
+template <typename TIn>
+struct Special {  // bits that a dword sets when one of its values is special
+  static constexpr uint32_t kExp = sizeof(TIn) == 2 ? 0x7f807f80u : 0x7f800000u;
+  static constexpr uint32_t kOne = sizeof(TIn) == 2 ? 0x00800080u : 0x00800000u;
+  static constexpr uint32_t kHit = sizeof(TIn) == 2 ? 0x80008000u : 0x80000000u;
+  uint32_t seen = 0;
+  __device__ __forceinline__ void look(u32x4 w) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) seen |= (w[e] & kExp) + kOne;
+  }
+  __device__ __forceinline__ bool any() const { return seen & kHit; }
+  // w with special values as zeros.
+  static __device__ __forceinline__ u32x4 cleared(u32x4 w) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (sizeof(TIn) == 2) {
+        if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+        if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu;
+      } else {
+        if ((w[e] & kExp) == kExp) w[e] = 0;
+      }
+    }
+    return w;
+  }
+};
+
+__device__ __forceinline__ float value_of(uint16_t x) {
+  return __uint_as_float((uint32_t)x << 16);
+}
+__device__ __forceinline__ float value_of(float x) { return x; }
+
 // Operand fragments of eight k-slots.  Raw: inputs as they are; Wide: f32
 // values.
 template <typename TIn>
@@ -98,6 +132,17 @@ struct Op<uint16_t> {
       }
     }
     return w;
+  }
+  // Slot i of the value whose parts are given.
+  static __device__ __forceinline__ float slot(const u32x4 (&part)[kParts],
+                                               int i) {
+    float x = 0.f;
+#pragma unroll
+    for (int y = kParts - 1; y >= 0; --y) {
+      const uint32_t w = part[y][i >> 1];
+      x += __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+    }
+    return x;
   }
   // Slots e = 0..7 of a raw fragment as f32, times s.
   static __device__ __forceinline__ Wide scaled(u32x4 a, f32x4 s0, f32x4 s1) {
@@ -163,6 +208,10 @@ struct Op<float> {
   }
   static __device__ __forceinline__ Raw wide(f32x4 x, f32x4 y) {
     return {__builtin_bit_cast(u32x4, x), __builtin_bit_cast(u32x4, y)};
+  }
+  static __device__ __forceinline__ float slot(const u32x4 (&part)[kParts],
+                                               int i) {
+    return __uint_as_float(part[i >> 2][i & 3]);
   }
   static __device__ __forceinline__ Raw scaled(const Raw& a, f32x4 s0,
                                                f32x4 s1) {

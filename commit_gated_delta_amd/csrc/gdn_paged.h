@@ -18,6 +18,7 @@ using gdn::misaligned;
 
 using gdn::op::f32x4;
 using gdn::op::Op;
+using gdn::op::Special;
 using gdn::op::Tile;
 using gdn::op::u32x4;
 
@@ -240,7 +241,7 @@ struct Rows {
     Wide pw[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) pw[r] = O::wide(sc[r][0], sc[r][1]);
-    constexpr int kTwo = CT % 2 == 0 ? 2 : 1;
+    constexpr int kTwo = RT == 1 ? 2 : 1;  // two accumulators at least
 #pragma unroll
     for (int c = 0; c < CT; c += kTwo) {
       Raw vf[kTwo];
@@ -257,15 +258,19 @@ struct Rows {
             acc[r][c + y] = O::step(i, vf[y], pw[r], acc[r][c + y]);
     }
   }
-  // What infinities and NaN in V at positions from .. stop - 1 of a step add
-  // to the rows that see them; `values` took them as zeros, as they have to
-  // count for the rows that do not.  (p is 0 for those, and 0 times NaN is
-  // not.)  Rarely needed and slow.
+  // What infinities and NaN in V at the positions of a step from p0 on add to
+  // the rows that see them; `values` took them as zeros.  Rarely needed and
+  // slow.
   __device__ __forceinline__ void special(const KvArgs& a, int n, int hk,
-                                          int p0, int from, int stop) {
-    const int lane = threadIdx.x & 63, g4 = lane >> 4;
+                                          int p0, int stop) {
+    // (through an empty asm, or what follows from it is kept in registers
+    // through the caller's loop)
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int g4 = lane >> 4;
+    if (stop > p0 + 32) stop = p0 + 32;
 #pragma unroll 1
-    for (int pos = from; pos < stop; ++pos) {
+    for (int pos = p0; pos < stop; ++pos) {
       const long row = row_of(a, n, hk, pos, D);
       if (row < 0) continue;
       const int i = pos - p0;
@@ -275,18 +280,19 @@ struct Rows {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = __shfl(sc[r][h][e], 16 * ((i & 15) >> 2) + (lane & 15));
-            if (h == i >> 4 && e == (i & 3)) p = x;
-          }
-        if (pos >= end[r]) continue;
+          for (int e = 0; e < 4; ++e)
+            if (i == (i & 12) + 16 * h + e)  // (uniform)
+              p = __shfl(sc[r][h][e], 4 * (i & 12) + (lane & 15));
+        const bool sees = pos < end[r];
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
+        for (int c = 0; c < CT; ++c) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float v = elem((const T*)a.v, row + 16 * c + 4 * g4 + e);
-            if (!(fabsf(v) < INFINITY)) acc[r][c][e] += p * v;
+            if (sees && !(fabsf(v) < INFINITY)) acc[r][c][e] += p * v;
           }
+          __builtin_amdgcn_sched_barrier(0);  // few loads at a time
+        }
       }
     }
   }
@@ -298,23 +304,6 @@ struct Rows {
     }
   }
 };
-
-// Whether a dword of V holds an infinity or a NaN, and the dword with those
-// as zeros.
-template <typename T>
-__device__ __forceinline__ bool clear_special(uint32_t& w) {
-  if constexpr (sizeof(T) == 4) {
-    const bool s = (w & 0x7f800000u) == 0x7f800000u;
-    if (s) w = 0;
-    return s;
-  } else {
-    const bool lo = (w & 0x7f80u) == 0x7f80u;
-    const bool hi = (w & 0x7f800000u) == 0x7f800000u;
-    if (lo) w &= 0xffff0000u;
-    if (hi) w &= 0xffffu;
-    return lo || hi;
-  }
-}
 
 // q rows row0 .. row0 + n - 1 of a key-value head (zeros past the last).
 template <int D, typename T>
@@ -360,7 +349,7 @@ __device__ __forceinline__ float* row_out(const AttendArgs& p, const Split& s,
 // step's K rows are loaded when this step's scores are done and its V rows
 // when V is in LDS, page numbers a step earlier.
 template <int D, typename T, int RT>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_kernel(
+__global__ __launch_bounds__(256, D * sizeof(T) >= 512 ? 1 : 2) void attend_kernel(
     AttendArgs p, gdn::LaneTable tl) {
   typedef Rows<D, T, RT> R;
   typedef typename R::O O;
@@ -468,23 +457,31 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_kernel(
            ((uint32_t)__ballot(here[1]) & 0xffffu) << 16;
     x.softmax(p.scale, whole, ok, p0);
     // V through LDS.  Rows that are not there count as zeros.
-    bool odd = false;
     if (!whole) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (!here[h])
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int y = 0; y < kPieces; ++y) vr[h][i][y] = u32x4{0, 0, 0, 0};
+    }
+    Special<T> odd;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int y = 0; y < kPieces; ++y) odd.look(vr[h][i][y]);
+    const bool is_odd = __any(odd.any());
+    if (is_odd) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < KS; ++i)
 #pragma unroll
-          for (int y = 0; y < kPieces; ++y) {
-            if (!here[h]) vr[h][i][y] = u32x4{0, 0, 0, 0};
-            if (pos_of(step, h) >= open)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t w = vr[h][i][y][e];
-                odd |= clear_special<T>(w);
-                vr[h][i][y][e] = w;
-              }
-          }
+          for (int y = 0; y < kPieces; ++y)
+            vr[h][i][y] = Special<T>::cleared(vr[h][i][y]);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -500,9 +497,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_kernel(
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     x.values(Vs, 0);
-    if (__any(odd))
-      x.special(a, s.lane, hk, p0, p0 > open ? p0 : open,
-                p0 + 32 < stop ? p0 + 32 : stop);
+    if (is_odd) x.special(a, s.lane, hk, p0, stop);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -570,6 +565,7 @@ void rows_kernel(AttendArgs p, gdn::LaneTable tl) {
   __shared__ __attribute__((aligned(16))) T Qs[kRows * TL::kPitch];
   __shared__ __attribute__((aligned(16))) T Ks[kTile * TL::kPitch];
   __shared__ __attribute__((aligned(16))) T Vs[kTile * TL::kPitch];
+  __shared__ int odd_tile[2];  // whether a tile's V holds special values
   const KvArgs& a = p.kv;
   const int per_item = a.h_kv * p.groups;
   const Split s = find_split(a, tl, blockIdx.x / per_item, p.target, false);
@@ -623,30 +619,32 @@ void rows_kernel(AttendArgs p, gdn::LaneTable tl) {
   }
   R x;
   x.init(row0 + 16 * RT * wave, rows, s.len, T_n, group);
+  if (tid == 0) odd_tile[0] = 0;
   for (int tile = 0; tile < tiles; ++tile) {
     const int t0 = begin + tile * kTile;
     const uint64_t here = ok;
     const bool whole = t0 + kTile <= (open < stop ? open : stop) && here == ~0ull;
-    bool odd = false;
     __syncthreads();  // the tile before has been read
+    Special<T> odd;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int r = r0 + i * kStep;
-      if (!whole) {
-        if (!(here >> r & 1)) vr[i] = u32x4{0, 0, 0, 0};
-        if (t0 + r >= open)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w = vr[i][e];
-            odd |= clear_special<T>(w);
-            vr[i][e] = w;
-          }
-      }
-      *reinterpret_cast<u32x4*>(Ks + TL::at(r, piece)) = kr[i];
-      *reinterpret_cast<u32x4*>(Vs + TL::at(r, piece)) = vr[i];
+      if (!whole && !(here >> r & 1)) vr[i] = u32x4{0, 0, 0, 0};
+      odd.look(vr[i]);
     }
-    if (whole) __syncthreads();
-    else odd = __syncthreads_or(odd);
+    if (odd.any()) {
+      odd_tile[tile & 1] = 1;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) vr[i] = Special<T>::cleared(vr[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      *reinterpret_cast<u32x4*>(Ks + TL::at(r0 + i * kStep, piece)) = kr[i];
+      *reinterpret_cast<u32x4*>(Vs + TL::at(r0 + i * kStep, piece)) = vr[i];
+    }
+    __syncthreads();
+    const bool is_odd = odd_tile[tile & 1];
+    if (tid == 0) odd_tile[~tile & 1] = 0;
     if (tile + 1 < tiles) {
       place(tile + 1);
       fetch();
@@ -674,9 +672,7 @@ void rows_kernel(AttendArgs p, gdn::LaneTable tl) {
       const int p0 = t0 + 32 * half;
       x.softmax(p.scale, whole, (uint32_t)(here >> (32 * half)), p0);
       x.values(Vs, 32 * half);
-      if (odd)
-        x.special(a, s.lane, hk, p0, p0 > open ? p0 : open,
-                  p0 + 32 < stop ? p0 + 32 : stop);
+      if (is_odd) x.special(a, s.lane, hk, p0, stop);
     }
   }
   x.finish();
@@ -776,7 +772,7 @@ static int check_kv_dims(const char* fn, const gdn_kv_dims* p) {
   if (d.n_lanes < 1 || d.n_lanes > GDN_MAX_LANES || d.t_max < 1 ||
       d.t_max > GDN_MAX_T || d.h_kv < 1 || d.h_q < 1 || d.h_q % d.h_kv != 0 ||
       d.d < 1 || d.page_size < 1 || d.n_pages < 1 || d.max_pages < 1 ||
-      (double)d.max_pages * d.page_size >= (double)(1 << 30) ||
+      (double)d.max_pages * d.page_size >= (double)(1 << 29) ||
       (double)d.n_lanes * d.t_max * d.h_q * 32 > (double)INT_MAX ||
       (double)d.n_lanes * d.h_q * 1024 > (double)INT_MAX ||
       (double)d.n_pages * d.page_size * d.h_kv > 9.0e15) {

@@ -506,7 +506,7 @@ typedef struct {
   int32_t page_size; /* token rows per page, >= 1                          */
   int32_t n_pages;   /* pages in the cache, >= 1                           */
   int32_t max_pages; /* columns of the page table, >= 1;                   */
-                     /* max_pages * page_size < 2^30                       */
+                     /* max_pages * page_size < 2^29                       */
 } gdn_kv_dims;
 
 /*
