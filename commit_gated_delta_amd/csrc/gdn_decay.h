@@ -635,6 +635,14 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[ct][j] = f32x4{0.f, 0.f, 0.f, 0.f};
       Wide sw[2][CT];
+      constexpr int QB = sizeof(TIn) == 4 ? 2 : 1;  // (bf16: no registers left)
+      Raw qf[QB][4];
+      auto query_operands = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          qf[i % QB][j] = O::template row<KL>(Qs, 16 * j, n, 4 * i + g4);
+      };
+      if constexpr (QB == 2) query_operands(0);
       auto state_operands = [&](int i) {
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
@@ -647,10 +655,8 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
         __builtin_amdgcn_sched_barrier(0);
-        Raw qf[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          qf[j] = O::template row<KL>(Qs, 16 * j, n, 4 * i + g4);
+        if constexpr (QB == 1) query_operands(i);
+        else if (i + 1 < KS) query_operands(i + 1);
         if (i + 1 < KS) state_operands(i + 1);
 #pragma unroll
         for (int m = 0; m < O::kSteps; ++m)
@@ -658,7 +664,8 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
-              acc[ct][j] = O::step(m, sw[i & 1][ct], qf[j], acc[ct][j]);
+              acc[ct][j] =
+                  O::step(m, sw[i & 1][ct], qf[i % QB][j], acc[ct][j]);
         interleave<12 * CT, 4>();
       }
       __builtin_amdgcn_sched_barrier(0);

@@ -139,7 +139,9 @@ struct Op<uint16_t> {
     float x = 0.f;
 #pragma unroll
     for (int y = kParts - 1; y >= 0; --y) {
-      const uint32_t w = part[y][i >> 1];
+      uint32_t w = part[y][0];
+#pragma unroll
+      for (int k = 1; k < 4; ++k) w = i >> 1 == k ? part[y][k] : w;
       x += __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
     }
     return x;
@@ -211,7 +213,10 @@ struct Op<float> {
   }
   static __device__ __forceinline__ float slot(const u32x4 (&part)[kParts],
                                                int i) {
-    return __uint_as_float(part[i >> 2][i & 3]);
+    uint32_t w = part[0][0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) w = i == k ? part[k / 4][k % 4] : w;
+    return __uint_as_float(w);
   }
   static __device__ __forceinline__ Raw scaled(const Raw& a, f32x4 s0,
                                                f32x4 s1) {

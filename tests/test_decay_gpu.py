@@ -172,6 +172,43 @@ def test_what_lies_behind_the_tokens_does_not_matter():
     assert (o[n:] == 7).all()
 
 
+@pytest.mark.parametrize("kind,d_k,d_v", [("bf16", 128, 128), ("bf16", 128, 50),
+                                          ("f32", 64, 64)])
+def test_infinities_and_nan_reach_no_earlier_token(kind, d_k, d_v):
+    """What a token's value row holds changes nothing before the token, in its
+    chunk of the prompt or before it, nor other heads, columns or sequences."""
+    lens, t = [700, 90], 333
+    x = _prompt(lens, 2, 1, d_k, d_v, kind, "slow", False, True)
+    clean, S = _run_prompt(lens, 2, 1, d_k, d_v, x, False)
+    x["v"][t, 0, 5] = math.inf
+    x["v"][t, 0, 9] = math.nan
+    o, S2 = _run_prompt(lens, 2, 1, d_k, d_v, x, False)
+    keep = torch.ones_like(o, dtype=torch.bool)
+    keep[t:700, 0, 5] = keep[t:700, 0, 9] = False
+    # (the chunk's sums are made in another order then)
+    assert torch.isfinite(o[keep]).all()
+    assert float((o - clean)[keep].abs().max()) <= 1e-4 * float(clean.abs().max())
+    assert torch.equal(o[:, 1], clean[:, 1]) or float(
+        (o - clean)[:, 1].abs().max()) <= 1e-4 * float(clean.abs().max())
+    assert torch.equal(o[700:], clean[700:])
+    assert (torch.isinf(o[t, 0, 5]) or torch.isnan(o[t, 0, 5])) and torch.isnan(o[t, 0, 9])
+    assert torch.equal(S2[1], S[1]) and torch.equal(S2[0, 1], S[0, 1])
+    assert torch.isfinite(S2[0, 0, :, :5]).all() and torch.isnan(S2[0, 0, :, 9]).all()
+
+
+def test_no_tokens():
+    """Sequences without tokens hand their states through."""
+    S0 = torch.randn(2, 2, 64, 64, device="cuda")
+    S = torch.empty_like(S0)
+    e = torch.empty(0, 2, 64, device="cuda")
+    gdn.decay_prefill([0, 0], 2, 2, 64, 64, e, e, e,
+                      torch.empty(0, 2, device="cuda"), S0, S, e, None)
+    assert torch.equal(S, S0)
+    gdn.decay_prefill([0, 0], 2, 2, 64, 64, e, e, e,
+                      torch.empty(0, 2, device="cuda"), None, S, e, None)
+    assert (S == 0).all()
+
+
 # ------------------------------------------------------------------ windows
 def _window(layers, t_lane, h_v, h_k, d_k, d_v, T, kind, gates, per_head,
             seed=1):

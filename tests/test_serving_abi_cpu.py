@@ -86,6 +86,12 @@ def test_prompt_workspace():
         assert _prompt(lens=(100000,), ws=P + 8) == EINVAL
 
 
+def test_prompt_without_tokens_needs_no_inputs():
+    none = dict(q=None, k=None, v=None, g=None, o=None)
+    assert _prompt(lens=(0, 0), S=None, **none) == EINVAL    # nothing is wanted
+    assert _prompt(lens=(0, 1), **none) == EINVAL
+
+
 # -------------------------------------------------------------------- paged
 def _kv(**over):
     d = dict(n_lanes=2, t_max=4, h_q=8, h_kv=2, d=128, page_size=16,
@@ -132,6 +138,20 @@ def test_attention_refusals():
     for bad in BAD_KV + [dict(d=96)]:
         assert gdn.paged_attention_workspace_bytes(_kv(**bad)) == 0
     assert gdn.lib.gdn_paged_attention_workspace_bytes(None) == 0
+
+
+def test_page_division():
+    """The multiplier the kernels divide positions by the page size with, for
+    every page size class and positions up to its limit."""
+    for page in list(range(1, 130)) + [255, 256, 257, 1000, 4095, 65537, (1 << 28) + 1]:
+        shift = 0
+        while 1 << shift < page:
+            shift += 1
+        mul = ((((1 << shift) - page) << 32) // page + 1) & 0xffffffff
+        for q in (0, 1, 2, 3, 7, 1000, (1 << 29) // page):
+            for pos in (q * page - 1, q * page, q * page + page // 2):
+                if 0 <= pos < 1 << 29:
+                    assert (((pos * mul) >> 32) + pos) >> shift == pos // page
 
 
 def test_append_refusals():
