@@ -353,9 +353,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p,
                                            kBufWord3);
 }
 
-template <typename TIn, int W, bool VEC>
+template <typename TIn, int W, bool VEC, bool kColumns>
 struct Transit {
-  typedef gdn::op::Tile<TIn, W> Tile;
+  typedef gdn::op::Tile<TIn, W, kColumns> Tile;
   static constexpr int kPer = Tile::kPer;
   static constexpr int kRows = 256 * kPer / W;
   static constexpr int kPieces = kChunk / kRows;
@@ -440,8 +440,8 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
   typedef typename O::Raw Raw;
   typedef typename O::Wide Wide;
   constexpr int KS = DK / 32, CT = CW / 16, W = 4 * CW;
-  typedef Transit<TIn, DK, true> KT;
-  typedef Transit<TIn, W, VEC> VT;
+  typedef Transit<TIn, DK, true, MODE == kStates> KT;
+  typedef Transit<TIn, W, VEC, true> VT;
   typedef typename KT::Tile KL;
   typedef typename VT::Tile VL;
   // (states alone leave room for a second set of tiles: the next chunk is

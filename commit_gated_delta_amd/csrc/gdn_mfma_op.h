@@ -19,13 +19,14 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // Staged rows in LDS.  bf16: W entries a row, its 16-byte pieces permuted by
-// an XOR with the row such that both ways of reading them are free of bank
-// conflicts: a piece of eight neighbouring rows (fragments along the row),
-// and 64 bytes of four neighbouring rows (transposed fragments).  A row of
-// fewer than 16 pieces shares its 256 bytes with the next ones.  Permuted
-// row numbers repeat every 16 rows, so a lane computes its offsets once.
+// an XOR with the row against bank conflicts (256 bytes a cycle): of a piece
+// of 16 rows (fragments along the row), or, in a tile of kColumns that is
+// only read transposed, of 32 bytes of eight rows.  (Transposed reads of the
+// first kind, 64 bytes of eight rows in halves of pieces, take two cycles.)
+// A row of fewer than 16 pieces shares its 256 bytes with the next ones.
+// Permutations repeat every 16 rows, so a lane computes its offsets once.
 // f32: rows one piece apart from a multiple of the banks.
-template <typename TIn, int W>
+template <typename TIn, int W, bool kColumns = false>
 struct Tile {
   static constexpr int kPer = 16 / sizeof(TIn);  // entries per piece
   static constexpr int kPieces = W / kPer;
@@ -33,7 +34,10 @@ struct Tile {
   static constexpr int kPitch = kSwizzled ? W : W + kPer;
   // Entry offset of piece p of row r.
   static __device__ __forceinline__ int at(int r, int p) {
-    if constexpr (kSwizzled) {
+    if constexpr (kSwizzled && kColumns) {
+      if constexpr (kPieces >= 16) p ^= (r & 7) << 1;
+      else if constexpr (kPieces == 8) p ^= (r >> 1 & 3) << 1;
+    } else if constexpr (kSwizzled) {
       if constexpr (kPieces >= 16) p ^= (r & 3) << 2 | (r >> 2 & 3);
       else if constexpr (kPieces == 8) p ^= (r >> 1 & 1) << 2 | (r >> 2 & 3);
       else p ^= r >> 2 & 3;

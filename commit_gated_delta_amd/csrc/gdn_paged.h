@@ -157,8 +157,8 @@ __device__ __forceinline__ float elem(const float* p, long i) { return p[i]; }
 //
 // Two kernels share this.  For up to 32 rows (16 at D = 256) the four waves
 // of attend_kernel share out the positions and each loads its own: the work
-// is reading the cache.  For more rows those of rows_kernel take 16 RT rows
-// each of the same positions, staged once for all four.
+// is reading the cache.  For more rows the waves of rows_kernel take 16 rows
+// each of the same positions, staged once for all of them.
 constexpr float kSlack = 8.f;
 
 // Scores, softmax state and outputs of a wave.
@@ -167,7 +167,8 @@ struct Rows {
   typedef Op<T> O;
   typedef typename O::Raw Raw;
   typedef typename O::Wide Wide;
-  typedef Tile<T, D> TL;
+  typedef Tile<T, D> TL;        // q and K
+  typedef Tile<T, D, true> VL;  // V
   static constexpr int KS = D / 32, CT = D / 16;
   f32x4 acc[RT][CT], sc[RT][2];
   float m[RT], l[RT];
@@ -247,7 +248,7 @@ struct Rows {
       Raw vf[kTwo];
 #pragma unroll
       for (int y = 0; y < kTwo; ++y)
-        vf[y] = O::template column<TL>(Vs, r0, 16 * (c + y), 4,
+        vf[y] = O::template column<VL>(Vs, r0, 16 * (c + y), 4,
                                        threadIdx.x & 63);
 #pragma unroll
       for (int i = 0; i < O::kSteps; ++i)
@@ -311,7 +312,7 @@ __device__ __forceinline__ void stage_q(T* Qs, const AttendArgs& p, int lane,
                                         int hk, int row0, int n, int rows) {
   typedef Tile<T, D> TL;
   const int group = p.kv.h_q / p.kv.h_kv;
-  for (int i = threadIdx.x; i < n * TL::kPieces; i += 256) {
+  for (int i = threadIdx.x; i < n * TL::kPieces; i += blockDim.x) {
     const int r = i / TL::kPieces, c = i % TL::kPieces;
     u32x4 x = {0, 0, 0, 0};
     if (row0 + r < rows) {
@@ -355,6 +356,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) >= 512 ? 1 : 2) void attend_kern
   typedef typename R::O O;
   typedef typename R::Raw Raw;
   typedef typename R::TL TL;
+  typedef typename R::VL VL;
   constexpr int KS = R::KS, CT = R::CT, kRows = 16 * RT;
   constexpr int kPieces = sizeof(Raw) / 16;  // 16-byte loads per fragment
   constexpr int kTileBytes = 32 * TL::kPitch * (int)sizeof(T);
@@ -490,7 +492,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) >= 512 ? 1 : 2) void attend_kern
 #pragma unroll
         for (int y = 0; y < kPieces; ++y)
           *reinterpret_cast<u32x4*>(
-              Vs + TL::at(n, kPieces * (4 * i + g4) + y) + 16 * h * TL::kPitch) =
+              Vs + VL::at(n, kPieces * (4 * i + g4) + y) + 16 * h * VL::kPitch) =
               vr[h][i][y];
     if (next < steps) fetch(vc, vr);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -549,19 +551,22 @@ __global__ __launch_bounds__(256, D * sizeof(T) >= 512 ? 1 : 2) void attend_kern
   }
 }
 
-// Many rows: the waves take 16 RT rows each, and a tile of positions is
-// staged in LDS for all of them.
-template <int D, typename T, int RT>
-__global__ __launch_bounds__(256, D == 256 || sizeof(T) == 4 ? 1 : 2)
+// Many rows: NW waves take 16 rows each, and a tile of positions is staged in
+// LDS for all of them.  (Four waves of 32 rows read half as much from LDS,
+// but two waves per SIMD leave the chain scores - softmax - values exposed.)
+template <int D, typename T, int NW>
+__global__ __launch_bounds__(64 * NW, D * sizeof(T) >= 512 ? NW / 4 : NW / 2)
 void rows_kernel(AttendArgs p, gdn::LaneTable tl) {
-  typedef Rows<D, T, RT> R;
+  typedef Rows<D, T, 1> R;
   typedef typename R::O O;
   typedef typename R::Raw Raw;
   typedef typename R::TL TL;
-  constexpr int KS = R::KS, CT = R::CT, kRows = 64 * RT;
+  typedef typename R::VL VL;
+  constexpr int KS = R::KS, CT = R::CT, kRows = 16 * NW;
   constexpr int kTile = sizeof(T) == 2 ? 64 : 32;  // positions per tile
-  constexpr int kStep = 256 / TL::kPieces;         // rows per piece of a thread
+  constexpr int kStep = 64 * NW / TL::kPieces;     // rows per piece of a thread
   constexpr int kN = kTile / kStep;                // pieces of a thread
+  static_assert(kN >= 1 && kN * kStep == kTile, "every thread has a piece");
   __shared__ __attribute__((aligned(16))) T Qs[kRows * TL::kPitch];
   __shared__ __attribute__((aligned(16))) T Ks[kTile * TL::kPitch];
   __shared__ __attribute__((aligned(16))) T Vs[kTile * TL::kPitch];
@@ -618,7 +623,7 @@ void rows_kernel(AttendArgs p, gdn::LaneTable tl) {
     look_up(1);
   }
   R x;
-  x.init(row0 + 16 * RT * wave, rows, s.len, T_n, group);
+  x.init(row0 + 16 * wave, rows, s.len, T_n, group);
   if (tid == 0) odd_tile[0] = 0;
   for (int tile = 0; tile < tiles; ++tile) {
     const int t0 = begin + tile * kTile;
@@ -640,7 +645,7 @@ void rows_kernel(AttendArgs p, gdn::LaneTable tl) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       *reinterpret_cast<u32x4*>(Ks + TL::at(r0 + i * kStep, piece)) = kr[i];
-      *reinterpret_cast<u32x4*>(Vs + TL::at(r0 + i * kStep, piece)) = vr[i];
+      *reinterpret_cast<u32x4*>(Vs + VL::at(r0 + i * kStep, piece)) = vr[i];
     }
     __syncthreads();
     const bool is_odd = odd_tile[tile & 1];
@@ -650,24 +655,18 @@ void rows_kernel(AttendArgs p, gdn::LaneTable tl) {
       fetch();
       look_up(tile + 2);
     }
-    if (row0 + 16 * RT * wave >= rows) continue;
-#pragma unroll
+    if (row0 + 16 * wave >= rows) continue;
+#pragma unroll 1
     for (int half = 0; half < kTile / 32; ++half) {
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-        x.sc[r][0] = x.sc[r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      x.sc[0][0] = x.sc[0][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
-        Raw kf[2];
+        const Raw qf = O::template row<TL>(Qs, 16 * wave, n, 4 * i + g4);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          kf[h] = O::template row<TL>(Ks, 32 * half + 16 * h, n, 4 * i + g4);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const Raw qf = O::template row<TL>(Qs, 16 * (RT * wave + r), n, 4 * i + g4);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) x.sc[r][h] = O::mul(kf[h], qf, x.sc[r][h]);
-        }
+          x.sc[0][h] = O::mul(
+              O::template row<TL>(Ks, 32 * half + 16 * h, n, 4 * i + g4), qf,
+              x.sc[0][h]);
       }
       const int p0 = t0 + 32 * half;
       x.softmax(p.scale, whole, (uint32_t)(here >> (32 * half)), p0);
@@ -676,16 +675,13 @@ void rows_kernel(AttendArgs p, gdn::LaneTable tl) {
     }
   }
   x.finish();
+  const int row = row0 + 16 * wave + n;
+  if (row >= rows) return;
+  float f;
+  float* dst = row_out(p, s, hk, row, D, x.m[0], x.l[0], g4 == 0, f);
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int row = row0 + 16 * (RT * wave + r) + n;
-    if (row >= rows) continue;
-    float f;
-    float* dst = row_out(p, s, hk, row, D, x.m[r], x.l[r], g4 == 0, f);
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
-      *reinterpret_cast<f32x4*>(dst + 16 * c + 4 * g4) = x.acc[r][c] * f;
-  }
+  for (int c = 0; c < CT; ++c)
+    *reinterpret_cast<f32x4*>(dst + 16 * c + 4 * g4) = x.acc[0][c] * f;
 }
 
 // Joins the splits of a lane: a wave per row of q, D / 64 columns per lane.
@@ -816,7 +812,7 @@ static KvArgs kv_args(const gdn_kv_dims& d, const void* k, const void* v,
 }
 
 // How a call is spread: few rows of q (attend_kernel) or many in groups of
-// 64 rt (rows_kernel), and the splits: kFewBlocks and kRowsBlocks workgroups
+// 16 a wave (rows_kernel), and the splits: kFewBlocks and kRowsBlocks workgroups
 // in all, short last splits included, and no more than the page tables have
 // units.  Measured, for 32 lanes x 8 heads x 16k..32k positions, one token:
 // 780, 618, 588, 584 us with 512, 1024, 1536, 2048 workgroups (more of them
@@ -827,15 +823,16 @@ constexpr int kFewBlocks = 2048;
 constexpr int kRowsBlocks = 512;
 
 struct Shape {
-  int rows, rt, groups, target, items, slots;
+  int rows, rt, waves, groups, target, items, slots;
   bool few;
 };
 static Shape shape_of(const gdn_kv_dims& d) {
   Shape s;
   s.rows = d.t_max * (d.h_q / d.h_kv);
   s.few = s.rows <= (d.d < 256 ? 32 : 16);
-  s.rt = d.d < 256 && s.rows > (s.few ? 16 : 64) ? 2 : 1;
-  s.groups = s.few ? 1 : (s.rows + 64 * s.rt - 1) / (64 * s.rt);
+  s.rt = s.few && s.rows > 16 ? 2 : 1;
+  s.waves = !s.few && s.rows > 64 && d.d < 256 ? 8 : 4;
+  s.groups = s.few ? 1 : (s.rows + 16 * s.waves - 1) / (16 * s.waves);
   const int items = (s.few ? kFewBlocks : kRowsBlocks) / (d.h_kv * s.groups);
   s.target = items - d.n_lanes > items / 2 ? items - d.n_lanes : items / 2;
   if (s.target < 1) s.target = 1;
@@ -862,11 +859,12 @@ static hipError_t attend(const gdn_kv_dims& d, const Shape& s,
       e = s.rt == 2 ? launch(attend_kernel<D, T, 2>, grid, dim3(256), st, p, tl)
                     : launch(attend_kernel<D, T, 1>, grid, dim3(256), st, p, tl);
     else
-      e = s.rt == 2 ? launch(rows_kernel<D, T, 2>, grid, dim3(256), st, p, tl)
-                    : launch(rows_kernel<D, T, 1>, grid, dim3(256), st, p, tl);
+      e = s.waves == 8
+              ? launch(rows_kernel<D, T, 8>, grid, dim3(512), st, p, tl)
+              : launch(rows_kernel<D, T, 4>, grid, dim3(256), st, p, tl);
   } else {
     e = s.few ? launch(attend_kernel<D, T, 1>, grid, dim3(256), st, p, tl)
-              : launch(rows_kernel<D, T, 1>, grid, dim3(256), st, p, tl);
+              : launch(rows_kernel<D, T, 4>, grid, dim3(256), st, p, tl);
   }
   // a cache of one unit per lane has nothing to join
   if (e != hipSuccess || (long)d.max_pages * d.page_size <= kUnit) return e;
