@@ -653,6 +653,9 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
           st[ct][i][1] *= all;
         }
       };
+      // (while it multiplies, a wave goes first on its SIMD: 318 -> 301 us for
+      // 32,768 tokens x 32 heads)
+      __builtin_amdgcn_s_setprio(1);
       state_operands(0);
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
@@ -677,6 +680,7 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) acc[ct][j] *= in;
       }
+      __builtin_amdgcn_s_setprio(0);
       __syncthreads();  // P^T is complete
     } else {
 #pragma unroll
@@ -787,6 +791,7 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
         kf[u & 1][y] = O::template column<KL>(Ks, 32 * (u / KS),
                                               32 * (u % KS) + 4 * y, 8, lane);
     };
+    __builtin_amdgcn_s_setprio(1);
     key_operands(0);
     write_operands(0);
 #pragma unroll
@@ -806,6 +811,7 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
       if (u == KS - 1 || u == KS) interleave<6 * CT, 10>();
     }
     __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(0);
     if constexpr (kSets == 2) set ^= 1;
     else __syncthreads();
     if (more) place(set, left - 1);
