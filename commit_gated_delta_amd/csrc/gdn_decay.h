@@ -444,14 +444,11 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
   typedef Transit<TIn, W, VEC, true> VT;
   typedef typename KT::Tile KL;
   typedef typename VT::Tile VL;
-  // (states alone leave room for a second set of tiles: the next chunk is
-  // placed while this one is read, with one barrier per chunk)
-  constexpr int kSets = MODE == kStates && sizeof(TIn) == 2 ? 2 : 1;
-  __shared__ __attribute__((aligned(16))) TIn Kset[kSets][kChunk * KL::kPitch];
+  __shared__ __attribute__((aligned(16))) TIn Ks[kChunk * KL::kPitch];
   __shared__ __attribute__((aligned(16))) TIn Qs[MODE == kOutput ? kChunk * KL::kPitch : 8];
-  __shared__ __attribute__((aligned(16))) TIn Vset[kSets][kChunk * VL::kPitch];
+  __shared__ __attribute__((aligned(16))) TIn Vs[kChunk * VL::kPitch];
   __shared__ u32x4 Ps[MODE == kOutput ? kFrags : 1][O::kParts][64];
-  __shared__ __attribute__((aligned(16))) Gates Gset[kSets];
+  __shared__ __attribute__((aligned(16))) Gates G;
   __shared__ int odd_chunk[2];  // whether a chunk's V holds special values
 
   const DecayArgs& a = p.a;
@@ -545,17 +542,17 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
   auto fetch_q = [&](int t0) {
     if constexpr (MODE == kOutput) qt.load(Q + t0 * ks, ks, T - t0);
   };
-  auto place = [&](int set, int left) {
+  auto place = [&](int left) {
     if constexpr (MODE == kOutput) {
       Special<TIn> odd;
 #pragma unroll
       for (int i = 0; i < VT::kPieces; ++i) odd.look(vt.r[i]);
       if (odd.any()) odd_chunk[left & 1] = 1;
     }
-    kt.store(Kset[set]);
+    kt.store(Ks);
     if constexpr (MODE == kOutput) qt.store(Qs);
-    vt.store(Vset[set]);
-    if (wave == 0) next_gates.store(Gset[set], lane);
+    vt.store(Vs);
+    if (wave == 0) next_gates.store(G, lane);
   };
 
   // A segment's own state is summed from its last chunk to its first, each
@@ -571,20 +568,18 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
     fetch_q(t0);
     sum = next_gates.make(gate);
   }
-  int set = 0, left = (T + kChunk - 1) / kChunk;  // chunks left
+  int left = (T + kChunk - 1) / kChunk;  // chunks left
   if constexpr (MODE == kOutput) {
     if (tid == 0) odd_chunk[left & 1] = 0;
     __syncthreads();
   }
-  if (T > 0) place(0, left);
+  if (T > 0) place(left);
   for (; left > 0; --left, t0 += t_step) {
     __syncthreads();
     if (MODE == kOutput && tid == 0) odd_chunk[~left & 1] = 0;
     const bool more = left > 1;
     const float since = back ? __builtin_amdgcn_exp2f((float)total) : 1.f;
     total += sum;
-    const TIn *Ks = Kset[set], *Vs = Vset[set];
-    const Gates& G = Gset[set];
     // the next chunk's K and V rows now; Q's when the state's operands have
     // left the registers
     gate = 0.f;
@@ -812,9 +807,8 @@ void chunk_kernel(ChunkArgs p, SegTable tab, int last_only) {
     }
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(0);
-    if constexpr (kSets == 2) set ^= 1;
-    else __syncthreads();
-    if (more) place(set, left - 1);
+    __syncthreads();
+    if (more) place(left - 1);
   }
 
   float* to = nullptr;
@@ -911,9 +905,9 @@ static int check_pointers(const char* fn, const DecayArgs& p, int in_dtype,
   if (tokens && (!p.k || !p.v || !p.g || (p.o && !p.q))) what = "required pointer is NULL";
   else if (in_dtype != GDN_BF16 && in_dtype != GDN_F32) what = "unknown in_dtype";
   else if (misaligned(p.q, 16) || misaligned(p.k, 16) || misaligned(p.v, 16) ||
-           misaligned(p.g, 16) || misaligned(p.s_in, 16) ||
+           misaligned(p.g, 4) || misaligned(p.s_in, 16) ||
            misaligned(p.s_out, 16) || misaligned(p.o, 16))
-    what = "pointers must be 16-byte aligned";
+    what = "pointers must be 16-byte aligned (g: 4-byte)";
   if (!what) return GDN_OK;
   snprintf(msg, sizeof(msg), "%s: %s", fn, what);
   return fail(GDN_EINVAL, msg);

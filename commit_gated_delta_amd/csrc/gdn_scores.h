@@ -612,9 +612,9 @@ extern "C" int gdn_token_scores(int32_t n_rows, int32_t vocab,
     return fail(GDN_EINVAL, "gdn_token_scores: sizes out of range");
   if (in_dtype != GDN_BF16 && in_dtype != GDN_F32)
     return fail(GDN_EINVAL, "gdn_token_scores: unknown in_dtype");
-  if (!(inv_temperature > 0.f) || !(inv_temperature < INFINITY))
+  if (!(inv_temperature >= 1e-30f) || !(inv_temperature <= 1e30f))
     return fail(GDN_EINVAL,
-                "gdn_token_scores: inv_temperature must be finite and > 0");
+                "gdn_token_scores: inv_temperature out of 1e-30..1e30");
   if (!logits || (tokens && !logprob) || (!tokens && logprob) ||
       (n_top > 0 && (!top_ids || !top_logprobs)))
     return fail(GDN_EINVAL, "gdn_token_scores: required pointer is NULL");

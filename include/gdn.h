@@ -428,7 +428,8 @@ int gdn_state_restore(const gdn_dims* dims, int32_t n_sel,
  * q and k are used as they are (no norm).  g is the log-decay: one value per
  * token and value head, or with GDN_FLAG_HEAD_DECAY one constant per value
  * head.  A gate below -1000 (-inf among them) counts as -1000, whose decay
- * is 0 in f32 all the same.  Every state, sum and decay is f32 or wider.
+ * is 0 in f32 all the same.  Every state, sum and decay is f32 or wider.  A
+ * token's infinities and NaN reach its own and later outputs of its head.
  *
  * gdn_decay_step: the recurrent form, for single tokens (t_max = 1) and
  * draft windows.  Advances every (layer, lane, value head) by t_lane[lane]
@@ -448,7 +449,7 @@ int gdn_state_restore(const gdn_dims* dims, int32_t n_sel,
  *            place (read only with GDN_FLAG_KEEP_STATE)
  *   o        device f32 [n_layers][n_lanes][t_max][h_v][d_v], or NULL
  *   flags    GDN_FLAG_HEAD_DECAY, GDN_FLAG_KEEP_STATE (not with o = NULL)
- * Every device pointer must be 16-byte aligned (GDN_EINVAL).
+ * Device pointers must be 16-byte aligned, g 4-byte (GDN_EINVAL).
  */
 int gdn_decay_step(const gdn_dims* dims, const int32_t* t_lane, const void* q,
                    const void* k, const void* v, int in_dtype, const float* g,
@@ -482,7 +483,7 @@ size_t gdn_decay_prefill_workspace_bytes(int32_t n_seqs,
  *            workspaces of their own
  *   flags    GDN_FLAG_HEAD_DECAY or 0
  * Sizes: d_k 16, 32, 64 or 128, d_v 1..1024, h_v a multiple of h_k.
- * Every device pointer must be 16-byte aligned (GDN_EINVAL).
+ * Device pointers must be 16-byte aligned, g 4-byte (GDN_EINVAL).
  */
 int gdn_decay_prefill(int32_t n_seqs, const int32_t* seq_len, int32_t h_v,
                       int32_t h_k, int32_t d_k, int32_t d_v, const void* q,
@@ -562,7 +563,7 @@ int gdn_kv_append(const gdn_kv_dims* dims, const int32_t* t_lane,
  *   logits      device, in_dtype (bf16 or f32), element-aligned
  *   tokens      device int32[n_rows] or NULL (then logprob is NULL too)
  *   n_top       0..GDN_MAX_TOP and at most vocab
- *   inv_temperature  finite, > 0
+ *   inv_temperature  1e-30 .. 1e30
  *   logprob     device f32[n_rows]: log p of the row's token; 0 for a
  *               negative token (no token given), NaN for one >= vocab
  *   entropy     device f32[n_rows] or NULL: -sum p log p

@@ -2,16 +2,14 @@
 per head, paged attention, token scores), written from their definitions, and
 the error bounds the tests hold the kernels to.
 
-Units: U32 = 2^-24 is half a step of f32; a value carried as two bf16 parts
-is off by at most SPLIT = 2^-18 of itself (each part by half a step, 2^-9, of
-what it stands for).
+Unit: U32 = 2^-24, half a step of f32.  (The kernels carry f32 operands of
+bf16 products as three parts of 8 bits, which is exact.)
 """
 import math
 
 import torch
 
 U32 = 2.0 ** -24
-SPLIT = 2.0 ** -18
 
 
 def decay_chain(q, k, v, g, S0, scale):
@@ -36,12 +34,12 @@ def decay_chain(q, k, v, g, S0, scale):
 
 def decay_bound(d_k, tokens):
     """Largest error of an output or state entry relative to the sum of its
-    terms' absolute values.  Two splits can lie on a term's way (the write
-    and the state it is read from); its decays are a product of
-    at most tokens / 64 + 2 rounded exponentials, each exact to 4 ulp of f32;
-    sums run over d_k entries, 64 tokens and one step per 64 tokens."""
+    terms' absolute values: a term's decays are a product of at most
+    tokens / 64 + 2 rounded exponentials, each exact to 4 steps of f32; sums
+    run over d_k entries and 64 tokens, at most a step of f32 for each, and
+    one addition per 64 tokens."""
     steps = tokens / 64 + 2
-    return 2 * SPLIT + (8 * steps + d_k + 64 + steps) * U32
+    return (8 * steps + 2 * (d_k + 64) + steps) * U32
 
 
 def step_bound(d_k, tokens):
@@ -52,9 +50,9 @@ def step_bound(d_k, tokens):
 
 def attend(q, k_cache, v_cache, table, kv_len, t_lane, scale):
     """f64 paged attention: (o, bound): rows of idle tokens are NaN in o.
-    Relative to sum p |v|, an output is off by the split of p, by the error
-    e of its score (and of the largest score) twice through the softmax, by
-    the sums (one step per position) and a few roundings.  A score's error is
+    Relative to sum p |v|, an output is off by the error e of its score (and
+    of the largest score) twice through the softmax, by the sums (one step
+    per position) and a few roundings.  A score's error is
     (d + 4) U32 times the sum of its terms' absolute values."""
     N, T, Hq, d = q.shape
     n_pages, Hkv, page, _ = k_cache.shape
@@ -84,7 +82,7 @@ def attend(q, k_cache, v_cache, table, kv_len, t_lane, scale):
                 o[n, t, h] = (p[:, None] * v[:, h // group]).sum(0)
                 e = (d + 4) * U32 * float(xa.max()) + 4 * U32
                 mag = (p[:, None] * v[:, h // group].abs()).sum(0)
-                tol[n, t, h] = mag * (SPLIT + 4 * e + (2 * len(x) + 16) * U32)
+                tol[n, t, h] = mag * (4 * e + (2 * len(x) + 16) * U32)
     return o, tol + 1e-30
 
 

@@ -292,6 +292,15 @@ def test_verify_commit_and_single_tokens_agree_bit_for_bit(kind, d_k, d_v):
     assert torch.equal(S_m[:, 2], x["S"][:, 2])
 
 
+def test_a_layer_of_the_gates():
+    """One layer's constant decays out of all layers' (8-byte aligned)."""
+    x = _window(1, [3, 2], 2, 1, 64, 64, 3, "bf16", "slow", True)
+    want = _run_window(x, [3, 2], True)
+    g = torch.stack([x["g"][0] - 1, x["g"][0], x["g"][0] + 1])
+    got = _run_window(dict(x, g=g[1:2]), [3, 2], True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_256_lanes():
     t_lane = [i % 3 for i in range(256)]
     x = _window(1, t_lane, 2, 1, 64, 64, 2, "bf16", "slow", False)

@@ -122,6 +122,19 @@ def test_given_tokens_that_are_not_in_the_vocabulary():
     assert float(lp[0]) == 0 and math.isnan(float(ent[0]))
 
 
+@pytest.mark.parametrize("it", [1e-30, 1e-4, 1e4, 1e30])
+def test_extreme_temperatures(it):
+    x, t = _logits(3, 20000, "f32")
+    x[1, ::2] = -math.inf
+    lp, ent, ids, best = _run(x, t, 3, it)
+    want = ref.scores(x, t, 3, it)
+    assert torch.equal(ids, want[2])
+    fine = torch.isfinite(want[0])
+    assert torch.equal(torch.isfinite(lp), fine)
+    assert float(((lp - want[0]).abs() / (1 + want[0].abs()))[fine].max()) < 1e-5
+    assert float((ent - want[1]).abs().max()) < 1e-4
+
+
 def test_sharp_and_flat_rows():
     x, t = _logits(4, 30000, "f32", spread=1.0)
     x[0] *= 40

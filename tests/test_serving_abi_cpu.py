@@ -40,7 +40,7 @@ def test_step_refusals():
                 dict(t_null=True), dict(q=None), dict(k=None), dict(v=None),
                 dict(g=None), dict(S=None), dict(dt=2), dict(flags=1),
                 dict(flags=4), dict(flags=32), dict(q=P + 8), dict(S=P + 4),
-                dict(o=P + 2), dict(g=P + 4),
+                dict(o=P + 2), dict(g=P + 2),
                 dict(o=None, flags=gdn.GDN_FLAG_KEEP_STATE)):
         assert _step(**bad) == EINVAL, bad
         assert _message()
@@ -67,7 +67,7 @@ def test_prompt_refusals():
                 dict(d_v=0), dict(d_v=2000), dict(q=None), dict(k=None),
                 dict(v=None), dict(g=None), dict(dt=5), dict(flags=16),
                 dict(flags=1), dict(S=None, o=None), dict(S0=P + 4),
-                dict(S=P + 8), dict(o=P + 4), dict(v=P + 2), dict(g=P + 4)):
+                dict(S=P + 8), dict(o=P + 4), dict(v=P + 2), dict(g=P + 2)):
         assert _prompt(**bad) == EINVAL, bad
         assert _message()
     # nothing to do
@@ -178,7 +178,7 @@ def test_scores_refusals():
     for bad in (dict(rows=0), dict(rows=-1), dict(vocab=0), dict(stride=999),
                 dict(top=-1), dict(top=33), dict(vocab=4, stride=4),
                 dict(logits=None), dict(dt=2), dict(it=0.0), dict(it=-1.0),
-                dict(it=math.inf), dict(it=math.nan), dict(tokens=None),
+                dict(it=math.inf), dict(it=math.nan), dict(it=1e-31), dict(it=1e31), dict(tokens=None),
                 dict(lp=None), dict(ids=None), dict(best=None),
                 dict(lp=None, tokens=None, ent=None, top=0),
                 dict(logits=P + 2), dict(dt=gdn.GDN_BF16, logits=P + 1),
