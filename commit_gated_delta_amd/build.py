@@ -23,9 +23,11 @@ FLAGS = ["-O3", "--offload-arch=gfx950", "-std=c++17", "-fPIC",
          "-ffp-contract=off", "-fno-fast-math",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-Wno-unused-command-line-argument"]
-# The prefill state chain scales and splits its MFMA accumulators every
-# chunk; keeping them in ordinary VGPRs avoids a copy through AGPRs.
-EXTRA = {"gdn_prefill.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=true"]}
+# The prefill state chains (gdn_prefill.hip, and gdn_decay.h in gdn_kda.hip)
+# scale and split their MFMA accumulators every chunk; keeping them in
+# ordinary VGPRs avoids a copy through AGPRs.
+EXTRA = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form=true"]
+         for f in ("gdn_prefill.hip", "gdn_kda.hip")}
 
 
 def build(verbose: bool = False) -> str:

@@ -1,6 +1,7 @@
 // gdn_decay.h -- linear attention with a decay per head, in its recurrent
 // form (gdn_decay_step) and over packed prompts (gdn_decay_prefill).
-// Compiled as part of gdn_prefill.hip.
+// Compiled as part of gdn_kda.hip (the library is a fixed set of translation
+// units; the other sibling of the gated delta rule lives there).
 //
 //   S_t = a_t S_{t-1} + k_t v_t^T,  o_t = scale S_t^T q_t,  a_t = exp(g_t)
 #pragma once

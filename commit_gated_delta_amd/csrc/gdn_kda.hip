@@ -30,6 +30,7 @@
 // all its lanes: lanes 0..R-1 compute them one token ahead (exp of the
 // loaded gate) into LDS, where the next token reads them back as broadcasts
 // after the token's exchange barrier.
+#include "gdn_decay.h"
 #include "gdn_window_common.h"
 
 namespace gdn {

@@ -63,7 +63,6 @@
 #include <type_traits>
 
 #include "gdn.h"
-#include "gdn_decay.h"
 #include "gdn_internal.h"
 
 namespace gdnp {
