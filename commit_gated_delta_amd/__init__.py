@@ -1,13 +1,15 @@
 """Python binding of libgdn.so: gated-delta verify, ReplaySSM commit and
-chunked prefill on MI355X (gfx950).
+chunked prefill on MI355X (gfx950), and the serving operators beside them
+(linear attention with a decay per head, paged attention, token scores).
 
-Argument marshalling only: every step of the path runs in the HIP kernels
-behind the C ABI declared in ``include/gdn.h``.  torch provides device
-memory and streams.  There is no fallback: if the built library is missing,
+Argument marshalling only (with checks of the tensors for the latter): every
+step of the path runs in the HIP kernels behind the C ABI declared in
+``include/gdn.h``.  torch provides device memory and streams.  There is no fallback: if the built library is missing,
 importing this package raises.
 
 Names follow the C ABI: ``verify``, ``commit``, ``prefill_chunked``,
-``records_bytes``, ``prefill_workspace_bytes``.
+``records_bytes``, ``prefill_workspace_bytes``, ``decay_step``,
+``decay_prefill``, ``paged_attention``, ``kv_append``, ``token_scores``, ...
 """
 from __future__ import annotations
 

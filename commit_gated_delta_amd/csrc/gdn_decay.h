@@ -44,6 +44,10 @@ struct DecayArgs {
 // windows of up to 16 on 8 lanes x 48 layers).  Its k and
 // q entries are DK/8 consecutive ones of the token's row.  o needs one sum
 // over the eight row groups per token.
+// A single token is bound by HBM (8 lanes x 32 heads, 34 MB: 9 us of which
+// half is latency); a window by HBM and by its three f32 operations per state
+// entry and token (8 lanes x 48 layers, up to 16 tokens: 0.87 GB in 178 us,
+// 4.9 TB/s).
 constexpr int kStepCols = 32;
 
 template <typename TIn, int R>
@@ -252,6 +256,11 @@ __global__ __launch_bounds__(256) void step_kernel(DecayArgs p,
 // first pass forms each segment's own state (from zero) and decay, a scan
 // turns those into the segments' start states, and the output pass runs all
 // segments at once.
+//
+// Measured, 32,768 tokens x 32 heads of 128, bf16: states pass 126 us (540 MB,
+// 4.3 TB/s), scan 14 us, output pass 301..317 us (1.39 GB, 4.5 TB/s; matrix
+// cores 41 % and vector ALUs 48 % busy, next to each other rather than at
+// once: two waves per SIMD are all that 250 registers leave).
 constexpr int kChunk = 64;
 
 // Segments of the sequences: sequence s has the segments first[s] ..
