@@ -475,6 +475,7 @@ __global__ __launch_bounds__(64) void join_kernel(ScoreArgs p) {
     const Part q = parts[i];
     if (q.m == -INFINITY) continue;
     const float d = q.m - m, f = __builtin_amdgcn_exp2f(d * (p.it * kLog2e));
+    if (f == 0.f) continue;  // (d z may have left f32: a slice of lowest values)
     z = __builtin_fmaf(f, q.z, z);
     w = __builtin_fmaf(f, __builtin_fmaf(d, q.z, q.w), w);
   }

@@ -113,6 +113,20 @@ def test_masked_empty_and_bad_rows(vocab, kind):
     assert float(lp[6]) < -1e30 and math.isfinite(float(ent[6]))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_whole_slices_at_the_lowest_value(kind):
+    """All but one token masked with the type's lowest value: p = 1 for it,
+    and nothing in the entropy from slices that hold nothing else."""
+    x = torch.full((3, 140000), torch.finfo(TYPES[kind]).min, device="cuda", dtype=TYPES[kind])
+    for r, i in enumerate((0, 70000, 139999)):
+        x[r, i] = 2.0
+    t = torch.tensor([0, 70000, 5], dtype=torch.int32, device="cuda")
+    lp, ent, ids, best = _run(x, t, 2)
+    assert ent.tolist() == [0, 0, 0] and lp[:2].tolist() == [0, 0]
+    assert float(lp[2]) < -1e38 and best[:, 0].tolist() == [0, 0, 0]
+    assert ids.tolist() == [[0, 1], [70000, 0], [139999, 0]]
+
+
 def test_given_tokens_that_are_not_in_the_vocabulary():
     x, _ = _logits(4, 300, "f32")
     t = torch.tensor([-1, 300, 299, -100], dtype=torch.int32, device="cuda")
