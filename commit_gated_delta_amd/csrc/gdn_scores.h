@@ -407,7 +407,9 @@ __global__ __launch_bounds__(kThreads, 4) void slice_kernel(ScoreArgs p) {
       }
     };
     const int entries = listed;
-    if (entries <= kList && tau > key_of(-INFINITY)) {
+    if (alone && r.bad) {  // (a negative NaN is in none of the lists)
+      if (tid < p.n_top) write_top(p, row, r, tid, 0.f, -1);
+    } else if (entries <= kList && tau > key_of(-INFINITY)) {
       for (int i = tid; i < entries; i += kThreads) {
         const uint32_t key = list_key[i];
         const int id = list_id[i];

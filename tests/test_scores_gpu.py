@@ -127,6 +127,18 @@ def test_whole_slices_at_the_lowest_value(kind):
     assert ids.tolist() == [[0, 1], [70000, 0], [139999, 0]]
 
 
+@pytest.mark.parametrize("vocab", [5, 100, 20011])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_nan_of_either_sign(vocab, kind):
+    x, t = _logits(4, vocab, kind)
+    x[0] = math.nan
+    x[1] = -x[0]
+    x[2, vocab // 2] = -x[0, 0]
+    ints = x.view(torch.int16 if kind == "bf16" else torch.int32)
+    assert int(ints[1, 0]) < 0 < int(ints[0, 0])
+    _check(x, t, 5)
+
+
 def test_given_tokens_that_are_not_in_the_vocabulary():
     x, _ = _logits(4, 300, "f32")
     t = torch.tensor([-1, 300, 299, -100], dtype=torch.int32, device="cuda")
