@@ -756,9 +756,9 @@ __global__ __launch_bounds__(256) void append_kernel(
   const int n = (int)(nt / a.t_max), t = (int)(nt % a.t_max);
   const int T = tl.v[n];
   if (t >= T) return;
-  const int pos = lane_len(a, n) - T + t;
-  if (pos < 0) return;
-  const long dst = row_of(a, n, h, pos, pieces);
+  const long pos = (long)a.kv_len[n] - T + t;
+  if (pos < 0 || pos >= a.max_pages * a.page) return;
+  const long dst = row_of(a, n, h, (int)pos, pieces);
   if (dst < 0) return;
   kc[dst + piece] = k[i];
   vc[dst + piece] = v[i];

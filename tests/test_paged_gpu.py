@@ -237,6 +237,31 @@ def test_append_drops_rows_without_a_page():
     assert torch.equal(x["k"], before)
 
 
+def test_append_drops_rows_past_the_table_and_before_the_cache():
+    """Lengths beyond the table's positions and shorter than the window: the
+    rows that have a position go there, the others nowhere."""
+    x = _case([4, 4, 4, 4], [10, 10, 10, 10], 2, 2, 64, 8, "bf16")
+    cols = x["dims"].max_pages
+    cap = cols * 8
+    x["table"].copy_(torch.randperm(x["dims"].n_pages, device="cuda")[:4 * cols].view(4, cols))
+    x["k"].nan_to_num_(3.0)
+    x["v"].nan_to_num_(3.0)
+    lens = [cap + 2, 1, 2**31 - 1, -2**31]
+    x["kv_len"].copy_(torch.tensor(lens, dtype=torch.int32))
+    k, v = (torch.randn(4, 4, 2, 64, device="cuda").bfloat16() for _ in range(2))
+    want = {c: x[c].clone() for c in ("k", "v")}
+    for n, length in enumerate(lens):
+        for t in range(4):
+            pos = length - 4 + t
+            if 0 <= pos < cap:
+                page = int(x["table"][n, pos // 8])
+                want["k"][page, :, pos % 8] = k[n, t]
+                want["v"][page, :, pos % 8] = v[n, t]
+    gdn.kv_append(x["dims"], [4] * 4, k, v, x["k"], x["v"], x["table"], x["kv_len"])
+    for c in ("k", "v"):
+        assert torch.equal(x[c], want[c])
+
+
 def test_captured_calls_follow_the_lengths():
     """Append and attention captured once; the replays see the lengths and
     pages of their time."""
