@@ -103,6 +103,9 @@ __device__ __forceinline__ Split find_split(const KvArgs& a,
   Split s;
   s.units = (all + target - 1) / target;
   if (s.units < 1) s.units = 1;
+  // (no lane has more, and so many positions still fit an int)
+  constexpr int kMost = (1 << 29) / kUnit;
+  if (s.units > kMost) s.units = kMost;
   s.lane = -1;
   int before = 0, slots = 0;
 #pragma unroll

@@ -553,7 +553,7 @@ __global__ __launch_bounds__(64) void join_kernel(ScoreArgs p) {
 }
 
 static bool sizes_ok(int32_t n_rows, int32_t vocab, int32_t n_top) {
-  return n_rows >= 1 && vocab >= 1 && n_top >= 0 && n_top <= GDN_MAX_TOP &&
+  return n_rows >= 1 && vocab >= 1 && vocab <= 1 << 30 && n_top >= 0 && n_top <= GDN_MAX_TOP &&
          n_top <= vocab;
 }
 

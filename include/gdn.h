@@ -558,7 +558,7 @@ int gdn_kv_append(const gdn_kv_dims* dims, const int32_t* t_lane,
 /*
  * Log probabilities of given tokens, with entropy and top alternatives, for
  * rows of logits: x = inv_temperature * logit, p = softmax(x).
- *   n_rows, vocab  >= 1
+ *   n_rows >= 1, vocab 1 .. 2^30
  *   row_stride  elements from one row of logits to the next, >= vocab
  *   logits      device, in_dtype (bf16 or f32), element-aligned
  *   tokens      device int32[n_rows] or NULL (then logprob is NULL too)

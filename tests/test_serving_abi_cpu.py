@@ -176,7 +176,7 @@ def _scores(rows=4, vocab=1000, stride=1000, logits=P, dt=gdn.GDN_F32,
 
 def test_scores_refusals():
     for bad in (dict(rows=0), dict(rows=-1), dict(vocab=0), dict(stride=999),
-                dict(top=-1), dict(top=33), dict(vocab=4, stride=4),
+                dict(vocab=2**30 + 1, stride=2**31), dict(top=-1), dict(top=33), dict(vocab=4, stride=4),
                 dict(logits=None), dict(dt=2), dict(it=0.0), dict(it=-1.0),
                 dict(it=math.inf), dict(it=math.nan), dict(it=1e-31), dict(it=1e31), dict(tokens=None),
                 dict(lp=None), dict(ids=None), dict(best=None),
