@@ -131,11 +131,12 @@ def test_whole_slices_at_the_lowest_value(kind):
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 def test_nan_of_either_sign(vocab, kind):
     x, t = _logits(4, vocab, kind)
-    x[0] = math.nan
-    x[1] = -x[0]
-    x[2, vocab // 2] = -x[0, 0]
     ints = x.view(torch.int16 if kind == "bf16" else torch.int32)
-    assert int(ints[1, 0]) < 0 < int(ints[0, 0])
+    plus, minus = (0x7fc0, 0x7fc0 - 2**15) if kind == "bf16" else (0x7fc00000, 0x7fc00000 - 2**31)
+    ints[0] = plus
+    ints[1] = minus
+    ints[2, vocab // 2] = minus
+    assert torch.isnan(x[:2]).all()
     _check(x, t, 5)
 
 
