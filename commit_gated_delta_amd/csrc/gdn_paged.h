@@ -692,56 +692,101 @@ void rows_kernel(AttendArgs p, gdn::LaneTable tl) {
     *reinterpret_cast<f32x4*>(dst + 16 * c + 4 * g4) = x.acc[0][c] * f;
 }
 
-// Joins the splits of a lane: a wave per row of q, D / 64 columns per lane.
-// Bound by reading the partial results (10 us for 32 MB), or by its launch.
-template <int D>
-__global__ __launch_bounds__(256) void join_kernel(AttendArgs p,
-                                                   gdn::LaneTable tl) {
+// Joins the splits of a lane: a workgroup of NW waves per row of q.  The
+// threads first turn the splits' maxima and sums into weights in LDS; then
+// each group of D / 4 lanes adds up splits of its own, four columns a lane,
+// and the groups' sums meet in registers and LDS.  Bound by its launch and the
+// chain length - maxima - partial results, or by reading those.
+// One wave per row where there are kManyRows of them (4096 rows of 15 splits:
+// 8.7, 9.5, 12.4, 37 us with 1, 2, 4, 16 waves).  Else 4 waves where a lane
+// has at most kFewSplits splits, and 16 where it may have more: one lane's
+// 25k positions, which are 198 splits, take 13 us with the attention itself,
+// against 41 us joined by one wave per row; 4 lanes x 2 heads 31 against 61.
+constexpr unsigned kManyRows = 1024;
+constexpr int kFewSplits = 64;
+constexpr int kFewBlocks = 2048;  // (see shape_of: a lane's splits are no more)
+template <int D, int NW, int N>
+__global__ __launch_bounds__(64 * NW) void join_kernel(AttendArgs p,
+                                                       gdn::LaneTable tl) {
+  constexpr int G = D / 4, kSets = 64 * NW / G;  // groups of lanes
+  constexpr int kAhead = 4;                      // splits in flight per group
+  __shared__ float weight[N];
+  __shared__ float tops[NW], sums[NW];
+  __shared__ __attribute__((aligned(16))) f32x4 part[NW][G];
   const KvArgs& a = p.kv;
   const int per_lane = a.h_kv * p.rows;
-  const long item = (long)blockIdx.x * 4 + threadIdx.x / 64;
-  const int n = gdn::uniform((int)(item / per_lane));
-  if (n >= a.lanes) return;
-  const int hk = gdn::uniform((int)(item % per_lane) / p.rows);
-  const int row = gdn::uniform((int)(item % p.rows));
+  const int n = (int)(blockIdx.x / per_lane), at = (int)(blockIdx.x % per_lane);
+  const int hk = at / p.rows, row = at % p.rows;
   const int group = a.h_q / a.h_kv;
   if (row >= tl.v[n] * group) return;
   const Split s = find_split(a, tl, n, p.target, true);
   if (s.n < 2) return;
-  const int lane = threadIdx.x & 63;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int set = tid / G, c = tid % G * 4;
   const long first = ((long)s.slot * a.h_kv + hk) * p.rows + row;
   const long step = (long)a.h_kv * p.rows;
-  float m = -INFINITY;
-  for (int i = lane; i < s.n; i += 64) m = fmaxf(m, p.part_ml[2 * (first + i * step)]);
+  const float* src = p.part_o + first * D + c;
+  f32x4 y[kAhead];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u * kSets;
+      y[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (i < s.n)
+        y[u] = *reinterpret_cast<const f32x4*>(src + i * step * D);
+    }
+  };
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + first;
+  // a thread's first split is kept, further ones are read again
+  float2 mine = {-INFINITY, 0.f};
+  if (tid < s.n) mine = ml[tid * step];
+  fetch(set);
+  float m = mine.x, l = 0.f;
+  for (int i = tid + 64 * NW; i < s.n; i += 64 * NW)
+    m = fmaxf(m, ml[i * step].x);
 #pragma unroll
   for (int x = 1; x < 64; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
-  float l = 0.f, acc[D / 64] = {};
-  constexpr int kAhead = 4;
-  for (int i = 0; i < s.n; i += kAhead) {
-    float ms[kAhead], ls[kAhead], o[kAhead][D / 64];
+  if (lane == 0) tops[wave] = m;
+  __syncthreads();
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const long at = first + (i + u < s.n ? i + u : i) * step;
-      ms[u] = p.part_ml[2 * at];
-      ls[u] = p.part_ml[2 * at + 1];
+  for (int w = 0; w < NW; ++w) m = fmaxf(m, tops[w]);
+  for (int i = tid; i < s.n; i += 64 * NW) {
+    if (i != tid) mine = ml[i * step];
+    // (a split that saw nothing has no weight; one with a NaN keeps it)
+    const float w = mine.x == -INFINITY && mine.y == 0.f
+                        ? 0.f
+                        : __builtin_amdgcn_exp2f(mine.x - m);
+    weight[i] = w;
+    l = __builtin_fmaf(w, mine.y, l);
+  }
+  l = gdn::wave_sum(l);
+  if (lane == 0) sums[wave] = l;
+  __syncthreads();
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int i0 = set; i0 < s.n; i0 += kAhead * kSets) {
+    if (i0 != set) fetch(i0);
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) o[u][c] = p.part_o[at * D + 64 * c + lane];
-    }
+    for (int u = 0; u < kAhead; ++u)
+      if (i0 + u * kSets < s.n) acc += y[u] * weight[i0 + u * kSets];
+  }
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (i + u >= s.n || (ms[u] == -INFINITY && ls[u] == 0.f)) continue;
-      const float w = __builtin_amdgcn_exp2f(ms[u] - m);
-      l = __builtin_fmaf(w, ls[u], l);
+  for (int x = G; x < 64; x *= 2)
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-        acc[c] = __builtin_fmaf(w, o[u][c], acc[c]);
-    }
+    for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor(acc[e], x);
+  if (lane < G) part[wave][lane] = acc;
+  __syncthreads();
+  if (tid >= G) return;
+  l = 0.f;
+  acc = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    l += sums[w];
+    acc += part[w][tid];
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   float* dst = p.o + (((long)n * a.t_max + row / group) * a.h_q + hk * group +
                       row % group) * D;
-#pragma unroll
-  for (int c = 0; c < D / 64; ++c) dst[64 * c + lane] = acc[c] * inv;
+  *reinterpret_cast<f32x4*>(dst + c) = acc * inv;
 }
 
 // One 16-byte piece of a key and of a value row per thread: a copy (8,192 rows
@@ -829,7 +874,6 @@ static KvArgs kv_args(const gdn_kv_dims& d, const void* k, const void* v,
 // even out the memory's latency); for 8 lanes x 4 heads x 8k..16k, 128 rows:
 // 121, 93, 117, 110 us with 256, 512, 768, 1024 (two a CU run at once, and
 // every split of 128 rows leaves 64 KiB to join).
-constexpr int kFewBlocks = 2048;
 constexpr int kRowsBlocks = 512;
 
 struct Shape {
@@ -877,10 +921,14 @@ static hipError_t attend(const gdn_kv_dims& d, const Shape& s,
               : launch(rows_kernel<D, T, 4>, grid, dim3(256), st, p, tl);
   }
   // a cache of one unit per lane has nothing to join
-  if (e != hipSuccess || (long)d.max_pages * d.page_size <= kUnit) return e;
-  const long rows = (long)d.n_lanes * d.h_kv * s.rows;
-  return launch(join_kernel<D>, dim3((unsigned)((rows + 3) / 4)), dim3(256), st,
-                p, tl);
+  const long units = ((long)d.max_pages * d.page_size + kUnit - 1) / kUnit;
+  if (e != hipSuccess || units < 2) return e;
+  const dim3 rows((unsigned)((long)d.n_lanes * d.h_kv * s.rows));
+  if (rows.x >= kManyRows)
+    return launch(join_kernel<D, 1, kFewBlocks>, rows, dim3(64), st, p, tl);
+  if (units <= kFewSplits || s.target <= kFewSplits)
+    return launch(join_kernel<D, 4, kFewSplits>, rows, dim3(256), st, p, tl);
+  return launch(join_kernel<D, 16, kFewBlocks>, rows, dim3(1024), st, p, tl);
 }
 
 template <typename T>

@@ -90,6 +90,19 @@ def test_attention(t_lane, lens, h_q, h_kv, d, page, kind):
     _check(x, t_lane, _run(x, t_lane, d ** -0.5), d ** -0.5)
 
 
+@pytest.mark.parametrize("t_lane,lens,h_q,h_kv,d,kind", [
+    ([1], [20001], 2, 1, 64, "bf16"),                  # many splits of few rows
+    ([1, 2], [15000, 9], 3, 1, 128, "f32"),
+    ([1], [12345], 1, 1, 256, "bf16"),
+    ([1] * 40, [20000] + [30] * 39, 32, 1, 64, "bf16"),  # and of many rows
+    ([1] * 18, [200] * 17 + [9000], 64, 2, 128, "bf16"),
+])
+def test_many_splits(t_lane, lens, h_q, h_kv, d, kind):
+    x = _case(t_lane, lens, h_q, h_kv, d, 64, kind)
+    x["q"][0, 0, 0] *= 4                               # weights far apart
+    _check(x, t_lane, _run(x, t_lane, d ** -0.5), d ** -0.5)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 def test_peaked_scores(kind):
     """Scores far apart: one position takes nearly everything, in any tile."""
