@@ -41,89 +41,91 @@ struct DecayArgs {
 // holds the DK/8 consecutive state rows r at the four columns 4c: 64 f32
 // registers at DK = 128, loaded and stored as 128-byte row pieces (streamed:
 // nothing reads a state again before every layer has run; 194 -> 179 us for
-// windows of up to 16 on 8 lanes x 48 layers).  Its k and
+// windows of up to 16 on 8 lanes x 48 layers, then without a load ahead).  Its k and
 // q entries are DK/8 consecutive ones of the token's row.  o needs one sum
 // over the eight row groups per token.
-// A single token is bound by HBM (8 lanes x 32 heads, 34 MB: 9 us of which
+// The next token's inputs are loaded while one is computed, with no branch
+// before their use, from wave-uniform addresses (16 lanes x 48 heads of 64 x
+// 32, windows of up to 33: 30 -> 20 us; one lane x 32 heads of 128 x 128,
+// window of 64: 57 -> 42 us).
+// A single token is bound by HBM (8 lanes x 32 heads, 34 MB: 8 us of which
 // half is latency); a window by HBM and by its three f32 operations per state
-// entry and token (8 lanes x 48 layers, up to 16 tokens: 0.87 GB in 178 us,
-// 4.9 TB/s).
+// entry and token (8 lanes x 48 layers, up to 16 tokens: 0.87 GB in 172 us,
+// 5.1 TB/s), and with few states by the latter's latency.
 constexpr int kStepCols = 32;
 
+// R consecutive entries of a row, as loaded.
 template <typename TIn, int R>
-__device__ __forceinline__ void load_row(const TIn* __restrict__ p,
-                                         float (&x)[R]) {
-  if constexpr (sizeof(TIn) == 4) {
-    if constexpr (R == 2) {
-      const float2 a = *reinterpret_cast<const float2*>(p);
-      x[0] = a.x;
-      x[1] = a.y;
-    } else {
-#pragma unroll
-      for (int i = 0; i < R / 4; ++i) {
-        const f32x4 a = reinterpret_cast<const f32x4*>(p)[i];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[4 * i + e] = a[e];
-      }
-    }
-  } else {
-    uint32_t w[R / 2];
-    if constexpr (R == 2) {
+struct RowRegs {
+  static constexpr int kWords = R * (int)sizeof(TIn) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const TIn* __restrict__ p) {
+    if constexpr (kWords == 1) {
       w[0] = *reinterpret_cast<const uint32_t*>(p);
-    } else if constexpr (R == 4) {
+    } else if constexpr (kWords == 2) {
       const uint2 a = *reinterpret_cast<const uint2*>(p);
       w[0] = a.x;
       w[1] = a.y;
     } else {
 #pragma unroll
-      for (int i = 0; i < R / 8; ++i) {
+      for (int i = 0; i < kWords / 4; ++i) {
         const u32x4 a = reinterpret_cast<const u32x4*>(p)[i];
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[4 * i + e] = a[e];
       }
     }
+  }
+  __device__ __forceinline__ void expand(float (&x)[R]) const {
+    if constexpr (sizeof(TIn) == 4) {
 #pragma unroll
-    for (int i = 0; i < R / 2; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      for (int i = 0; i < R; ++i) x[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R / 2; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
     }
   }
-}
+};
 
-// Four consecutive columns from column c of a row of n (V4: n % 4 == 0 and
-// the row 16-byte (bf16: 8-byte) aligned); columns past the end read as 0.
-template <bool V4>
-__device__ __forceinline__ f32x4 load_cols(const float* __restrict__ row,
-                                           int c, int n) {
-  if constexpr (V4) {
-    if (c < n) return __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(row + c));
-    return f32x4{0.f, 0.f, 0.f, 0.f};
-  } else {
+// Four consecutive columns of a row, as loaded.  V4: their number is a
+// multiple of four and the row 16-byte (bf16: 8-byte) aligned.  Columns past
+// the last one read as others and are never stored, so that no load is behind
+// a branch: at[e] is the column to read for e (V4: for e = 0).
+template <typename TIn, bool V4>
+struct ColRegs {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const TIn* __restrict__ row,
+                                       const int (&at)[4]) {
+    if constexpr (!V4) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(TIn) == 4) w[e] = __float_as_uint(row[at[e]]);
+        else w[e] = row[at[e]];
+      }
+    } else if constexpr (sizeof(TIn) == 4) {
+      const u32x4 a = __builtin_nontemporal_load(
+          reinterpret_cast<const u32x4*>(row + at[0]));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = a[e];
+    } else {
+      const uint2 a = *reinterpret_cast<const uint2*>(row + at[0]);
+      w[0] = a.x;
+      w[1] = a.y;
+    }
+  }
+  __device__ __forceinline__ f32x4 expand() const {
     f32x4 x;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = c + e < n ? row[c + e] : 0.f;
+    for (int e = 0; e < 4; ++e)
+      if constexpr (sizeof(TIn) == 4) x[e] = __uint_as_float(w[e]);
+      else if constexpr (!V4) x[e] = __uint_as_float(w[e] << 16);
+      else
+        x[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
     return x;
   }
-}
-template <bool V4>
-__device__ __forceinline__ f32x4 load_cols(const uint16_t* __restrict__ row,
-                                           int c, int n) {
-  f32x4 x = {0.f, 0.f, 0.f, 0.f};
-  if constexpr (V4) {
-    if (c < n) {
-      const uint2 w = *reinterpret_cast<const uint2*>(row + c);
-      x[0] = __uint_as_float(w.x << 16);
-      x[1] = __uint_as_float(w.x & 0xffff0000u);
-      x[2] = __uint_as_float(w.y << 16);
-      x[3] = __uint_as_float(w.y & 0xffff0000u);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (c + e < n) x[e] = __uint_as_float((uint32_t)row[c + e] << 16);
-  }
-  return x;
-}
+};
 template <bool V4>
 __device__ __forceinline__ void store_cols(float* __restrict__ row, int c,
                                            int n, f32x4 x) {
@@ -155,7 +157,8 @@ __device__ __forceinline__ float sum_groups(f32x4 y) {
 }
 
 // One head's chain over T tokens.  Pointers are at the first token's row of
-// the head; qs, vs, gs are the token strides.
+// the head; qs, vs, gs are the token strides.  Without o, q is not used (but
+// read: it may be k).
 template <int DK, typename TIn, bool V4>
 __device__ __forceinline__ void decay_chain(
     const TIn* __restrict__ q, const TIn* __restrict__ k,
@@ -166,22 +169,40 @@ __device__ __forceinline__ void decay_chain(
   const int lane = threadIdx.x & 63;
   const int c = col0 + 4 * (lane & 7), r0 = (lane >> 3) * R;
   f32x4 st[R];
+  int at[4];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
-    st[i] = s_in ? load_cols<V4>(s_in + (long)(r0 + i) * dv, c, dv)
-                 : f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int e = 0; e < 4; ++e)
+    at[e] = V4 ? (c < dv ? c : col0) : (c + e < dv ? c + e : col0);
+  // the inputs of the next token are on their way while one is computed
+  RowRegs<TIn, R> kr, qr;
+  ColRegs<TIn, V4> vr;
+  float gr;
+  auto fetch = [&](int t) {
+    kr.load(k + t * qs + r0);
+    qr.load(q + t * qs + r0);
+    vr.load(v + t * vs, at);
+    gr = g[t * gs];
+  };
+  fetch(0);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    ColRegs<float, V4> x;
+    x.load(s_in + (long)(r0 + i) * dv, at);
+    st[i] = x.expand();
+  }
   for (int t = 0; t < T; ++t) {
     float kk[R], qq[R];
-    load_row<TIn, R>(k + t * qs + r0, kk);
-    const f32x4 vv = load_cols<V4>(v + t * vs, c, dv);
-    const float a = expf(g[t * gs]);
+    kr.expand(kk);
+    qr.expand(qq);
+    const f32x4 vv = vr.expand();
+    const float a = expf(gr);
+    fetch(t + 1 < T ? t + 1 : t);
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         st[i][e] = __builtin_fmaf(kk[i], vv[e], a * st[i][e]);
     if (o) {
-      load_row<TIn, R>(q + t * qs + r0, qq);
       f32x4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < R; ++i)
@@ -203,7 +224,7 @@ template <int DK, typename TIn, bool V4>
 __global__ __launch_bounds__(256) void step_kernel(DecayArgs p,
                                                    gdn::LaneTable tl) {
   const int ncb = (p.d_v + kStepCols - 1) / kStepCols;
-  const long unit = (long)blockIdx.x * 4 + threadIdx.x / 64;
+  const long unit = (long)blockIdx.x * 4 + gdn::uniform(threadIdx.x / 64);
   const long item = unit / ncb;
   const int col0 = (int)(unit % ncb) * kStepCols;
   const int h = (int)(item % p.h_v);
@@ -218,7 +239,7 @@ __global__ __launch_bounds__(256) void step_kernel(DecayArgs p,
   const long qo = tok * ks + (long)hk * DK, vo = tok * vs + (long)h * p.d_v;
   const long so = item * DK * p.d_v;
   decay_chain<DK, TIn, V4>(
-      (const TIn*)p.q + qo, (const TIn*)p.k + qo, (const TIn*)p.v + vo,
+      (const TIn*)(p.o ? p.q : p.k) + qo, (const TIn*)p.k + qo, (const TIn*)p.v + vo,
       p.per_head ? p.g + (long)layer * p.h_v + h : p.g + tok * p.h_v + h,
       p.s_in + so, p.s_out ? p.s_out + so : nullptr, p.o ? p.o + vo : nullptr,
       ks, vs, p.per_head ? 0 : p.h_v, T, p.d_v, col0, p.scale);
