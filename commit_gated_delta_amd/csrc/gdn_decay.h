@@ -288,6 +288,7 @@ constexpr int kChunk = 64;
 // first[s + 1] - 1 of seg tokens each (the last one shorter).
 struct SegTable {
   int n, seg;
+  int cols;  // of d_v per workgroup
   int first[GDN_MAX_LANES + 1];
   int start[GDN_MAX_LANES + 1];  // token rows start[s] .. start[s + 1] - 1
 };
@@ -976,11 +977,15 @@ static long step_blocks(long states, int d_v) {
 // Measured for 7 f32 sequences of up to 1000 tokens on 8 heads: 68, 41, 27 us
 // with segments of at least 512, 256 and 128 tokens.  A call whose sequences
 // all have at most four chunks is not worth the two more launches.
+// Workgroups take 128 columns of d_v, or 64 where that is all there are or
+// where wider ones would not even be one per CU (kNarrowBlocks): with 64 a
+// chunk takes less time, if more in all.  1024 tokens x 16 heads 34 -> 28 us,
+// 200 x 32 heads 27 -> 19 us, 250 x 8 f32 heads 57 -> 36 us; with up to two a
+// CU 131,072 x 4 heads would take 289 against 250 us.
 constexpr int kTargetBlocks = 512;
 constexpr int kMinSeg = 2 * kChunk;
 constexpr int kWhole = 4 * kChunk;
-
-static int block_cols(int d_v) { return d_v <= 64 ? 64 : 128; }
+constexpr int kNarrowBlocks = 256;
 
 // The number of tokens, or -1 for bad lengths.
 static long plan_segments(int32_t n_seqs, const int32_t* seq_len, int h_v,
@@ -997,8 +1002,8 @@ static long plan_segments(int32_t n_seqs, const int32_t* seq_len, int h_v,
     if (seq_len[i] > longest) longest = seq_len[i];
     t.start[i + 1] = (int)tokens;
   }
-  const int w = block_cols(d_v);
-  const long work = chunks * h_v * ((d_v + w - 1) / w);
+  t.cols = d_v <= 64 ? 64 : 128;
+  const long work = chunks * h_v * ((d_v + t.cols - 1) / t.cols);
   long seg = (work + kTargetBlocks - 1) / kTargetBlocks * kChunk;
   if (seg < kMinSeg) seg = kMinSeg;
   if (longest <= kWhole) seg = kWhole;
@@ -1008,6 +1013,9 @@ static long plan_segments(int32_t n_seqs, const int32_t* seq_len, int h_v,
     const long n = (seq_len[i] + seg - 1) / seg;
     t.first[i + 1] = t.first[i] + (int)(n < 1 ? 1 : n);
   }
+  // with less than a workgroup per CU, narrower ones are done sooner
+  if ((long)t.first[n_seqs] * h_v * ((d_v + t.cols - 1) / t.cols) <= kNarrowBlocks)
+    t.cols = 64;
   return tokens;
 }
 
@@ -1023,9 +1031,8 @@ static size_t workspace_bytes(const SegTable& t, int h_v, int d_k, int d_v) {
 }
 
 template <int MODE, typename... Args>
-static hipError_t launch_chunks(int d_k, int d_v, int in_dtype, bool vec,
+static hipError_t launch_chunks(int d_k, int d_v, int w, int in_dtype, bool vec,
                                 long items, hipStream_t st, Args&&... args) {
-  const int w = block_cols(d_v);
   const dim3 grid((unsigned)(items * ((d_v + w - 1) / w)));
   auto go = [&](auto dk, auto cw, auto t, auto v) {
     return launch(chunk_kernel<decltype(dk)::value, decltype(cw)::value,
@@ -1142,7 +1149,7 @@ extern "C" int gdn_decay_prefill(int32_t n_seqs, const int32_t* seq_len,
     return fail(GDN_EINVAL,
                 "gdn_decay_prefill: pointers must be 16-byte aligned");
   if (tokens == 0 && !S_final) return GDN_OK;
-  const int w = block_cols(d_v), segs = tab.first[n_seqs];
+  const int w = tab.cols, segs = tab.first[n_seqs];
   const double scan = ((double)d_k * d_v + 255) / 256;
   if ((double)segs * h_v * ((d_v + w - 1) / w) > (double)INT_MAX ||
       (double)n_seqs * h_v * scan > (double)INT_MAX)
@@ -1154,7 +1161,7 @@ extern "C" int gdn_decay_prefill(int32_t n_seqs, const int32_t* seq_len,
     p.slots = (float*)workspace;
     p.decay = (float*)((char*)workspace +
                        (slots_bytes(tab, h_v, d_k, d_v) + 255) / 256 * 256);
-    e = launch_chunks<kStates>(d_k, d_v, in_dtype, vec,
+    e = launch_chunks<kStates>(d_k, d_v, w, in_dtype, vec,
                               (long)(segs - n_seqs) * h_v, st, p, tab, 0);
     if (e == hipSuccess)
       e = launch(segment_scan_kernel,
@@ -1164,10 +1171,10 @@ extern "C" int gdn_decay_prefill(int32_t n_seqs, const int32_t* seq_len,
   }
   // without outputs only the last segments are left to run
   if (e == hipSuccess && o)
-    e = launch_chunks<kOutput>(d_k, d_v, in_dtype, vec, (long)segs * h_v, st,
+    e = launch_chunks<kOutput>(d_k, d_v, w, in_dtype, vec, (long)segs * h_v, st,
                                p, tab, 0);
   else if (e == hipSuccess)
-    e = launch_chunks<kStates>(d_k, d_v, in_dtype, vec, (long)n_seqs * h_v, st,
+    e = launch_chunks<kStates>(d_k, d_v, w, in_dtype, vec, (long)n_seqs * h_v, st,
                                p, tab, 1);
   return gdn::hip_status(e, "gdn_decay_prefill launch");
 }
