@@ -134,17 +134,27 @@ __device__ __forceinline__ void write_top(const ScoreArgs& p, long row,
 constexpr int kList = 512;
 constexpr int kStrict = kList - 4 * GDN_MAX_TOP;  // room for those above tau
 
+// Whether a row's slices, of N logits per thread at most, are equally long: a
+// short last one has few threads with logits, and then the alternatives take
+// the slow way (53 rows x 2214 logits, top 20: 20 -> 14 us).  Slices of many
+// logits are full, which keeps their ids simple (108 -> 75 us for 1024 rows x
+// 131,072).
+template <int N>
+constexpr bool kEven = N == 8;
+
 // The n largest of a slice when more than the list holds is at least tau (or
 // tau is -inf, where entries that stand for no logit look the same).
 template <typename TIn, int V, typename Put>
 __device__ __forceinline__ void pick_tied(
     const ScoreArgs& p, const float (&val)[V][16 / sizeof(TIn)], uint32_t tau,
-    int first, int skew, int& listed, uint32_t* list_key, int* list_id,
-    Put&& put) {
+    int first, int end, int skew, int& listed, uint32_t* list_key,
+    int* list_id, Put&& put) {
   constexpr int E = 16 / sizeof(TIn);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   auto id_of = [&](int c, int e) {
-    return (first + c * kThreads) * E - skew + e;
+    const int i = first + c * kThreads;
+    // (no id behind the end of an even slice; other slices end with the row)
+    return kEven<V * E> && i >= end ? -1 : i * E - skew + e;
   };
   __syncthreads();
   if (tid == 0) listed = 0;
@@ -280,17 +290,19 @@ __global__ __launch_bounds__(kThreads, 4) void slice_kernel(ScoreArgs p) {
   const int skew = (int)((uintptr_t)x % 16 / sizeof(TIn));
   const u32x4* line = reinterpret_cast<const u32x4*>(x - skew);
   const int lines = (p.vocab + skew + E - 1) / E;
-  const int first = slice * (kThreads * V) + tid;
+  const int per = kEven<V * E> ? (lines + p.slices - 1) / p.slices : kThreads * V;
+  const int first = slice * per + tid;
+  const int end = (slice + 1) * per < lines ? (slice + 1) * per : lines;
 
   u32x4 raw[V];
 #pragma unroll
   for (int c = 0; c < V; ++c) {
     const int i = first + c * kThreads;
-    raw[c] = line[i < lines ? i : lines - 1];
+    raw[c] = line[i < end ? i : lines - 1];
   }
 #pragma unroll
   for (int c = 0; c < V; ++c) {
-    const int id = (first + c * kThreads) * E - skew;
+    const int i = first + c * kThreads, id = i < end ? i * E - skew : p.vocab;
     if (id < 0 || id > p.vocab - E) {
 #pragma unroll
       for (int e = 0; e < E; ++e)
@@ -407,8 +419,14 @@ __global__ __launch_bounds__(kThreads, 4) void slice_kernel(ScoreArgs p) {
       }
     };
     const int entries = listed;
+    const int begin = slice == 0 ? 0 : slice * per * E - skew;
+    const int stop = end * E - skew < p.vocab ? end * E - skew : p.vocab;
+    const int have = stop - begin < 0 ? 0 : stop - begin;
+    const int wanted = have < p.n_top ? have : p.n_top;
     if (alone && r.bad) {  // (a negative NaN is in none of the lists)
       if (tid < p.n_top) write_top(p, row, r, tid, 0.f, -1);
+    } else if (m == -INFINITY) {  // nothing but -inf: the lowest ids
+      if (tid < wanted) put(tid, key_of(-INFINITY), begin + tid);
     } else if (entries <= kList && tau > key_of(-INFINITY)) {
       for (int i = tid; i < entries; i += kThreads) {
         const uint32_t key = list_key[i];
@@ -423,27 +441,24 @@ __global__ __launch_bounds__(kThreads, 4) void slice_kernel(ScoreArgs p) {
       }
     } else {
       tau = search(tau, 15, 0);
-      pick_tied<TIn, V>(p, val, tau, first, skew, listed, list_key, list_id, put);
+      pick_tied<TIn, V>(p, val, tau, first, end, skew, listed, list_key, list_id,
+                        put);
     }
-    // a slice of fewer logits than n
-    if (!alone && tid == 0) {
-      const int from = slice * (kThreads * V) * E - skew;
-      const int begin = from < 0 ? 0 : from;
-      const int end = from + kThreads * V * E < p.vocab ? from + kThreads * V * E
-                                                        : p.vocab;
-      const int have = end - begin;
-      p.parts[part].n = have < p.n_top ? have : p.n_top;
-    }
+    if (!alone && tid == 0) p.parts[part].n = wanted;
   }
 }
 
-// Joins the slices of a row, one wave each (11 us for 1024 rows of 16 lists of
-// 20, 5 us for 16 rows): the sums, then the n largest by
-// taking the largest head of the slices' lists n times.  A lane keeps the
-// lists of K consecutive slices, so that equal logits are met lowest id
-// first.
-constexpr int kJoinList = 2048;
-
+// Joins the slices of a row: the sums (every wave for itself), then as in a
+// slice: with tau at most the n-th largest of 256 sampled entries, the first
+// ones of every list, what is at least tau goes to a list in LDS (a little
+// more than n entries), whose entries count the ones before them.  Should
+// they not fit (equal logits in many slices), the first wave takes the largest
+// head of the lists n times; a lane keeps the lists of K consecutive slices,
+// so that equal logits are met lowest id first.
+// Bound by its launch and three loads in a row: 9 us for 1024 rows of 16 lists
+// of 20, 5 us for 16 rows.  (Taking the largest head of the lists n times from
+// the start took 11 and 5 us, and 9 to 16 us for few rows of lists of 20 to
+// 32, now 4 to 8.)
 template <int CTRL, int ROWS>
 __device__ __forceinline__ uint32_t dpp_max_key(uint32_t x) {
   const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL,
@@ -460,11 +475,34 @@ __device__ __forceinline__ uint32_t wave_max_key(uint32_t x) {
   return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
 }
 
-template <typename TIn>
-__global__ __launch_bounds__(64) void join_kernel(ScoreArgs p) {
-  const int lane = threadIdx.x;
+template <typename TIn, bool TOP>
+__global__ __launch_bounds__(TOP ? kThreads : 64) void join_kernel(ScoreArgs p) {
+  __shared__ __attribute__((aligned(16))) uint32_t sample_of[kThreads];
+  __shared__ uint32_t list_key[TOP ? kList : 1];
+  __shared__ int list_id[TOP ? kList : 1];
+  __shared__ int listed;
+  const int tid = threadIdx.x, lane = tid & 63;
   const long row = blockIdx.x;
   const Part* parts = p.parts + row * p.slices;
+  const int all = p.slices * p.n_top;
+  const float* values = p.values + row * all;
+  const int* ids = p.ids + row * all;
+  uint32_t sample = 0;  // (below every key)
+  if constexpr (TOP) {
+    if (p.slices <= kThreads) {
+      const int s = tid % p.slices, i = tid / p.slices;
+      if (i < p.n_top && i < parts[s].n)
+        sample = key_of(values[s * p.n_top + i]);
+    } else {
+      for (int s = tid; s < p.slices; s += kThreads)
+        if (parts[s].n > 0) {
+          const uint32_t k = key_of(values[s * p.n_top]);
+          sample = k > sample ? k : sample;
+        }
+    }
+    sample_of[tid] = sample;
+    if (tid == 0) listed = 0;
+  }
   float m = -INFINITY;
   bool bad = false;
   for (int i = lane; i < p.slices; i += 64) {
@@ -485,69 +523,89 @@ __global__ __launch_bounds__(64) void join_kernel(ScoreArgs p) {
   w = gdn::wave_sum(w);
   if (__any(bad)) z = NAN;
   const RowSums r = row_sums(m, z, w, p.it);
-  if (lane == 0) write_row<TIn>(p, row, r);
-  if (p.n_top == 0) return;
-
-  // the lists, in LDS when they fit
-  __shared__ float lds_values[kJoinList];
-  __shared__ int lds_ids[kJoinList];
-  const int K = (p.slices + 63) / 64, all = p.slices * p.n_top;
-  const float* values = p.values + row * all;
-  const int* ids = p.ids + row * all;
-  if (all <= kJoinList) {
-    for (int i = lane; i < all; i += 64) {
-      lds_values[i] = values[i];
-      lds_ids[i] = ids[i];
+  if (tid == 0) write_row<TIn>(p, row, r);
+  if constexpr (TOP) {
+    if (r.bad) {  // (the lists may lack entries)
+      if (tid < p.n_top) write_top(p, row, r, tid, 0.f, -1);
+      return;
     }
     __syncthreads();
-    values = lds_values;
-    ids = lds_ids;
-  }
-  uint32_t last = 0xffffffffu;
-  int last_id = -1;
-  // head of the lane's lists: the first of what comes after (last, last_id)
-  uint32_t key = 0;  // 0: none left
-  float value = 0.f;
-  int id = 0, taken = 0;
-  const int mine = K == 1 && lane < p.slices ? parts[lane].n : 0;
-  auto head = [&]() {
-    key = 0;
-    if (K == 1) {  // one list, taken in order
-      if (taken < mine) {
-        value = values[lane * p.n_top + taken];
-        id = ids[lane * p.n_top + taken];
-        key = key_of(value);
+    const u32x4 of4 = *reinterpret_cast<const u32x4*>(&sample_of[4 * lane]);
+    uint32_t tau = 0;
+    for (int b = 31; b >= 16; --b) {
+      const uint32_t t = tau | 1u << b;
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n += __popcll(__ballot(of4[i] >= t));
+      if (n >= p.n_top) tau = t;
+    }
+    for (int i = tid; i < all; i += kThreads) {
+      const uint32_t key = key_of(values[i]);
+      if (key < tau) continue;
+      const int s = i / p.n_top;
+      if (i - s * p.n_top >= parts[s].n) continue;
+      const int slot = atomicAdd(&listed, 1);
+      if (slot < kList) {
+        list_key[slot] = key;
+        list_id[slot] = ids[i];
+      }
+    }
+    __syncthreads();
+    const int entries = listed;
+    if (entries <= kList) {
+      for (int i = tid; i < entries; i += kThreads) {
+        const uint32_t key = list_key[i];
+        const int id = list_id[i];
+        int place = 0;
+#pragma unroll 4
+        for (int j = 0; j < entries; ++j) {
+          const uint32_t k = list_key[j];
+          place += k > key || (k == key && list_id[j] < id);
+        }
+        if (place < p.n_top)
+          write_top(p, row, r, place,
+                    __uint_as_float(key >> 31 ? key & 0x7fffffffu : ~key), id);
       }
       return;
     }
-    for (int k = 0; k < K; ++k) {
-      const int s = lane * K + k;
-      if (s >= p.slices) break;
-      const int n = parts[s].n;
-      for (int i = 0; i < n; ++i) {
-        const float v = values[s * p.n_top + i];
-        const uint32_t q = key_of(v);
-        const int j = ids[s * p.n_top + i];
-        if (q > last || (q == last && j <= last_id)) continue;
-        if (q > key) {
-          key = q;
-          value = v;
-          id = j;
+    if (tid >= 64) return;
+    const int K = (p.slices + 63) / 64;
+    uint32_t last = 0xffffffffu;
+    int last_id = -1;
+    // head of the lane's lists: the first of what comes after (last, last_id)
+    uint32_t key = 0;  // 0: none left
+    float value = 0.f;
+    int id = 0;
+    auto head = [&]() {
+      key = 0;
+      for (int k = 0; k < K; ++k) {
+        const int s = lane * K + k;
+        if (s >= p.slices) break;
+        const int n = parts[s].n;
+        for (int i = 0; i < n; ++i) {
+          const float v = values[s * p.n_top + i];
+          const uint32_t q = key_of(v);
+          const int j = ids[s * p.n_top + i];
+          if (q > last || (q == last && j <= last_id)) continue;
+          if (q > key) {
+            key = q;
+            value = v;
+            id = j;
+          }
+          break;
         }
-        break;
       }
-    }
-  };
-  head();
-  for (int place = 0; place < p.n_top; ++place) {
-    const uint32_t best = wave_max_key(key);
-    const int win = __builtin_ctzll(__ballot(key == best));
-    last = best;
-    last_id = __builtin_amdgcn_readlane(id, win);
-    if (lane == win) {
-      write_top(p, row, r, place, value, id);
-      ++taken;
-      head();
+    };
+    head();
+    for (int place = 0; place < p.n_top; ++place) {
+      const uint32_t best = wave_max_key(key);
+      const int win = __builtin_ctzll(__ballot(key == best));
+      last = best;
+      last_id = __builtin_amdgcn_readlane(id, win);
+      if (lane == win) {
+        write_top(p, row, r, place, value, id);
+        head();
+      }
     }
   }
 }
@@ -589,7 +647,9 @@ static hipError_t run(const ScoreArgs& p, int v, hipStream_t st) {
     e = top ? launch(slice_kernel<TIn, kFew, true>, grid, block, st, p)
             : launch(slice_kernel<TIn, kFew, false>, grid, block, st, p);
   if (e != hipSuccess || p.slices == 1) return e;
-  return launch(join_kernel<TIn>, dim3((unsigned)p.rows), dim3(64), st, p);
+  const dim3 rows((unsigned)p.rows);
+  return top ? launch(join_kernel<TIn, true>, rows, block, st, p)
+             : launch(join_kernel<TIn, false>, rows, dim3(64), st, p);
 }
 
 }  // namespace gdnt

@@ -63,6 +63,9 @@ def _logits(rows, vocab, kind, spread=3.0, seed=0):
     (300, 5003, 3, "bf16", 1.0),
     (1, 262144, 32, "bf16", 1.0),
     (700, 1537, 1, "f32", 1.0),
+    (2, 600001, 5, "bf16", 1.0),          # more slices than threads
+    (53, 2214, 20, "bf16", 1.0),
+    (3, 300007, 32, "f32", 1.0),
 ])
 def test_scores(rows, vocab, top, kind, it):
     x, t = _logits(rows, vocab, kind)
@@ -79,6 +82,17 @@ def test_ties_go_to_the_lowest_id():
     for kind in ("bf16", "f32"):
         _check(x.to(TYPES[kind]), t, 32)
         _check(x.to(TYPES[kind])[:, :900], t, 20)
+
+
+def test_slices_without_logits():
+    """Slices of nothing but -inf between others, and too few logits left."""
+    x, t = _logits(4, 40003, "bf16")
+    x[0, 2000:30000] = -math.inf
+    x[1, :39990] = -math.inf
+    x[2, 7:] = -math.inf
+    x[3, 1::2] = -math.inf
+    _check(x, t, 32)
+    _check(x.float(), t, 20)
 
 
 def test_ascending_and_descending_rows():
