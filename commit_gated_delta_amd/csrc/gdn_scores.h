@@ -458,7 +458,7 @@ __global__ __launch_bounds__(kThreads, 4) void slice_kernel(ScoreArgs p) {
 // Bound by its launch and three loads in a row: 9 us for 1024 rows of 16 lists
 // of 20, 5 us for 16 rows.  (Taking the largest head of the lists n times from
 // the start took 11 and 5 us, and 9 to 16 us for few rows of lists of 20 to
-// 32, now 4 to 8.)
+// 32, now 6 to 8.)
 template <int CTRL, int ROWS>
 __device__ __forceinline__ uint32_t dpp_max_key(uint32_t x) {
   const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL,
