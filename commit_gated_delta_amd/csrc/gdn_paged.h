@@ -873,21 +873,28 @@ static KvArgs kv_args(const gdn_kv_dims& d, const void* k, const void* v,
 // 780, 618, 588, 584 us with 512, 1024, 1536, 2048 workgroups (more of them
 // even out the memory's latency); for 8 lanes x 4 heads x 8k..16k, 128 rows:
 // 121, 93, 117, 110 us with 256, 512, 768, 1024 (two a CU run at once, and
-// every split of 128 rows leaves 64 KiB to join).
+// every split of 128 rows leaves 64 KiB to join).  Rows of 512 bytes and more
+// leave one workgroup of attend_kernel per CU, whose start and end nothing
+// hides, so there are as many as CUs (kWideBlocks): d = 256, bf16, 2 heads, 8
+// lanes x 4k..8k: 32, 37, 37, 49, 49 us with 256, 512, 768, 1024, 2048; one
+// lane x 30k: 23 us, and 30 with any more; 66 lanes x up to 8.5k: 102, 106,
+// 108, 119, 128 us; f32, d = 128, 16 lanes x 8 heads: 124, 105, 102, 109, 119.
 constexpr int kRowsBlocks = 512;
+constexpr int kWideBlocks = 256;
 
 struct Shape {
   int rows, rt, waves, groups, target, items, slots;
   bool few;
 };
-static Shape shape_of(const gdn_kv_dims& d) {
+static Shape shape_of(const gdn_kv_dims& d, int size) {
   Shape s;
   s.rows = d.t_max * (d.h_q / d.h_kv);
   s.few = s.rows <= (d.d < 256 ? 32 : 16);
   s.rt = s.few && s.rows > 16 ? 2 : 1;
   s.waves = !s.few && s.rows > 64 && d.d < 256 ? 8 : 4;
   s.groups = s.few ? 1 : (s.rows + 16 * s.waves - 1) / (16 * s.waves);
-  const int items = (s.few ? kFewBlocks : kRowsBlocks) / (d.h_kv * s.groups);
+  const int blocks = !s.few ? kRowsBlocks : d.d * size < 512 ? kFewBlocks : kWideBlocks;
+  const int items = blocks / (d.h_kv * s.groups);
   s.target = items - d.n_lanes > items / 2 ? items - d.n_lanes : items / 2;
   if (s.target < 1) s.target = 1;
   const long units = ((long)d.max_pages * d.page_size + kUnit - 1) / kUnit;
@@ -896,8 +903,9 @@ static Shape shape_of(const gdn_kv_dims& d) {
   s.slots = 2l * s.target < most ? 2 * s.target : (int)most;
   return s;
 }
+// (bf16 never needs less)
 static size_t attend_bytes(const gdn_kv_dims& d) {
-  const Shape s = shape_of(d);
+  const Shape s = shape_of(d, 2);
   const size_t n = (size_t)s.slots * d.h_kv * s.rows;
   return n * (d.d + 2) * sizeof(float);
 }
@@ -977,7 +985,7 @@ extern "C" int gdn_paged_attention(const gdn_kv_dims* dims,
   rc = check_lanes(fn, *dims, t_lane, tl, any);
   if (rc != GDN_OK) return rc;
   if (!any) return GDN_OK;
-  const Shape s = shape_of(*dims);
+  const Shape s = shape_of(*dims, dtype == GDN_BF16 ? 2 : 4);
   AttendArgs p;
   p.kv = kv_args(*dims, k_cache, v_cache, page_table, kv_len);
   p.q = q;
