@@ -220,8 +220,9 @@ struct Rows {
           for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[r][h][e]);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
+        // (where both are -inf there is nothing to rescale: l counts, below)
         const float keep =
-            m[r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[r] - top);
+            top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[r] - top);
         m[r] = top;
         l[r] *= keep;
 #pragma unroll
@@ -238,6 +239,14 @@ struct Rows {
           sc[r][h][e] = __builtin_amdgcn_exp2f(sc[r][h][e] - ref);
           l[r] += sc[r][h][e];
         }
+      // As long as m is -inf, l counts the steps with a position that the row
+      // sees: scores of -inf alone have no softmax, which is not the same as
+      // no position.  (Rows past the last one have end 0.)
+      if (m[r] == -INFINITY && p0 < end[r]) {
+        const uint32_t seen = whole ? ~0u : ok;
+        if (end[r] - p0 >= 32 ? seen : seen & ((1u << (end[r] - p0)) - 1))
+          l[r] += 1.f;
+      }
     }
   }
   // O^T += V^T P^T with V rows r0 .. r0 + 31 of the tile.
@@ -329,14 +338,15 @@ __device__ __forceinline__ void stage_q(T* Qs, const AttendArgs& p, int lane,
 }
 
 // Where a row's result goes: o, when the lane has one split, or the split's
-// slot (unnormalised, with its m and l).
+// slot (unnormalised, with its m and l).  A row that saw nothing (l = 0) gets
+// zeros, one that saw scores of -inf alone NaN.
 __device__ __forceinline__ float* row_out(const AttendArgs& p, const Split& s,
                                           int hk, int row, int d, float m,
                                           float l, bool first, float& scale) {
   const KvArgs& a = p.kv;
   const int group = a.h_q / a.h_kv;
   if (s.n == 1) {
-    scale = l == 0.f ? 0.f : 1.f / l;
+    scale = l == 0.f ? 0.f : m == -INFINITY ? NAN : 1.f / l;
     return p.o + (((long)s.lane * a.t_max + row / group) * a.h_q + hk * group +
                   row % group) * d;
   }
@@ -544,10 +554,9 @@ __global__ __launch_bounds__(256, D * sizeof(T) >= 512 ? 1 : 2) void attend_kern
     for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w][0][row]);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const float mw = ml[w][0][row];
-      if (mw != -INFINITY || ml[w][1][row] != 0.f)
-        tot += ml[w][1][row] *
-               (mw == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mw - top));
+      tot += ml[w][1][row] *
+             (top == -INFINITY ? 1.f
+                               : __builtin_amdgcn_exp2f(ml[w][0][row] - top));
       y += *reinterpret_cast<const f32x4*>(
           reinterpret_cast<const float*>(pool + w * kPer) + row * kSumPitch + c);
     }
@@ -752,7 +761,8 @@ __global__ __launch_bounds__(64 * NW) void join_kernel(AttendArgs p,
   for (int w = 0; w < NW; ++w) m = fmaxf(m, tops[w]);
   for (int i = tid; i < s.n; i += 64 * NW) {
     if (i != tid) mine = ml[i * step];
-    // (a split that saw nothing has no weight; one with a NaN keeps it)
+    // (a split that saw nothing has no weight, one with a NaN keeps it, and
+    // where all that was seen scored -inf the weights are NaN)
     const float w = mine.x == -INFINITY && mine.y == 0.f
                         ? 0.f
                         : __builtin_amdgcn_exp2f(mine.x - m);

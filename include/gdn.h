@@ -523,8 +523,9 @@ typedef struct {
  *               them; taken as 0..max_pages*page_size
  *   o           device f32 [n_lanes][t_max][h_q][d]: softmax over positions
  *               0 .. kv_len - t_lane + t of scale * (q_t . k), times v.  A
- *               token that sees no position gets zeros.  What masked rows of
- *               the cache hold (NaN, infinities) does not matter.
+ *               token that sees no position gets zeros, one whose scores are
+ *               all -inf (products past f32 among them) NaN.  What masked
+ *               rows of the cache hold (NaN, infinities) does not matter.
  *   workspace   device, ws_bytes >= gdn_paged_attention_workspace_bytes(dims)
  *               (which depends on the dims alone; 0 for invalid dims); calls
  *               that overlap in time need workspaces of their own
