@@ -220,9 +220,8 @@ struct Rows {
           for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[r][h][e]);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        // (where both are -inf there is nothing to rescale: l counts, below)
         const float keep =
-            top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[r] - top);
+            m[r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[r] - top);
         m[r] = top;
         l[r] *= keep;
 #pragma unroll
@@ -239,14 +238,6 @@ struct Rows {
           sc[r][h][e] = __builtin_amdgcn_exp2f(sc[r][h][e] - ref);
           l[r] += sc[r][h][e];
         }
-      // As long as m is -inf, l counts the steps with a position that the row
-      // sees: scores of -inf alone have no softmax, which is not the same as
-      // no position.  (Rows past the last one have end 0.)
-      if (m[r] == -INFINITY && p0 < end[r]) {
-        const uint32_t seen = whole ? ~0u : ok;
-        if (end[r] - p0 >= 32 ? seen : seen & ((1u << (end[r] - p0)) - 1))
-          l[r] += 1.f;
-      }
     }
   }
   // O^T += V^T P^T with V rows r0 .. r0 + 31 of the tile.
@@ -309,12 +300,33 @@ struct Rows {
       }
     }
   }
-  __device__ __forceinline__ void finish() {
+  // Sums l.  The wave's steps were those of 32 positions from p0, p0 + stride,
+  // .. on, before stop.  A row whose m is still -inf has seen no position
+  // (l = 0), or scores of -inf alone, which have no softmax: l = 1 then.  Told
+  // apart here, where it costs the steps nothing (a count there made windows
+  // of 16 1 % slower).
+  __device__ __forceinline__ void finish(const KvArgs& a, const int* table,
+                                         int p0, int stride, int stop) {
+    bool open = false;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       l[r] += __shfl_xor(l[r], 16);
       l[r] += __shfl_xor(l[r], 32);
+      open |= m[r] == -INFINITY && p0 < end[r];
     }
+    if (!__any(open)) return;
+    int first = stop;  // first position that is there
+#pragma unroll 1
+    for (; p0 < stop && first == stop; p0 += stride) {
+      const int pos = p0 + (threadIdx.x & 31);
+      const bool there =
+          pos < stop && (unsigned)table[page_of(a, pos)] < (unsigned)a.n_pages;
+      const uint32_t hit = (uint32_t)__ballot(there);
+      if (hit) first = p0 + __builtin_ctz(hit);
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      if (m[r] == -INFINITY && first < stop && first < end[r]) l[r] += 1.f;
   }
 };
 
@@ -362,9 +374,10 @@ __device__ __forceinline__ float* row_out(const AttendArgs& p, const Split& s,
 // Few rows: four waves share out a split's positions, 32 at a step.  The next
 // step's K rows are loaded when this step's scores are done and its V rows
 // when V is in LDS, page numbers a step earlier.  Bound by HBM: 32 lanes x 8
-// heads x 16k..32k positions of 128, bf16, 3.3 GB in 579 us (5.7 TB/s).  Short
-// caches by the chain of loads length - page - rows (8 lanes x 2 heads x 1k
-// positions of 256: 12 us).
+// heads x 16k..32k positions of 128, bf16, 3.3 GB in 582 us (5.7 TB/s).  Short
+// caches by what comes in turn (8 lanes x 2 heads of 256): 5.3 us with empty
+// caches (launch, lengths, search of the split, q), 8 with one step of one
+// wave, 10.6 with one of all four and their sum, 11.7 with eight splits.
 template <int D, typename T, int RT>
 __global__ __launch_bounds__(256, D * sizeof(T) >= 512 ? 1 : 2) void attend_kernel(
     AttendArgs p, gdn::LaneTable tl) {
@@ -523,7 +536,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) >= 512 ? 1 : 2) void attend_kern
 
   // the four waves' results: each scaled to the common maximum, written to
   // LDS and added up by all threads
-  x.finish();
+  x.finish(a, table, begin + 32 * wave, 128, stop);
   if (g4 == 0)
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -691,7 +704,7 @@ void rows_kernel(AttendArgs p, gdn::LaneTable tl) {
       if (is_odd) x.special(a, s.lane, hk, p0, stop);
     }
   }
-  x.finish();
+  x.finish(a, table, begin, 32, stop);
   const int row = row0 + 16 * wave + n;
   if (row >= rows) return;
   float f;
@@ -882,8 +895,10 @@ static KvArgs kv_args(const gdn_kv_dims& d, const void* k, const void* v,
 // units.  Measured, for 32 lanes x 8 heads x 16k..32k positions, one token:
 // 780, 618, 588, 584 us with 512, 1024, 1536, 2048 workgroups (more of them
 // even out the memory's latency); for 8 lanes x 4 heads x 8k..16k, 128 rows:
-// 121, 93, 117, 110 us with 256, 512, 768, 1024 (two a CU run at once, and
-// every split of 128 rows leaves 64 KiB to join).  Rows of 512 bytes and more
+// 121, 93, 117, 110 us with 256, 512, 768, 1024 (two a CU run at once there,
+// d = 128 in bf16, and every split of 128 rows leaves 64 KiB to join; d = 256,
+// and d = 128 in f32 with eight waves, fit one a CU and take the same number
+// without a measurement of their own).  Rows of 512 bytes and more
 // leave one workgroup of attend_kernel per CU, whose start and end nothing
 // hides, so there are as many as CUs (kWideBlocks): d = 256, bf16, 2 heads, 8
 // lanes x 4k..8k: 32, 37, 37, 49, 49 us with 256, 512, 768, 1024, 2048; one
