@@ -279,9 +279,11 @@ __global__ __launch_bounds__(256) void step_kernel(DecayArgs p,
 // segments at once.
 //
 // Measured, 32,768 tokens x 32 heads of 128, bf16: states pass 126 us (540 MB,
-// 4.3 TB/s), scan 14 us, output pass 301..317 us (1.39 GB, 4.5 TB/s; matrix
-// cores 41 % and vector ALUs 48 % busy, next to each other rather than at
-// once: two waves per SIMD are all that 250 registers leave).
+// 4.3 TB/s), scan 14 us, output pass 301..317 us (1.39 GB, 4.5 TB/s).  Bound
+// by the bytes, at nine tenths and more of a copy's 4.75 TB/s: 2.0 GB in all
+// where 1.35 would do, since both passes read K and V from HBM.  (Matrix
+// cores 41 % and vector ALUs 48 % busy in the output pass, two waves per SIMD
+// being all that 250 registers leave.)
 constexpr int kChunk = 64;
 
 // Segments of the sequences: sequence s has the segments first[s] ..

@@ -270,7 +270,8 @@ __device__ __forceinline__ void pick_tied(
 //
 // Bound by vector instructions, about nine per logit for the sums and a
 // quarter of its time for the alternatives: 1024 rows x 131,072 bf16 logits,
-// top 20, in 74 us (3.6 TB/s); 16 f32 rows in 6.5 us.  (64 logits a thread
+// top 20, in 76 us (3.6 TB/s) with the vector ALUs issuing in every cycle; 16
+// f32 rows in 6.5 us.  (64 logits a thread
 // took too many registers, 269 us; a tau per wave instead of per workgroup
 // left four times the entries, 190 us.)
 template <typename TIn, int V, bool TOP>

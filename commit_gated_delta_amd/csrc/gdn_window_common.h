@@ -1,7 +1,8 @@
 // gdn_window_common.h -- pieces shared by the window kernels (gated delta
 // rule and its per-channel-decay sibling): sizes, lane tables, device
-// helpers and host-side launch plumbing.  Included by gdn_window.hip and
-// gdn_kda.hip only.
+// helpers and host-side launch plumbing.  The serving operators
+// (gdn_decay.h, gdn_paged.h, gdn_scores.h) use the lane tables, the wave
+// helpers and the launch plumbing.
 #pragma once
 #include <hip/hip_runtime.h>
 

@@ -484,6 +484,9 @@ size_t gdn_decay_prefill_workspace_bytes(int32_t n_seqs,
  *   flags    GDN_FLAG_HEAD_DECAY or 0
  * Sizes: d_k 16, 32, 64 or 128, d_v 1..1024, h_v a multiple of h_k.
  * Device pointers must be 16-byte aligned, g 4-byte (GDN_EINVAL).
+ * The same call gives the same bits every time.  A sequence's last bits may
+ * differ with what it is packed with: long sequences run in segments whose
+ * length follows from the work of the whole call.
  */
 int gdn_decay_prefill(int32_t n_seqs, const int32_t* seq_len, int32_t h_v,
                       int32_t h_k, int32_t d_k, int32_t d_v, const void* q,
@@ -532,7 +535,11 @@ typedef struct {
  * Query head h reads key-value head h / (h_q / h_kv).  page_table and kv_len
  * are read when the kernels run, so a captured call follows them.  Scores,
  * softmax sums and outputs are f32 or wider.  q, the caches, o and the
- * workspace must be 16-byte aligned (GDN_EINVAL).
+ * workspace must be 16-byte aligned (GDN_EINVAL).  The same call gives the
+ * same bits every time.  A token's last bits may differ with the other lanes'
+ * lengths and with its window: positions are split by the lengths of all
+ * lanes, and the tokens and heads that share a key-value head are rescaled
+ * together.
  */
 size_t gdn_paged_attention_workspace_bytes(const gdn_kv_dims* dims);
 int gdn_paged_attention(const gdn_kv_dims* dims, const int32_t* t_lane,
