@@ -109,7 +109,11 @@ __device__ __forceinline__ RowSums row_sums(float m, float z, float w,
 }
 __device__ __forceinline__ float log_p(const ScoreArgs& p, const RowSums& r,
                                        float x) {
-  return r.bad ? NAN : r.empty ? -INFINITY : (x - r.m) * p.it - r.lz;
+  // (halves: the difference of two logits may be past f32 where its product
+  // with a small inverse temperature is not)
+  return r.bad     ? NAN
+         : r.empty ? -INFINITY
+                   : (0.5f * x - 0.5f * r.m) * (2.f * p.it) - r.lz;
 }
 template <typename TIn>
 __device__ __forceinline__ void write_row(const ScoreArgs& p, long row,
