@@ -193,3 +193,12 @@ def test_rows_at_odd_offsets_and_strides(kind):
         _check(part, t % vocab, 20)
     wide, _ = _logits(2 * rows, 16384, kind)
     _check(wide[::2], t, 32)
+
+
+@pytest.mark.parametrize("rows,vocab", SIZES)
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_without_alternatives(rows, vocab, kind):
+    assert_many(rows, vocab)
+    x, t = _logits(rows, vocab, kind)
+    x[3::5, 11:] = -math.inf
+    _check(x, t, 0, 1.25)
