@@ -197,7 +197,7 @@ def _keep(s):
         s["dims"] = gdn.KvDims.of(c["lanes"], c["window"], c["h_q"], c["h_kv"], c["d"], c["page"],
                                   cache.shape[0], s["table"].shape[1])
         if op == "attend":
-            need = gdn.paged_attention_fp4_workspace_bytes(s["dims"])
+            need = gdn.paged_attention_mxfp_workspace_bytes(s["dims"])
     s["workspace"] = torch.empty(need, dtype=torch.uint8, device="cuda")
 
 
@@ -250,7 +250,7 @@ def _own_append_fp4(s):
     c = s["case"]
     q = torch.empty(s["q"].shape, dtype=s["q"].dtype, device="cuda")
     k, v = (torch.empty(s["k"].shape, dtype=torch.bfloat16, device="cuda") for _ in range(2))
-    _gdn().rope_append_fp4(s["dims"], s["t_lane"], s["q"], s["k"], s["v"], s["inv_freq"], c["rot"], q,
+    _gdn().rope_append_mxfp(s["dims"], s["t_lane"], s["q"], s["k"], s["v"], s["inv_freq"], c["rot"], q,
                            s["k_codes"], s["k_scales"], s["v_codes"], s["v_scales"], s["table"],
                            s["kv_len"], k_held=k, v_held=v, positions=s["positions"],
                            interleaved=c["pairs"])
@@ -259,7 +259,7 @@ def _own_append_fp4(s):
 
 def _own_attend(s):
     o = torch.empty(s["q"].shape, device="cuda")
-    _gdn().paged_attention_fp4(s["dims"], s["t_lane"], s["q"], s["k_codes"], s["k_scales"], s["v_codes"],
+    _gdn().paged_attention_mxfp(s["dims"], s["t_lane"], s["q"], s["k_codes"], s["k_scales"], s["v_codes"],
                                s["v_scales"], s["table"], s["kv_len"], o, s["workspace"],
                                scale=s["case"]["d"] ** -0.5)
     return o
