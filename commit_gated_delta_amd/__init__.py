@@ -1,6 +1,8 @@
 """Python binding of libgdn.so: gated-delta verify, ReplaySSM commit and
 chunked prefill on MI355X (gfx950), and the serving operators beside them
-(linear attention with a decay per head, paged attention, token scores).
+(linear attention with a decay per head, paged attention with a cache in the
+rows' type or in 4 bits, position rotation, token scores, sampled
+verification).
 
 Argument marshalling only (with checks of the tensors for the latter): every
 step of the path runs in the HIP kernels behind the C ABI declared in
@@ -9,7 +11,9 @@ importing this package raises.
 
 Names follow the C ABI: ``verify``, ``commit``, ``prefill_chunked``,
 ``records_bytes``, ``prefill_workspace_bytes``, ``decay_step``,
-``decay_prefill``, ``paged_attention``, ``kv_append``, ``token_scores``, ...
+``decay_prefill``, ``paged_attention``, ``kv_append``, ``token_scores``,
+``rope_append``, ``rope_append_mxfp``, ``paged_attention_mxfp``,
+``draft_verify``, ...
 """
 from __future__ import annotations
 
@@ -29,6 +33,7 @@ GDN_FLAG_PREFILL_ONE_CHAIN = 2
 GDN_FLAG_TOKENWISE = 4
 GDN_FLAG_HEAD_DECAY = 8
 GDN_FLAG_KEEP_STATE = 16
+GDN_FLAG_ROPE_PAIRS = 32
 GDN_MAX_LANES = 256
 GDN_MAX_T = 64
 GDN_MAX_TOP = 32
@@ -42,7 +47,10 @@ EXPORTED = ("gdn_records_bytes", "gdn_verify", "gdn_commit",
             "gdn_decay_prefill_workspace_bytes", "gdn_decay_prefill",
             "gdn_paged_attention_workspace_bytes", "gdn_paged_attention",
             "gdn_kv_append", "gdn_token_scores_workspace_bytes",
-            "gdn_token_scores", "gdn_strerror", "gdn_last_error")
+            "gdn_token_scores", "gdn_rope_append", "gdn_rope_append_mxfp",
+            "gdn_paged_attention_mxfp_workspace_bytes",
+            "gdn_paged_attention_mxfp", "gdn_draft_verify_workspace_bytes",
+            "gdn_draft_verify", "gdn_strerror", "gdn_last_error")
 PREFILL_SCRATCH_BYTES = 64 << 20
 
 
@@ -145,6 +153,22 @@ def _load_library():
                                      ctypes.c_int, vp, i32, f] + [
                                          vp] * 5 + [sz, vp]
     lib.gdn_token_scores.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    rows = [kp, ip, vp, i64, vp, i64, vp, i64, ctypes.c_int, vp, i32, vp, vp]
+    lib.gdn_rope_append.argtypes = rows + [vp] * 4 + [ctypes.c_int, vp]
+    lib.gdn_rope_append.restype = ctypes.c_int
+    lib.gdn_rope_append_mxfp.argtypes = rows + [vp] * 8 + [ctypes.c_int, vp]
+    lib.gdn_rope_append_mxfp.restype = ctypes.c_int
+    lib.gdn_paged_attention_mxfp_workspace_bytes.argtypes = [kp]
+    lib.gdn_paged_attention_mxfp_workspace_bytes.restype = sz
+    lib.gdn_paged_attention_mxfp.argtypes = [kp, ip, vp, ctypes.c_int] + [
+        vp] * 8 + [sz, f, vp]
+    lib.gdn_paged_attention_mxfp.restype = ctypes.c_int
+    lib.gdn_draft_verify_workspace_bytes.argtypes = [i32] * 3
+    lib.gdn_draft_verify_workspace_bytes.restype = sz
+    lib.gdn_draft_verify.argtypes = [i32, i32, ip, i32, vp, i64, vp, i64,
+                                     ctypes.c_int] + [vp] * 7 + [sz, vp]
+    lib.gdn_draft_verify.restype = ctypes.c_int
     lib.gdn_strerror.argtypes = [ctypes.c_int]
     lib.gdn_strerror.restype = ctypes.c_char_p
     lib.gdn_last_error.argtypes = []
@@ -582,3 +606,157 @@ def token_scores(logits, tokens, n_top, logprob, entropy, top_ids,
     if raw_status:
         return st
     _check(st, "gdn_token_scores")
+
+
+def _rows(t, name, dtype, n, t_max, h, d, device):
+    """Address and token stride of rows [n, t_max, h, d], each token's h rows
+    contiguous and the tokens equally far apart (a part of a projection's
+    output, say)."""
+    if (t.dtype is dtype and t.get_device() == device
+            and t.shape == (n, t_max, h, d)):
+        s0, s1, s2, s3 = t.stride()
+        step = s1 if t_max > 1 else s0 if n > 1 else h * d
+        if (s3 == 1 and (s2 == d or h == 1) and step >= h * d
+                and (n == 1 or s0 == t_max * step)):
+            return t.data_ptr(), step
+    raise ValueError(
+        "%s: expected %s rows [%d, %d, %d, %d] with contiguous heads and "
+        "equally spaced tokens on the current device (cuda:%d), got %s %s, "
+        "strides %s on %s" % (name, dtype, n, t_max, h, d, device, t.dtype,
+                              tuple(t.shape), t.stride(), t.device))
+
+
+def _rope_args(dims, t_lane, q, k, v, inv_freq, rot_dim, q_out, positions,
+               dev):
+    """The arguments that both writers begin with."""
+    n, tm, d, kind = dims.n_lanes, dims.t_max, dims.d, k.dtype
+    lanes, code = _lanes(t_lane, n), _code(kind)
+    qp, qs = (None, 0) if q is None else _rows(q, "q", kind, n, tm, dims.h_q,
+                                               d, dev)
+    kp, ks = _rows(k, "k", kind, n, tm, dims.h_kv, d, dev)
+    vp, vs = _rows(v, "v", kind, n, tm, dims.h_kv, d, dev)
+    return (ctypes.byref(dims), lanes, qp, qs, kp, ks, vp, vs, code,
+            _optional(inv_freq, "inv_freq", _F32, rot_dim // 2, dev), rot_dim,
+            _optional(positions, "positions", _I32, n * tm, dev),
+            _optional(q_out, "q_out", kind, n * tm * dims.h_q * d, dev))
+
+
+def rope_append(dims: KvDims, t_lane, q, k, v, inv_freq, rot_dim, q_out,
+                k_cache, v_cache, page_table, kv_len, positions=None,
+                interleaved=False, stream=None, raw_status=False):
+    """gdn_rope_append on torch tensors.  q, k, v may be views of one
+    projection's output; interleaved=True sets GDN_FLAG_ROPE_PAIRS."""
+    n, kind, dev = dims.n_lanes, k.dtype, torch.cuda.current_device()
+    nc = dims.n_pages * dims.page_size * dims.h_kv * dims.d
+    st = lib.gdn_rope_append(
+        *_rope_args(dims, t_lane, q, k, v, inv_freq, rot_dim, q_out,
+                    positions, dev),
+        _tensor(k_cache, "k_cache", kind, nc, dev),
+        _tensor(v_cache, "v_cache", kind, nc, dev),
+        _tensor(page_table, "page_table", _I32, n * dims.max_pages, dev),
+        _tensor(kv_len, "kv_len", _I32, n, dev),
+        GDN_FLAG_ROPE_PAIRS if interleaved else 0, _stream_on(stream, dev))
+    if raw_status:
+        return st
+    _check(st, "gdn_rope_append")
+
+
+def _fp4_cache(dims, k_codes, k_scales, v_codes, v_scales, dev):
+    rows = dims.n_pages * dims.page_size * dims.h_kv
+    nc, ns = rows * (dims.d // 2), rows * (dims.d // 32)
+    return (_tensor(k_codes, "k_codes", _U8, nc, dev),
+            _tensor(k_scales, "k_scales", _U8, ns, dev),
+            _tensor(v_codes, "v_codes", _U8, nc, dev),
+            _tensor(v_scales, "v_scales", _U8, ns, dev))
+
+
+def rope_append_mxfp(dims: KvDims, t_lane, q, k, v, inv_freq, rot_dim, q_out,
+                    k_codes, k_scales, v_codes, v_scales, page_table, kv_len,
+                    k_held=None, v_held=None, positions=None,
+                    interleaved=False, stream=None, raw_status=False):
+    """gdn_rope_append_mxfp on torch tensors."""
+    n, dev = dims.n_lanes, torch.cuda.current_device()
+    nr = n * dims.t_max * dims.h_kv * dims.d
+    st = lib.gdn_rope_append_mxfp(
+        *_rope_args(dims, t_lane, q, k, v, inv_freq, rot_dim, q_out,
+                    positions, dev),
+        *_fp4_cache(dims, k_codes, k_scales, v_codes, v_scales, dev),
+        _tensor(page_table, "page_table", _I32, n * dims.max_pages, dev),
+        _tensor(kv_len, "kv_len", _I32, n, dev),
+        _optional(k_held, "k_held", torch.bfloat16, nr, dev),
+        _optional(v_held, "v_held", torch.bfloat16, nr, dev),
+        GDN_FLAG_ROPE_PAIRS if interleaved else 0, _stream_on(stream, dev))
+    if raw_status:
+        return st
+    _check(st, "gdn_rope_append_mxfp")
+
+
+def paged_attention_mxfp_workspace_bytes(dims: KvDims) -> int:
+    return int(lib.gdn_paged_attention_mxfp_workspace_bytes(ctypes.byref(dims)))
+
+
+def paged_attention_mxfp(dims: KvDims, t_lane, q, k_codes, k_scales, v_codes,
+                        v_scales, page_table, kv_len, o, workspace, scale=1.0,
+                        stream=None, raw_status=False):
+    """gdn_paged_attention_mxfp on torch tensors."""
+    n, kind = dims.n_lanes, q.dtype
+    lanes, code, dev = _lanes(t_lane, n), _code(kind), torch.cuda.current_device()
+    nq = n * dims.t_max * dims.h_q * dims.d
+    ws, ws_bytes = _workspace(workspace, dev)
+    st = lib.gdn_paged_attention_mxfp(
+        ctypes.byref(dims), lanes, _tensor(q, "q", kind, nq, dev), code,
+        *_fp4_cache(dims, k_codes, k_scales, v_codes, v_scales, dev),
+        _tensor(page_table, "page_table", _I32, n * dims.max_pages, dev),
+        _tensor(kv_len, "kv_len", _I32, n, dev),
+        _tensor(o, "o", _F32, nq, dev), ws, ws_bytes, scale,
+        _stream_on(stream, dev))
+    if raw_status:
+        return st
+    _check(st, "gdn_paged_attention_mxfp")
+
+
+def _logit_rows(t, name, dtype, n, rows, vocab, device):
+    """Address and row stride of logits [n, rows, vocab] with contiguous,
+    equally spaced rows."""
+    if (t.dtype is dtype and t.get_device() == device
+            and t.shape == (n, rows, vocab)):
+        s0, s1, s2 = t.stride()
+        step = s1 if rows > 1 else s0 if n > 1 else vocab
+        if (s2 == 1 or vocab == 1) and step >= vocab and (
+                n == 1 or rows == 0 or s0 == rows * step):
+            return t.data_ptr(), step
+    raise ValueError(
+        "%s: expected %s logits [%d, %d, %d] with contiguous, equally spaced "
+        "rows on the current device (cuda:%d), got %s %s, strides %s on %s" % (
+            name, dtype, n, rows, vocab, device, t.dtype, tuple(t.shape),
+            t.stride(), t.device))
+
+
+def draft_verify_workspace_bytes(n_lanes, t_max, vocab) -> int:
+    return int(lib.gdn_draft_verify_workspace_bytes(n_lanes, t_max, vocab))
+
+
+def draft_verify(t_lane, logits, draft_logits, tokens, uniforms,
+                 inv_temperature, m_lane, next_token, workspace, accept=None,
+                 stream=None, raw_status=False):
+    """gdn_draft_verify on torch tensors: logits [n_lanes, t_max, vocab],
+    draft_logits [n_lanes, t_max - 1, vocab] or None."""
+    n, tm, vocab = logits.shape
+    kind = logits.dtype
+    lanes, code, dev = _lanes(t_lane, n), _code(kind), torch.cuda.current_device()
+    lp, ls = _logit_rows(logits, "logits", kind, n, tm, vocab, dev)
+    dp, ds = (None, 0) if draft_logits is None or tm == 1 else _logit_rows(
+        draft_logits, "draft_logits", kind, n, tm - 1, vocab, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    st = lib.gdn_draft_verify(
+        n, tm, lanes, vocab, lp, ls, dp, ds, code,
+        _tensor(tokens, "tokens", _I32, n * tm, dev),
+        _tensor(uniforms, "uniforms", _F32, n * tm, dev),
+        _tensor(inv_temperature, "inv_temperature", _F32, n, dev),
+        _tensor(m_lane, "m_lane", _I32, n, dev),
+        _tensor(next_token, "next_token", _I32, n, dev),
+        _optional(accept, "accept", _F32, n * tm, dev), ws, ws_bytes,
+        _stream_on(stream, dev))
+    if raw_status:
+        return st
+    _check(st, "gdn_draft_verify")

@@ -29,6 +29,10 @@
 #include "gdn_paged.h"
 #include "gdn_scores.h"
 
+#include "gdn_draft.h"
+#include "gdn_paged_mxfp.h"
+#include "gdn_rope.h"
+
 namespace gdns {
 
 constexpr int kThreads = 256;

@@ -35,6 +35,11 @@
  *   gdn_token_scores     log probabilities of given tokens, entropies and
  *                        top alternatives of rows of logits: what the
  *                        accepted prefix m of a window is decided from.
+ *   gdn_rope_append,     the cache's writer with the position rotation on the
+ *   gdn_rope_append_mxfp  way, into rows of the inputs' type or of 4 bits.
+ *   gdn_paged_attention_mxfp  the attention over the 4-bit cache.
+ *   gdn_draft_verify     the accepted prefix m and the next token of sampled
+ *                        windows, from given random numbers.
  *
  * The rule (Yang, Kautz & Hatamizadeh, "Gated Delta Networks: Improving
  * Mamba2 with Delta Rule", ICLR 2025, Sec. 3), per value head with state S
@@ -106,7 +111,8 @@ enum {
   GDN_FLAG_PREFILL_ONE_CHAIN = 2, /* gdn_prefill_chunked*: never in segments */
   GDN_FLAG_TOKENWISE = 4,        /* the verify calls: always token by token */
   GDN_FLAG_HEAD_DECAY = 8,       /* gdn_decay_*: g holds one constant a head */
-  GDN_FLAG_KEEP_STATE = 16       /* gdn_decay_step: S is read, not written  */
+  GDN_FLAG_KEEP_STATE = 16,      /* gdn_decay_step: S is read, not written  */
+  GDN_FLAG_ROPE_PAIRS = 32       /* gdn_rope_append*: neighbours form pairs */
 };
 
 typedef struct {
@@ -564,6 +570,89 @@ int gdn_kv_append(const gdn_kv_dims* dims, const int32_t* t_lane,
                   const int32_t* kv_len, void* stream);
 
 /*
+ * gdn_kv_append with the position rotation on the way: queries and keys are
+ * turned by their position, keys and values go into the cache, in one pass
+ * over the rows.  Channel pair i (of rot_dim / 2) of a row at position p
+ * becomes
+ *   a' = a cos(p f_i) - b sin(p f_i),   b' = b cos(p f_i) + a sin(p f_i)
+ * with f = inv_freq and (a, b) channels i and i + rot_dim / 2, or with
+ * GDN_FLAG_ROPE_PAIRS channels 2 i and 2 i + 1.  Channels from rot_dim on and
+ * the values are copied bit for bit.  Angles are reduced in f64, cosine, sine
+ * and the products are f32, rounded once to the outputs' type.
+ *   dims, t_lane, page_table, kv_len, k_cache, v_cache  as for gdn_kv_append
+ *               (the same places, the same rows dropped)
+ *   q, k, v     device, dtype (bf16 or f32): token t of lane n has its rows
+ *               [h][d] at element (n * t_max + t) * stride of each; a stride
+ *               is at least the rows' size and a multiple of 16 bytes, so the
+ *               three may be parts of one projection's output.  q may be NULL
+ *               (q_out too): keys and values alone.
+ *   inv_freq    device f32[rot_dim / 2], finite (NULL when rot_dim is 0)
+ *   rot_dim     a multiple of 16 in 0..d
+ *   positions   device int32 [n_lanes][t_max], or NULL: the position in the
+ *               cache, kv_len[n] - t_lane[n] + t.  They turn the rows only
+ *               (a tree's depths, say); where a row goes does not depend on
+ *               them.
+ *   q_out       device [n_lanes][t_max][h_q][d], dtype: the turned queries
+ *               (of dropped rows too).  May be q itself when its stride is
+ *               h_q * d; other overlaps are undefined.
+ *   flags       GDN_FLAG_ROPE_PAIRS or 0
+ * Token rows t >= t_lane are neither read nor written.  Pointers to rows must
+ * be 16-byte aligned, the others 4-byte (GDN_EINVAL).
+ */
+int gdn_rope_append(const gdn_kv_dims* dims, const int32_t* t_lane,
+                    const void* q, int64_t q_stride, const void* k,
+                    int64_t k_stride, const void* v, int64_t v_stride,
+                    int dtype, const float* inv_freq, int32_t rot_dim,
+                    const int32_t* positions, void* q_out, void* k_cache,
+                    void* v_cache, const int32_t* page_table,
+                    const int32_t* kv_len, int flags, void* stream);
+
+/*
+ * The same into a cache held in 4 bits.  A row's channels form blocks of 32,
+ * each with a scale s = 2^(b - 127) from a byte b and 32 codes of 4 bits, the
+ * values +-{0, 0.5, 1, 1.5, 2, 3, 4, 6} s; byte j of a row's codes holds
+ * channel 2 j in its lower and 2 j + 1 in its upper half (the bits of a code:
+ * sign, two of exponent, one of fraction).
+ *   k_codes, v_codes    device uint8 [n_pages][h_kv][page_size][d / 2]
+ *   k_scales, v_scales  device uint8 [n_pages][h_kv][page_size][d / 32]
+ * A block's scale is the smallest power of two with max |x| <= 6 s, 2^-126 at
+ * least and 2^124 at most (magnitudes past 6 * 2^124 become that), and every
+ * value the nearest one that the codes have, ties to the even code; rounding
+ * is from the turned f32 row.  A block that holds an infinity or a NaN has
+ * b = 255 and codes 0: all of it reads as NaN.
+ *   k_held, v_held  device bf16 [n_lanes][t_max][h_kv][d] or NULL: the new
+ *               tokens' rows as the cache holds them (exact in bf16), for a
+ *               prompt's own attention that is to see what later steps will;
+ *               written for dropped rows too
+ * The rest as for gdn_rope_append.  All eight pointers to cache rows, codes,
+ * scales and held rows must be 16-byte aligned.
+ */
+int gdn_rope_append_mxfp(const gdn_kv_dims* dims, const int32_t* t_lane,
+                        const void* q, int64_t q_stride, const void* k,
+                        int64_t k_stride, const void* v, int64_t v_stride,
+                        int dtype, const float* inv_freq, int32_t rot_dim,
+                        const int32_t* positions, void* q_out,
+                        uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
+                        uint8_t* v_scales, const int32_t* page_table,
+                        const int32_t* kv_len, void* k_held, void* v_held,
+                        int flags, void* stream);
+
+/*
+ * gdn_paged_attention over that cache (or any in its layout; byte 0 is
+ * 2^-127, byte 255 NaN).  Queries are bf16 or f32, the products and sums f32
+ * or wider; a query row that holds an infinity or a NaN gives NaN.  The rest,
+ * what masked rows may hold among it, as for gdn_paged_attention, with its
+ * own workspace size.
+ */
+size_t gdn_paged_attention_mxfp_workspace_bytes(const gdn_kv_dims* dims);
+int gdn_paged_attention_mxfp(const gdn_kv_dims* dims, const int32_t* t_lane,
+                            const void* q, int dtype, const uint8_t* k_codes,
+                            const uint8_t* k_scales, const uint8_t* v_codes,
+                            const uint8_t* v_scales, const int32_t* page_table,
+                            const int32_t* kv_len, float* o, void* workspace,
+                            size_t ws_bytes, float scale, void* stream);
+
+/*
  * Log probabilities of given tokens, with entropy and top alternatives, for
  * rows of logits: x = inv_temperature * logit, p = softmax(x).
  *   n_rows >= 1, vocab 1 .. 2^30
@@ -593,6 +682,57 @@ int gdn_token_scores(int32_t n_rows, int32_t vocab, int64_t row_stride,
                      const void* logits, int in_dtype, const int32_t* tokens,
                      int32_t n_top, float inv_temperature, float* logprob,
                      float* entropy, int32_t* top_ids, float* top_logprobs,
+                     void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Verification of sampled draft windows (speculative sampling): the accepted
+ * prefix m of every lane's window and its next token, distributed as if the
+ * model had sampled every token itself.  Row t of a lane's logits gives the
+ * distribution of the window's token t + 1: p_t = softmax(inv_temperature *
+ * logits row); the drafter's row gives q_t likewise, or without drafter
+ * logits q_t is 1 at the drafted token.  With w = tokens[t + 1] and u =
+ * uniforms[t], draft t + 1 stands when u q_t(w) < p_t(w).  m counts the
+ * anchor (token 0) and the drafts up to the first that falls, so it is the m
+ * of gdn_commit.  The next token is sampled from max(p - q, 0) of row m - 1
+ * when a draft fell there, else from p of the last row: the lowest id whose
+ * running sum of weights is above uniforms[t_lane - 1] times their whole.
+ * A window of the anchor alone (t_lane = 1) samples one token.
+ *   n_lanes     1..GDN_MAX_LANES;  t_max 1..GDN_MAX_T
+ *   t_lane      host int32[n_lanes], 0..t_max (0: nothing of the lane is read
+ *               or written)
+ *   vocab       1 .. 2^30
+ *   logits      device, in_dtype (bf16 or f32), element-aligned: row t of
+ *               lane n at element (n * t_max + t) * row_stride (>= vocab)
+ *   draft_logits  device, in_dtype: row t < t_max - 1 of lane n at element
+ *               (n * (t_max - 1) + t) * draft_stride (>= vocab); or NULL
+ *   tokens      device int32 [n_lanes][t_max]; token 0, the anchor, is not
+ *               read.  A draft outside 0..vocab-1 falls.
+ *   uniforms    device f32 [n_lanes][t_max], in 0 .. 1, 1 excluded
+ *   inv_temperature  device f32[n_lanes], 1e-30 .. 1e30
+ *   m_lane      device int32[n_lanes]: 1..t_lane
+ *   next_token  device int32[n_lanes]
+ *   accept      device f32 [n_lanes][t_max] or NULL: min(1, p_t(w) / q_t(w))
+ *               for t < t_lane - 1, of the drafts behind the first fallen one
+ *               too; other entries are left as they were
+ * A logit of -inf has probability 0.  A row that holds a NaN or +inf, or
+ * nothing but -inf, has no distribution, nor has any row of a lane whose
+ * inverse temperature is out of range: a draft falls there (accept NaN), and
+ * next_token is -1 when it would be sampled there.  Where p - q leaves
+ * nothing (p = q to rounding) the token is sampled from p.
+ * Chances of drafts are exact to a few steps of f32; the sums that the next
+ * token is looked up in are f64.
+ *   workspace   device, 16-byte aligned, ws_bytes >=
+ *               gdn_draft_verify_workspace_bytes(...); calls that overlap in
+ *               time need workspaces of their own
+ */
+size_t gdn_draft_verify_workspace_bytes(int32_t n_lanes, int32_t t_max,
+                                        int32_t vocab);
+int gdn_draft_verify(int32_t n_lanes, int32_t t_max, const int32_t* t_lane,
+                     int32_t vocab, const void* logits, int64_t row_stride,
+                     const void* draft_logits, int64_t draft_stride,
+                     int in_dtype, const int32_t* tokens,
+                     const float* uniforms, const float* inv_temperature,
+                     int32_t* m_lane, int32_t* next_token, float* accept,
                      void* workspace, size_t ws_bytes, void* stream);
 
 /* Static description of a status code; never NULL. */
