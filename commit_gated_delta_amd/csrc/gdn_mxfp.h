@@ -2,11 +2,13 @@
 // with a scale 2^(b - 127) from a byte b and 32 codes of 4 bits (sign, two
 // bits of exponent, one of fraction: 0, 0.5, 1, 1.5, 2, 3, 4, 6), two codes a
 // byte, the even channel in the lower half.  These are the elements and
-// scales that gfx950 converts and multiplies itself.
+// scales that gfx950 converts itself.
 #pragma once
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+
+#include "gdn.h"
 
 namespace gdnk {
 
@@ -16,7 +18,15 @@ struct Fp4Rows {
 };
 
 constexpr uint32_t kScaleNan = 255;  // every value of the block is a NaN
-constexpr uint32_t kScaleMost = 251, kScaleLeast = 1;
+constexpr uint32_t kScaleMost = 251, kScaleLeast = 1;  // of what is written
+// Blocks whose scale byte is at least this read as NaN (their largest values
+// are past f32).
+constexpr uint32_t kScaleOdd = 253;
+
+// Cache rows are counted in 32 bits (2^32 of them fill the memory).
+static bool rows_fit(const gdn_kv_dims& d) {
+  return (double)d.n_pages * d.page_size * d.h_kv < 4294967296.0;
+}
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t codes_u32x4 __attribute__((ext_vector_type(4)));

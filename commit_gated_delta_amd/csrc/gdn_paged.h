@@ -371,6 +371,58 @@ __device__ __forceinline__ float* row_out(const AttendArgs& p, const Split& s,
   return p.part_o + at * d;
 }
 
+// The four waves' results: each scaled to the common maximum, written to LDS
+// (a part of `pitch` floats a wave) and added up by all threads.
+constexpr int kSumPad = 4;  // a row's floats past D (rows on different banks)
+template <int D, typename R, int ROWS>
+__device__ __forceinline__ void sum_waves(const AttendArgs& p, const Split& s,
+                                          int hk, int rows, const R& x,
+                                          float* pool, int pitch,
+                                          float (&ml)[4][2][ROWS]) {
+  constexpr int kSumPitch = D + kSumPad, RT = ROWS / 16, CT = R::CT;
+  const int tid = threadIdx.x, lane = tid & 63, wave = gdn::uniform(tid >> 6);
+  const int n = lane & 15, g4 = lane >> 4;
+  if (g4 == 0)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      ml[wave][0][16 * r + n] = x.m[r];
+      ml[wave][1][16 * r + n] = x.l[r];
+    }
+  __syncthreads();
+  float* sum = pool + wave * pitch;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w][0][16 * r + n]);
+    const float keep =
+        x.m[r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x.m[r] - top);
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+      *reinterpret_cast<f32x4*>(sum + (16 * r + n) * kSumPitch + 16 * c +
+                                4 * g4) = x.acc[r][c] * keep;
+  }
+  __syncthreads();
+  const int used = rows < ROWS ? rows : ROWS;
+  for (int i = tid; i < used * (D / 4); i += 256) {
+    const int row = i / (D / 4), c = i % (D / 4) * 4;
+    float top = -INFINITY, tot = 0.f;
+    f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w][0][row]);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      tot += ml[w][1][row] *
+             (top == -INFINITY ? 1.f
+                               : __builtin_amdgcn_exp2f(ml[w][0][row] - top));
+      y += *reinterpret_cast<const f32x4*>(pool + w * pitch + row * kSumPitch + c);
+    }
+    float f;
+    float* dst = row_out(p, s, hk, row, D, top, tot, c == 0, f);
+    *reinterpret_cast<f32x4*>(dst + c) = y * f;
+  }
+}
+
 // Few rows: four waves share out a split's positions, 32 at a step.  The next
 // step's K rows are loaded when this step's scores are done and its V rows
 // when V is in LDS, page numbers a step earlier.  Bound by HBM: 32 lanes x 8
@@ -386,11 +438,10 @@ __global__ __launch_bounds__(256, D * sizeof(T) >= 512 ? 1 : 2) void attend_kern
   typedef typename R::Raw Raw;
   typedef typename R::TL TL;
   typedef typename R::VL VL;
-  constexpr int KS = R::KS, CT = R::CT, kRows = 16 * RT;
+  constexpr int KS = R::KS, kRows = 16 * RT;
   constexpr int kPieces = sizeof(Raw) / 16;  // 16-byte loads per fragment
   constexpr int kTileBytes = 32 * TL::kPitch * (int)sizeof(T);
-  constexpr int kSumPitch = D + 4;  // (rows on different banks)
-  constexpr int kSumBytes = kRows * kSumPitch * 4;
+  constexpr int kSumBytes = kRows * (D + kSumPad) * 4;
   constexpr int kPer = kTileBytes > kSumBytes ? kTileBytes : kSumBytes;
   __shared__ __attribute__((aligned(16))) T Qs[kRows * TL::kPitch];
   __shared__ __attribute__((aligned(16))) char pool[4 * kPer];
@@ -534,49 +585,8 @@ __global__ __launch_bounds__(256, D * sizeof(T) >= 512 ? 1 : 2) void attend_kern
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
 
-  // the four waves' results: each scaled to the common maximum, written to
-  // LDS and added up by all threads
   x.finish(a, table, begin + 32 * wave, 128, stop);
-  if (g4 == 0)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      ml[wave][0][16 * r + n] = x.m[r];
-      ml[wave][1][16 * r + n] = x.l[r];
-    }
-  __syncthreads();
-  float* sum = reinterpret_cast<float*>(pool + wave * kPer);
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w][0][16 * r + n]);
-    const float keep =
-        x.m[r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x.m[r] - top);
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
-      *reinterpret_cast<f32x4*>(sum + (16 * r + n) * kSumPitch + 16 * c +
-                                4 * g4) = x.acc[r][c] * keep;
-  }
-  __syncthreads();
-  const int used = rows < kRows ? rows : kRows;
-  for (int i = tid; i < used * (D / 4); i += 256) {
-    const int row = i / (D / 4), c = i % (D / 4) * 4;
-    float top = -INFINITY, tot = 0.f;
-    f32x4 y = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w][0][row]);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      tot += ml[w][1][row] *
-             (top == -INFINITY ? 1.f
-                               : __builtin_amdgcn_exp2f(ml[w][0][row] - top));
-      y += *reinterpret_cast<const f32x4*>(
-          reinterpret_cast<const float*>(pool + w * kPer) + row * kSumPitch + c);
-    }
-    float f;
-    float* dst = row_out(p, s, hk, row, D, top, tot, c == 0, f);
-    *reinterpret_cast<f32x4*>(dst + c) = y * f;
-  }
+  sum_waves<D>(p, s, hk, rows, x, reinterpret_cast<float*>(pool), kPer / 4, ml);
 }
 
 // Many rows: NW waves take 16 rows each, and a tile of positions is staged in
@@ -911,14 +921,14 @@ struct Shape {
   int rows, rt, waves, groups, target, items, slots;
   bool few;
 };
-static Shape shape_of(const gdn_kv_dims& d, int size) {
+static Shape shape_of(const gdn_kv_dims& d, int few_blocks, int rows_blocks) {
   Shape s;
   s.rows = d.t_max * (d.h_q / d.h_kv);
   s.few = s.rows <= (d.d < 256 ? 32 : 16);
   s.rt = s.few && s.rows > 16 ? 2 : 1;
   s.waves = !s.few && s.rows > 64 && d.d < 256 ? 8 : 4;
   s.groups = s.few ? 1 : (s.rows + 16 * s.waves - 1) / (16 * s.waves);
-  const int blocks = !s.few ? kRowsBlocks : d.d * size < 512 ? kFewBlocks : kWideBlocks;
+  const int blocks = s.few ? few_blocks : rows_blocks;
   const int items = blocks / (d.h_kv * s.groups);
   s.target = items - d.n_lanes > items / 2 ? items - d.n_lanes : items / 2;
   if (s.target < 1) s.target = 1;
@@ -928,11 +938,31 @@ static Shape shape_of(const gdn_kv_dims& d, int size) {
   s.slots = 2l * s.target < most ? 2 * s.target : (int)most;
   return s;
 }
-// (bf16 never needs less)
-static size_t attend_bytes(const gdn_kv_dims& d) {
-  const Shape s = shape_of(d, 2);
+static Shape shape_of(const gdn_kv_dims& d, int size) {
+  return shape_of(d, d.d * size < 512 ? kFewBlocks : kWideBlocks, kRowsBlocks);
+}
+static size_t slot_bytes(const gdn_kv_dims& d, const Shape& s) {
   const size_t n = (size_t)s.slots * d.h_kv * s.rows;
   return n * (d.d + 2) * sizeof(float);
+}
+// (bf16 never needs less)
+static size_t attend_bytes(const gdn_kv_dims& d) {
+  return slot_bytes(d, shape_of(d, 2));
+}
+
+template <int D>
+static hipError_t join(const gdn_kv_dims& d, const Shape& s,
+                       const AttendArgs& p, const gdn::LaneTable& tl,
+                       hipStream_t st) {
+  // a cache of one unit per lane has nothing to join
+  const long units = ((long)d.max_pages * d.page_size + kUnit - 1) / kUnit;
+  if (units < 2) return hipSuccess;
+  const dim3 rows((unsigned)((long)d.n_lanes * d.h_kv * s.rows));
+  if (rows.x >= kManyRows)
+    return launch(join_kernel<D, 1, kFewBlocks>, rows, dim3(64), st, p, tl);
+  if (units <= kFewSplits || s.target <= kFewSplits)
+    return launch(join_kernel<D, 4, kFewSplits>, rows, dim3(256), st, p, tl);
+  return launch(join_kernel<D, 16, kFewBlocks>, rows, dim3(1024), st, p, tl);
 }
 
 template <int D, typename T>
@@ -953,15 +983,7 @@ static hipError_t attend(const gdn_kv_dims& d, const Shape& s,
     e = s.few ? launch(attend_kernel<D, T, 1>, grid, dim3(256), st, p, tl)
               : launch(rows_kernel<D, T, 4>, grid, dim3(256), st, p, tl);
   }
-  // a cache of one unit per lane has nothing to join
-  const long units = ((long)d.max_pages * d.page_size + kUnit - 1) / kUnit;
-  if (e != hipSuccess || units < 2) return e;
-  const dim3 rows((unsigned)((long)d.n_lanes * d.h_kv * s.rows));
-  if (rows.x >= kManyRows)
-    return launch(join_kernel<D, 1, kFewBlocks>, rows, dim3(64), st, p, tl);
-  if (units <= kFewSplits || s.target <= kFewSplits)
-    return launch(join_kernel<D, 4, kFewSplits>, rows, dim3(256), st, p, tl);
-  return launch(join_kernel<D, 16, kFewBlocks>, rows, dim3(1024), st, p, tl);
+  return e != hipSuccess ? e : join<D>(d, s, p, tl, st);
 }
 
 template <typename T>

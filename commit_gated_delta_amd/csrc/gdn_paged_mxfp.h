@@ -1,6 +1,20 @@
 // gdn_paged_mxfp.h -- attention of draft windows or single tokens over a paged
 // key-value cache held in 4 bits (gdn_paged_attention_mxfp).  Compiled as part
 // of gdn_state.hip.
+//
+// The splits, the softmax and the layout of scores and outputs are those of
+// gdn_paged.h; what differs is how K and V reach the matrix cores:
+//
+// Scores.  A product may sum its slots in any order, so a lane takes a quarter
+// of a row's channels as they lie in the cache, and each dword of codes,
+// widened to bf16 (exact), is its part of an operand of 16 x 16 x 32 against
+// the same channels of q.  (The instructions that take 4-bit codes and their
+// scales as they are multiply by 8-bit floats at most, and add up with about
+// 16 bits below the largest product: q cut into two or five such floats gave
+// log probabilities 5e-6 off, rms, where this gives 1e-7.)
+//
+// Values are widened on their way through LDS, from where the transposed read
+// takes them as in gdn_paged.h.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -13,91 +27,468 @@
 namespace gdnk {
 
 struct Attend4Args {
-  KvArgs kv;
+  AttendArgs at;
   Fp4Rows k4, v4;
-  const void* q;
-  float* o;
-  float scale;
 };
 
-// One workgroup per row of q: 256 positions at a time, a thread a position
-// for the scores and a thread a channel for the values.
-template <typename T>
-__global__ __launch_bounds__(256) void attend4_kernel(Attend4Args p,
-                                                      gdn::LaneTable tl, int d) {
-  __shared__ float qs[256], ps[256];
-  __shared__ long at[256];
-  __shared__ float red[2][4];
-  const KvArgs& a = p.kv;
-  const int h = blockIdx.x % a.h_q;
-  const long nt = blockIdx.x / a.h_q;
-  const int n = (int)(nt / a.t_max), t = (int)(nt % a.t_max);
-  const int T_n = tl.v[n];
-  if (t >= T_n) return;
-  const int hk = h / (a.h_q / a.h_kv), len = lane_len(a, n);
-  const int end = len - T_n + t + 1;  // positions seen
-  const int tid = threadIdx.x;
-  const long row = (nt * a.h_q + h) * d;
-  qs[tid] = tid < d ? elem((const T*)p.q, row + tid) : 0.f;
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  bool any = false;
-  __syncthreads();
-  for (int p0 = 0; p0 < end; p0 += 256) {
-    const int pos = p0 + tid;
-    long r = -1;
-    float x = -INFINITY;
-    if (pos < end) r = row_of(a, n, hk, pos, 1);
-    if (r >= 0) {
-      x = 0.f;
-      for (int c = 0; c < d; c += 8) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(p.k4.codes + r * (d / 2) + c / 2);
-        const codes_u32x4 v = fp4_values(w, p.k4.scales[r * (d / 32) + c / 32]);
+// What lane 16 g + n holds of a row: its channels D / 4 g .. D / 4 (g + 1) - 1,
+// so of codes D / 32 dwords, each an operand's eight slots, in one or two
+// blocks.
+template <int D>
+struct Own {
+  static constexpr int kDwords = D / 32;
+  static constexpr int kScales = D == 256 ? 2 : 1;
+  uint32_t codes[kDwords];
+  uint32_t scale[kScales];
+  __device__ __forceinline__ void load(const Fp4Rows& c, uint32_t row, int g) {
+    const uint8_t* at = c.codes + ((uint64_t)row * (D / 2) + (D / 8) * g);
+    if constexpr (D == 64) {
+      const uint2 w = *reinterpret_cast<const uint2*>(at);
+      codes[0] = w.x;
+      codes[1] = w.y;
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x += qs[c + 2 * i] * __uint_as_float(v[i] << 16);
-          x += qs[c + 2 * i + 1] * __uint_as_float(v[i] & 0xffff0000u);
+      for (int y = 0; y < kDwords / 4; ++y) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(at + 16 * y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) codes[4 * y + i] = w[i];
+      }
+    }
+    const uint8_t* s = c.scales + (uint64_t)row * (D / 32);
+    if constexpr (D == 256) {
+      const uint32_t w = *reinterpret_cast<const uint16_t*>(s + 2 * g);
+      scale[0] = w & 255;
+      scale[1] = w >> 8;
+    } else {
+      scale[0] = s[D == 64 ? g >> 1 : g];
+    }
+  }
+  __device__ __forceinline__ u32x4 values(int i) const {
+    return fp4_values(codes[i], scale[i * kScales / kDwords]);
+  }
+};
+
+// Query rows as B operands: lane 16 g + n holds channels D / 4 g + 8 i .. + 7
+// of row n, i < D / 32; f32 rows as three bf16 parts.
+template <int D, typename T>
+struct Query {
+  typedef Op<uint16_t> O;
+  typedef std::conditional_t<sizeof(T) == 2, u32x4, typename O::Wide> Piece;
+  Piece q[D / 32];
+  // The row at `row`, or zeros.
+  __device__ __forceinline__ void load(const T* row, bool zero) {
+    const T* at = row + (D / 4) * ((threadIdx.x & 63) >> 4);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      u32x4 w[sizeof(T) / 2];
+#pragma unroll
+      for (int y = 0; y < (int)sizeof(T) / 2; ++y) {
+        w[y] = reinterpret_cast<const u32x4*>(at + 8 * i)[y];
+        if (zero) w[y] = u32x4{0, 0, 0, 0};
+      }
+      if constexpr (sizeof(T) == 2) q[i] = w[0];
+      else q[i] = O::wide(__builtin_bit_cast(f32x4, w[0]), __builtin_bit_cast(f32x4, w[1]));
+    }
+  }
+  // Scores of 16 positions.
+  __device__ __forceinline__ f32x4 scores(const Own<D>& k) const {
+    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) c = O::mul(k.values(i), q[i], c);
+    return c;
+  }
+};
+
+// The row of q at row `row` of key-value head hk.
+template <int D, typename T>
+__device__ __forceinline__ const T* query_row(const AttendArgs& p, int lane,
+                                              int hk, int row) {
+  const int group = p.kv.h_q / p.kv.h_kv;
+  return (const T*)p.q + (((long)lane * p.kv.t_max + row / group) * p.kv.h_q +
+                          hk * group + row % group) * D;
+}
+
+// Rows that see a position whose value block b is NaN get NaN in its
+// channels; `values` took it as zeros.  What a row sees is a prefix, so the
+// first such position, p0 + first, is enough.
+template <int D, int RT>
+__device__ __forceinline__ void mark_odd(Rows<D, uint16_t, RT>& x, int b,
+                                         int pos) {
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c / 2 == b && pos < x.end[r]) x.acc[r][c][e] = NAN;
+}
+
+// Waves per SIMD that the registers are kept to: f32 queries take three times
+// the registers of bf16 ones.
+template <int D, typename T, int RT>
+constexpr int few4_waves() {
+  constexpr int q = D * RT * (int)sizeof(T);  // 128 * 2: one tile in bf16
+  return q <= 256 ? 3 : q <= 512 ? 2 : 1;
+}
+template <int D, typename T, int NW>
+constexpr int rows4_waves() {
+  return D * sizeof(T) <= 256 ? NW / 2 : NW / 4;
+}
+
+// Row of a position in its page, counted over the cache (fewer than 2^32).
+__device__ __forceinline__ uint32_t cache_row(const KvArgs& a, int page, int h,
+                                              int pos, bool& there) {
+  there = (unsigned)page < (unsigned)a.n_pages;
+  const uint32_t row = ((uint32_t)page * a.h_kv + h) * a.page +
+                       (uint32_t)(pos - page_of(a, pos) * a.page);
+  return there ? row : 0;  // (any row of the cache will do)
+}
+
+// Few rows, as attend_kernel: four waves share out a split's positions, 32 at
+// a step, and lane 16 g + n holds its channels of positions n and 16 + n.
+template <int D, typename T, int RT>
+__global__ __launch_bounds__(256, (few4_waves<D, T, RT>())) void attend4_kernel(
+    Attend4Args q, gdn::LaneTable tl) {
+  typedef Rows<D, uint16_t, RT> R;
+  typedef typename R::VL VL;
+  typedef Own<D> Part;
+  constexpr int kRows = 16 * RT;
+  constexpr int kTileBytes = 32 * D * 2;
+  constexpr int kSumBytes = kRows * (D + kSumPad) * 4;
+  constexpr int kWave = kTileBytes > kSumBytes ? kTileBytes : kSumBytes;
+  __shared__ __attribute__((aligned(16))) char pool[4 * kWave];
+  __shared__ float ml[4][2][kRows];
+  const AttendArgs& p = q.at;
+  const KvArgs& a = p.kv;
+  const Split s = find_split(a, tl, blockIdx.x / a.h_kv, p.target, false);
+  if (s.lane < 0) return;
+  const int hk = blockIdx.x % a.h_kv;
+  const int group = a.h_q / a.h_kv, T_n = tl.v[s.lane];
+  const int rows = T_n * group;
+  const int tid = threadIdx.x, lane = tid & 63, wave = gdn::uniform(tid >> 6);
+  const int n = lane & 15, g4 = lane >> 4;
+  const int begin = s.nth * s.units * kUnit;
+  const int stop = begin + s.units * kUnit < s.len ? begin + s.units * kUnit : s.len;
+  const int steps = (stop - begin + 31) / 32;
+  const int open = s.len - T_n + 1;  // first position that some row cannot see
+  uint16_t* Vs = reinterpret_cast<uint16_t*>(pool + wave * kWave);
+  const int* table = a.table + (long)s.lane * a.max_pages;
+
+  int page[2];     // page numbers of the step after the next
+  bool there[2];   // whether the positions of the step in hand are
+  uint32_t at[2];  // and their rows
+  auto look_up = [&](int step) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int pos = begin + 32 * step + 16 * h + n;
+      page[h] = pos < stop ? table[page_of(a, pos)] : -1;
+    }
+  };
+  auto place = [&](int step) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      at[h] = cache_row(a, page[h], hk, begin + 32 * step + 16 * h + n, there[h]);
+  };
+  Part kp[2], vp[2];
+  auto fetch = [&](const Fp4Rows& c, Part (&r)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) r[h].load(c, at[h], g4);
+  };
+
+  if (wave < steps) {
+    look_up(wave);
+    place(wave);
+    fetch(q.k4, kp);
+    fetch(q.v4, vp);
+    look_up(wave + 4);
+  }
+  R x;
+  x.init(0, rows, s.len, T_n, group);
+  Query<D, T> query[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    // (rows past the last: the first one's channels as zeros)
+    const int row = 16 * r + n < rows ? 16 * r + n : 0;
+    query[r].load(query_row<D, T>(p, s.lane, hk, row), 16 * r + n >= rows);
+  }
+  for (int step = wave; step < steps; step += 4) {
+    const bool here[2] = {there[0], there[1]};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int y = 0; y < Part::kScales; ++y)
+        if (kp[h].scale[y] >= kScaleOdd) kp[h].scale[y] = kScaleNan;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) x.sc[r][h] = query[r].scores(kp[h]);
+    }
+    const int next = step + 4;
+    if (next < steps) {
+      place(next);
+      fetch(q.k4, kp);
+      look_up(next + 4);
+    }
+    const int p0 = begin + 32 * step;
+    const bool whole =
+        p0 + 32 <= (open < stop ? open : stop) && __all(here[0] && here[1]);
+    uint32_t ok = 0;  // bit of position i of the step: its row is there
+    if (!whole)
+      ok = ((uint32_t)__ballot(here[0]) & 0xffffu) |
+           ((uint32_t)__ballot(here[1]) & 0xffffu) << 16;
+    x.softmax(p.scale, whole, ok, p0);
+    // V through LDS.  Rows that are not there count as zeros.
+    bool off[2][Part::kScales], odd = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int y = 0; y < Part::kScales; ++y) {
+        off[h][y] = here[h] && vp[h].scale[y] >= kScaleOdd;
+        odd |= off[h][y];
+        if (off[h][y] || !here[h]) {
+          vp[h].scale[y] = 0;
+#pragma unroll
+          for (int i = 0; i < Part::kDwords; ++i)
+            if (i * Part::kScales / Part::kDwords == y) vp[h].codes[i] = 0;
         }
       }
-      x *= p.scale;
+#pragma unroll
+      for (int i = 0; i < Part::kDwords; ++i)
+        *reinterpret_cast<u32x4*>(Vs + VL::at(n, Part::kDwords * g4 + i) +
+                                  16 * h * VL::kPitch) = vp[h].values(i);
     }
-    float top = x, sum = r >= 0 ? 1.f : 0.f;
-    for (int i = 1; i < 64; i *= 2) {
-      const float o = __shfl_xor(top, i);
-      top = top != top || o != o ? NAN : fmaxf(top, o);
-      sum += __shfl_xor(sum, i);
-    }
-    if (tid % 64 == 0) {
-      red[0][tid / 64] = top;
-      red[1][tid / 64] = sum;
-    }
-    at[tid] = r;
-    __syncthreads();
-    for (int w = 0; w < 4; ++w) {
-      any |= red[1][w] > 0.f;
-      const float o = red[0][w];
-      top = top != top || o != o ? NAN : fmaxf(top, o);
-    }
-    const float next = top != top || m != m ? NAN : fmaxf(m, top);
-    const float keep = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - next);
-    const float e = r < 0 || next == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x - next);
-    ps[tid] = e;
-    m = next;
-    __syncthreads();
-    acc *= keep;
-    l *= keep;
-    const int stop = end - p0 < 256 ? end - p0 : 256;
-    for (int i = 0; i < stop; ++i) {
-      l += ps[i];
-      if (tid < d && at[i] >= 0) {
-        const uint32_t w = p.v4.codes[at[i] * (d / 2) + tid / 2];
-        const uint32_t v = fp4_values(w, p.v4.scales[at[i] * (d / 32) + tid / 32])[0];
-        acc += ps[i] * __uint_as_float(tid & 1 ? v & 0xffff0000u : v << 16);
+    const bool is_odd = __any(odd);
+    if (next < steps) fetch(q.v4, vp);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    x.values(Vs, 0);
+    if (is_odd) {
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b) {
+        // positions of the step whose block b is NaN
+        const int y = D == 256 ? b & 1 : 0;
+        const int g = D == 64 ? 32 * b : D == 128 ? 16 * b : 16 * (b >> 1);
+        const uint32_t hit = ((uint32_t)(__ballot(off[0][y]) >> g) & 0xffffu) |
+                             ((uint32_t)(__ballot(off[1][y]) >> g) & 0xffffu) << 16;
+        if (hit) mark_odd(x, b, p0 + __builtin_ctz(hit));
       }
     }
-    __syncthreads();
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
-  if (tid < d)
-    p.o[row + tid] = !any ? 0.f : m == -INFINITY ? NAN : acc / l;
+  x.finish(a, table, begin + 32 * wave, 128, stop);
+  sum_waves<D>(p, s, hk, rows, x, reinterpret_cast<float*>(pool), kWave / 4, ml);
+}
+
+// Many rows, as rows_kernel: NW waves take 16 rows each of the same tile of
+// 64 positions, whose K lies in LDS as it is in the cache and whose V is
+// widened once for all of them.  Two tiles take turns, so that one barrier a
+// tile is enough.
+template <int D, typename T, int NW>
+__global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW>())) void rows4_kernel(
+    Attend4Args q, gdn::LaneTable tl) {
+  typedef Rows<D, uint16_t, 1> R;
+  typedef typename R::VL VL;
+  constexpr int kRows = 16 * NW, kTile = 64, kBlocks = D / 32;
+  constexpr int kPieces = kTile * kBlocks;                    // of K, or of V
+  constexpr int kThreads = 64 * NW;
+  constexpr int kN = (kPieces + kThreads - 1) / kThreads;     // of a thread
+  __shared__ __attribute__((aligned(16))) u32x4 Kc[2][kPieces];
+  __shared__ uint8_t Ks[2][kPieces];
+  __shared__ __attribute__((aligned(16))) uint16_t Vs[2][kTile * D];
+  __shared__ int odd_first[3][kBlocks];  // of a tile's rows, by block; kTile: none
+  const AttendArgs& p = q.at;
+  const KvArgs& a = p.kv;
+  const int per_item = a.h_kv * p.groups;
+  const Split s = find_split(a, tl, blockIdx.x / per_item, p.target, false);
+  if (s.lane < 0) return;
+  const int hk = blockIdx.x % per_item / p.groups;
+  const int row0 = blockIdx.x % p.groups * kRows;
+  const int group = a.h_q / a.h_kv, T_n = tl.v[s.lane];
+  const int rows = T_n * group;
+  if (row0 >= rows) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = gdn::uniform(tid >> 6);
+  const int n = lane & 15, g4 = lane >> 4;
+  const int begin = s.nth * s.units * kUnit;
+  const int stop = begin + s.units * kUnit < s.len ? begin + s.units * kUnit : s.len;
+  const int tiles = (stop - begin + kTile - 1) / kTile;
+  const int open = s.len - T_n + 1;
+  const int* table = a.table + (long)s.lane * a.max_pages;
+
+  // lane i of every wave keeps track of row i of a tile
+  int page = -1;        // page number of the row, a tile ahead of its use
+  uint32_t at = 0;      // where it is
+  uint64_t ok = 0;      // rows of the tile in transit that are there
+  auto look_up = [&](int tile) {
+    const int pos = begin + tile * kTile + lane;
+    page = pos < stop ? table[page_of(a, pos)] : -1;
+  };
+  auto place = [&](int tile) {
+    bool there;
+    at = cache_row(a, page, hk, begin + tile * kTile + lane, there);
+    ok = __ballot(there);
+  };
+  u32x4 kr[kN], vr[kN];
+  uint32_t ks[kN], vs[kN];
+  // (threads without a piece take a copy of another's)
+  auto piece_of = [&](int i) { return (tid + i * kThreads) % kPieces; };
+  auto fetch = [&]() {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int src = piece_of(i) / kBlocks, b = piece_of(i) % kBlocks;
+      const uint64_t off = (uint64_t)(uint32_t)__shfl((int)at, src) * kBlocks + b;
+      kr[i] = *reinterpret_cast<const u32x4*>(q.k4.codes + 16 * off);
+      ks[i] = q.k4.scales[off];
+      vr[i] = *reinterpret_cast<const u32x4*>(q.v4.codes + 16 * off);
+      vs[i] = q.v4.scales[off];
+    }
+  };
+  // Place of block b of row r in Kc and Ks: rows of 2 to 8 blocks share 256
+  // bytes, their blocks permuted so that 16 rows' block b lie apart.
+  auto spot = [&](int r, int b) {
+    return r * kBlocks + (b ^ (r / (16 / kBlocks)) % kBlocks);
+  };
+  auto put = [&](int tile, uint64_t here) {
+    const int buf = tile & 1;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int r = piece_of(i) / kBlocks, b = piece_of(i) % kBlocks;
+      const bool is_there = here >> r & 1, off = vs[i] >= kScaleOdd;
+      if (is_there && off) atomicMin(&odd_first[tile % 3][b], r);
+      if (!is_there || off) {
+        vr[i] = u32x4{0, 0, 0, 0};
+        vs[i] = 0;
+      }
+      Kc[buf][spot(r, b)] = kr[i];
+      Ks[buf][spot(r, b)] = (uint8_t)(ks[i] >= kScaleOdd ? kScaleNan : ks[i]);
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        *reinterpret_cast<u32x4*>(Vs[buf] + VL::at(r, 4 * b + y)) =
+            fp4_values(vr[i][y], vs[i]);
+    }
+  };
+  if (tid < 3 * kBlocks) odd_first[tid / kBlocks][tid % kBlocks] = kTile;
+  uint64_t here = 0;
+  if (tiles > 0) {
+    look_up(0);
+    place(0);
+    fetch();
+    look_up(1);
+  }
+  R x;
+  x.init(row0 + 16 * wave, rows, s.len, T_n, group);
+  Query<D, T> query;
+  {
+    const int row = row0 + 16 * wave + n;
+    query.load(query_row<D, T>(p, s.lane, hk, row < rows ? row : 0), row >= rows);
+  }
+  __syncthreads();
+  if (tiles > 0) {
+    here = ok;
+    put(0, here);
+    if (tiles > 1) {
+      place(1);
+      fetch();
+      look_up(2);
+    }
+  }
+  for (int tile = 0; tile < tiles; ++tile) {
+    const int t0 = begin + tile * kTile, buf = tile & 1;
+    const uint64_t now = here;
+    const bool whole = t0 + kTile <= (open < stop ? open : stop) && now == ~0ull;
+    __syncthreads();  // this tile is there, and the one before has been read
+    if (tid < kBlocks) odd_first[(tile + 2) % 3][tid] = kTile;
+    if (tile + 1 < tiles) {
+      here = ok;
+      put(tile + 1, here);
+      if (tile + 2 < tiles) {
+        place(tile + 2);
+        fetch();
+        look_up(tile + 3);
+      }
+    }
+    if (row0 + 16 * wave >= rows) continue;
+#pragma unroll 1
+    for (int half = 0; half < kTile / 32; ++half) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = 32 * half + 16 * h + n;
+        Own<D> k;
+        if constexpr (D == 64) {
+          const int w = spot(r, g4 >> 1);
+          const uint2 y = reinterpret_cast<const uint2*>(&Kc[buf][w])[g4 & 1];
+          k.codes[0] = y.x;
+          k.codes[1] = y.y;
+          k.scale[0] = Ks[buf][w];
+        } else {
+#pragma unroll
+          for (int y = 0; y < D / 128; ++y) {
+            const int w = spot(r, D / 128 * g4 + y);
+            const u32x4 c = Kc[buf][w];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) k.codes[4 * y + i] = c[i];
+            k.scale[y] = Ks[buf][w];
+          }
+        }
+        x.sc[0][h] = query.scores(k);
+      }
+      const int p0 = t0 + 32 * half;
+      x.softmax(p.scale, whole, (uint32_t)(now >> (32 * half)), p0);
+      x.values(Vs[buf], 32 * half);
+    }
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+      const int first = gdn::uniform(odd_first[tile % 3][b]);
+      if (first < kTile) mark_odd(x, b, t0 + first);
+    }
+  }
+  x.finish(a, table, begin, 32, stop);
+  const int row = row0 + 16 * wave + n;
+  if (row >= rows) return;
+  float f;
+  float* dst = row_out(p, s, hk, row, D, x.m[0], x.l[0], g4 == 0, f);
+#pragma unroll
+  for (int c = 0; c < R::CT; ++c)
+    *reinterpret_cast<f32x4*>(dst + 16 * c + 4 * g4) = x.acc[0][c] * f;
+}
+
+// ---------------------------------------------------------------- host side
+constexpr int kFew4Blocks = 2048, kRows4Blocks = 512;
+
+static Shape shape4_of(const gdn_kv_dims& d) {
+  return shape_of(d, kFew4Blocks, kRows4Blocks);
+}
+
+template <int D, typename T>
+static hipError_t attend4(const gdn_kv_dims& d, const Shape& s,
+                          const Attend4Args& p, const gdn::LaneTable& tl,
+                          hipStream_t st) {
+  const dim3 grid((unsigned)((long)s.items * d.h_kv * s.groups));
+  hipError_t e;
+  if (!s.few) {
+    if constexpr (D < 256) {
+      e = s.waves == 8
+              ? launch(rows4_kernel<D, T, 8>, grid, dim3(512), st, p, tl)
+              : launch(rows4_kernel<D, T, 4>, grid, dim3(256), st, p, tl);
+    } else {
+      e = launch(rows4_kernel<D, T, 4>, grid, dim3(256), st, p, tl);
+    }
+  } else if constexpr (D < 256) {
+    e = s.rt == 2 ? launch(attend4_kernel<D, T, 2>, grid, dim3(256), st, p, tl)
+                  : launch(attend4_kernel<D, T, 1>, grid, dim3(256), st, p, tl);
+  } else {
+    e = launch(attend4_kernel<D, T, 1>, grid, dim3(256), st, p, tl);
+  }
+  return e != hipSuccess ? e : join<D>(d, s, p.at, tl, st);
+}
+
+template <typename T>
+static hipError_t attend4(const gdn_kv_dims& d, const Shape& s,
+                          const Attend4Args& p, const gdn::LaneTable& tl,
+                          hipStream_t st) {
+  if (d.d == 64) return attend4<64, T>(d, s, p, tl, st);
+  if (d.d == 128) return attend4<128, T>(d, s, p, tl, st);
+  return attend4<256, T>(d, s, p, tl, st);
 }
 
 }  // namespace gdnk
@@ -105,9 +496,10 @@ __global__ __launch_bounds__(256) void attend4_kernel(Attend4Args p,
 extern "C" size_t gdn_paged_attention_mxfp_workspace_bytes(
     const gdn_kv_dims* dims) {
   if (gdnk::check_kv_dims("gdn_paged_attention_mxfp_workspace_bytes", dims) !=
-      GDN_OK)
+          GDN_OK ||
+      !gdnk::rows_fit(*dims))
     return 0;
-  return gdnk::attend_bytes(*dims);
+  return gdnk::slot_bytes(*dims, gdnk::shape4_of(*dims));
 }
 
 extern "C" int gdn_paged_attention_mxfp(
@@ -129,6 +521,8 @@ extern "C" int gdn_paged_attention_mxfp(
       misaligned(workspace, 16) || misaligned(page_table, 4) ||
       misaligned(kv_len, 4))
     return fail(GDN_EINVAL, "gdn_paged_attention_mxfp: misaligned pointer");
+  if (!rows_fit(*dims))
+    return fail(GDN_EINVAL, "gdn_paged_attention_mxfp: 2^32 rows or more in the cache");
   const size_t need = gdn_paged_attention_mxfp_workspace_bytes(dims);
   if (need > 0 && (!workspace || ws_bytes < need))
     return fail(GDN_EWORKSPACE, "gdn_paged_attention_mxfp: workspace too small");
@@ -137,14 +531,22 @@ extern "C" int gdn_paged_attention_mxfp(
   rc = check_lanes(fn, *dims, t_lane, tl, any);
   if (rc != GDN_OK) return rc;
   if (!any) return GDN_OK;
-  Attend4Args p = {kv_args(*dims, nullptr, nullptr, page_table, kv_len),
-                   {(uint8_t*)k_codes, (uint8_t*)k_scales},
-                   {(uint8_t*)v_codes, (uint8_t*)v_scales},
-                   q, o, scale * kLog2e};
-  const dim3 grid((unsigned)((long)dims->n_lanes * dims->t_max * dims->h_q));
+  const Shape s = shape4_of(*dims);
+  Attend4Args p;
+  p.at.kv = kv_args(*dims, nullptr, nullptr, page_table, kv_len);
+  p.at.q = q;
+  p.at.o = o;
+  p.at.part_o = (float*)workspace;
+  p.at.part_ml = p.at.part_o + (size_t)s.slots * dims->h_kv * s.rows * dims->d;
+  p.at.scale = scale * kLog2e;
+  p.at.target = s.target;
+  p.at.rows = s.rows;
+  p.at.groups = s.groups;
+  p.k4 = {(uint8_t*)k_codes, (uint8_t*)k_scales};
+  p.v4 = {(uint8_t*)v_codes, (uint8_t*)v_scales};
   const hipError_t e =
       dtype == GDN_BF16
-          ? launch(attend4_kernel<uint16_t>, grid, dim3(256), (hipStream_t)stream, p, tl, dims->d)
-          : launch(attend4_kernel<float>, grid, dim3(256), (hipStream_t)stream, p, tl, dims->d);
+          ? attend4<uint16_t>(*dims, s, p, tl, (hipStream_t)stream)
+          : attend4<float>(*dims, s, p, tl, (hipStream_t)stream);
   return gdn::hip_status(e, "gdn_paged_attention_mxfp launch");
 }

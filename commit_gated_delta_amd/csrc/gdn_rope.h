@@ -309,6 +309,8 @@ extern "C" int gdn_rope_append_mxfp(
       misaligned(v_codes, 16) || misaligned(v_scales, 16) ||
       misaligned(k_held, 16) || misaligned(v_held, 16))
     return fail(GDN_EINVAL, "gdn_rope_append_mxfp: misaligned pointer");
+  if (!rows_fit(*dims))
+    return fail(GDN_EINVAL, "gdn_rope_append_mxfp: 2^32 rows or more in the cache");
   if (!any) return GDN_OK;
   RopeArgs p = {kv_args(*dims, nullptr, nullptr, page_table, kv_len),
                 q, k, v, q_stride, k_stride, v_stride, q_out, nullptr, nullptr,

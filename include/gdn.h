@@ -624,8 +624,9 @@ int gdn_rope_append(const gdn_kv_dims* dims, const int32_t* t_lane,
  *               tokens' rows as the cache holds them (exact in bf16), for a
  *               prompt's own attention that is to see what later steps will;
  *               written for dropped rows too
- * The rest as for gdn_rope_append.  All eight pointers to cache rows, codes,
- * scales and held rows must be 16-byte aligned.
+ * The rest as for gdn_rope_append, but n_pages * h_kv * page_size < 2^32
+ * (GDN_EINVAL).  Pointers to codes, scales and held rows must be 16-byte
+ * aligned.
  */
 int gdn_rope_append_mxfp(const gdn_kv_dims* dims, const int32_t* t_lane,
                         const void* q, int64_t q_stride, const void* k,
@@ -638,11 +639,13 @@ int gdn_rope_append_mxfp(const gdn_kv_dims* dims, const int32_t* t_lane,
                         int flags, void* stream);
 
 /*
- * gdn_paged_attention over that cache (or any in its layout; byte 0 is
- * 2^-127, byte 255 NaN).  Queries are bf16 or f32, the products and sums f32
- * or wider; a query row that holds an infinity or a NaN gives NaN.  The rest,
- * what masked rows may hold among it, as for gdn_paged_attention, with its
- * own workspace size.
+ * gdn_paged_attention over that cache (or any in its layout: scale byte 0 is
+ * 2^-127, and a block whose byte is 253 to 255 reads as NaN; a value below
+ * 2^-126 may count as zero).  Queries are
+ * bf16 or f32, the products and sums f32 or wider; a query row that holds an
+ * infinity or a NaN gives NaN.  n_pages * h_kv * page_size < 2^32
+ * (GDN_EINVAL).  The rest, what masked rows may hold among it, as for
+ * gdn_paged_attention, with its own workspace size.
  */
 size_t gdn_paged_attention_mxfp_workspace_bytes(const gdn_kv_dims* dims);
 int gdn_paged_attention_mxfp(const gdn_kv_dims* dims, const int32_t* t_lane,

@@ -97,20 +97,16 @@ def attend(q, k, v, table, kv_len, t_lane, scale, page, n_pages):
     """f64 attention over decoded rows k, v [n_pages, h_kv, page, d]: (o,
     bound); rows of idle tokens are NaN in o.
 
-    A score is off by (d + 8) U32 of the sum of its terms' sizes, and by what
-    the query loses when it is cut into parts of four bits under a common
-    scale per 32 channels: 2^-22 of the block's largest magnitude for every
-    channel (the last part's step below its normal numbers).  Through the
-    softmax an error e of the scores (and of the largest one) moves an output
-    by 4 e of sum p |v|, the sums by one step a position, and a few
-    roundings."""
+    A score is off by (d + 8) U32 of the sum of its terms' sizes (the codes'
+    values and the bf16 parts of an f32 query are exact).  Through the softmax
+    an error e of the scores (and of the largest one) moves an output by 4 e of
+    sum p |v|, the sums by one step a position, and a few roundings."""
     N, T, Hq, d = q.shape
     Hkv = k.shape[1]
     group = Hq // Hkv
     q, table, kv_len = q.double().cpu(), table.cpu(), kv_len.cpu()
     o = torch.full(q.shape, math.nan, dtype=torch.float64)
     tol = torch.zeros(q.shape, dtype=torch.float64)
-    qmax = q.abs().unflatten(-1, (-1, 32)).amax(-1)
     cap = table.shape[1] * page
     for n in range(N):
         length = min(max(int(kv_len[n]), 0), cap)
@@ -129,10 +125,9 @@ def attend(q, k, v, table, kv_len, t_lane, scale, page, n_pages):
                 rows = slice(h * group, (h + 1) * group)
                 x = scale * q[n, t, rows] @ a.T                     # [group, L]
                 size = abs(scale) * q[n, t, rows].abs() @ a.abs().T
-                lost = abs(scale) * qmax[n, t, rows] @ a.abs().unflatten(-1, (-1, 32)).sum(-1).T
                 p = torch.softmax(x, 1)
                 o[n, t, rows] = p @ b
-                e = ((d + 8) * U32 * size + 2.0 ** -22 * lost).amax(1) + 4 * U32
+                e = (d + 8) * U32 * size.amax(1) + 4 * U32
                 mag = p @ b.abs()
                 tol[n, t, rows] = mag * (4 * e[:, None] + (2 * a.shape[0] + 16) * U32)
     return o, tol + 1e-30

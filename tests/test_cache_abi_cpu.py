@@ -69,7 +69,8 @@ def test_rope_refusals(fp4):
             c[i] = what
             bad.append(dict(caches=c))
     if fp4:
-        bad += [dict(held=(P + 8, None)), dict(held=(None, P + 2))]
+        bad += [dict(held=(P + 8, None)), dict(held=(None, P + 2)),
+                dict(n_pages=1 << 27)]                   # 2^32 rows
     for b in bad:
         assert _rope(fp4, **b) == EINVAL, b
         assert _message()
@@ -91,7 +92,8 @@ def test_attention_refusals():
     bad = BAD_KV + [dict(t=(5, 1)), dict(t=(-1, 1)), dict(t_null=True),
                     dict(q=None), dict(table=None), dict(lens=None),
                     dict(o=None), dict(dt=3), dict(q=P + 8), dict(o=P + 4),
-                    dict(ws=P + 8), dict(table=P + 2), dict(lens=P + 1)]
+                    dict(ws=P + 8), dict(table=P + 2), dict(lens=P + 1),
+                    dict(n_pages=1 << 27)]               # 2^32 rows
     for i in range(4):
         for what in (None, P + 8):
             c = [P] * 4
@@ -105,7 +107,7 @@ def test_attention_refusals():
     assert _attend(ws_bytes=need - 1) == EWORK
     assert _attend(ws=None) == EWORK
     assert _attend(t=(0, 0)) == OK
-    for b in BAD_KV + [dict(d=96)]:
+    for b in BAD_KV + [dict(d=96), dict(n_pages=1 << 27)]:
         assert gdn.paged_attention_mxfp_workspace_bytes(_kv(**b)) == 0
     assert gdn.lib.gdn_paged_attention_mxfp_workspace_bytes(None) == 0
     assert gdn.lib.gdn_paged_attention_mxfp(

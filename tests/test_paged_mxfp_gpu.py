@@ -124,8 +124,7 @@ def test_peaked_scores(kind, T):
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 def test_queries_of_any_size(kind):
-    """Blocks of a query row from tiny to huge, zeros among them: each has a
-    scale of its own."""
+    """Blocks of a query row from tiny to huge, zeros among them."""
     x = _case([1, 2], [90, 30], 4, 2, 128, 16, kind)
     for i, f in enumerate((1e-30, 1e-3, 0.0, 1e4)):
         x["q"][0, 0, :, 32 * i:32 * i + 32] *= f
@@ -208,6 +207,32 @@ def test_later_tokens_of_a_window_do_not_matter(T, h_q, d, kind):
     assert torch.isnan(first[..., :32]).all()
     assert torch.equal(first[..., 32:], clean[0, bad:, :h_q // 2][..., 32:])
     assert torch.isnan(second).all()
+
+
+@pytest.mark.parametrize("byte", [253, 254, 255])
+@pytest.mark.parametrize("T,d", [(1, 64), (1, 128), (2, 256), (40, 64), (40, 128), (40, 256)])
+def test_blocks_that_read_as_nan(byte, T, d):
+    """Value blocks with the largest scale bytes, in one and in several
+    places of a step: NaN in their channels for the tokens that see one, the
+    other channels as before.  Key blocks: NaN in every channel."""
+    x = _case([T], [500], 4, 2, d, 16, "bf16")
+    clean = _run(x, [T], 0.1)
+    bad = {0: [3, 17, 300], d // 32 - 1: [500 - T // 2 - 1, 499]}     # block: positions
+    for b, where in bad.items():
+        for pos in where:
+            x["v_scales"][int(x["table"][0, pos // 16]), 1, pos % 16, b] = byte
+    o = _run(x, [T], 0.1)
+    assert torch.equal(o[0, :, :2], clean[0, :, :2])
+    want = clean.clone()
+    for b, where in bad.items():
+        for t in range(T):
+            if min(where) <= 500 - T + t:
+                want[0, t, 2:, 32 * b:32 * b + 32] = math.nan
+    assert torch.equal(torch.isnan(o), torch.isnan(want))
+    assert torch.equal(o.nan_to_num(9.0), want.nan_to_num(9.0))
+    x["k_scales"][int(x["table"][0, 400 // 16]), 0, 400 % 16, 1] = byte
+    o = _run(x, [T], 0.1)
+    assert torch.isnan(o[0, :, :2]).all() and torch.equal(o[0, :, 2:].nan_to_num(9.0), want[0, :, 2:].nan_to_num(9.0))
 
 
 def test_nan_in_the_cache_reaches_the_rows_that_see_it():
