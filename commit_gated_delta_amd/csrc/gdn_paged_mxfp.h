@@ -27,8 +27,9 @@
 namespace gdnk {
 
 struct Attend4Args {
-  AttendArgs at;
+  AttendArgs at;  // (its scale without its sign)
   Fp4Rows k4, v4;
+  uint32_t flip;  // turns the signs of a dword of q, where the scale is negative
 };
 
 // What lane 16 g + n holds of a row: its channels D / 4 g .. D / 4 (g + 1) - 1,
@@ -40,8 +41,11 @@ struct Own {
   static constexpr int kScales = D == 256 ? 2 : 1;
   uint32_t codes[kDwords];
   uint32_t scale[kScales];
-  __device__ __forceinline__ void load(const Fp4Rows& c, uint32_t row, int g) {
-    const uint8_t* at = c.codes + ((uint64_t)row * (D / 2) + (D / 8) * g);
+  // Of row `row` + `more`, which may be the wave's and the lane's part.
+  __device__ __forceinline__ void load(const Fp4Rows& c, uint32_t row,
+                                       uint32_t more, int g) {
+    const uint8_t* at = c.codes + (uint64_t)row * (D / 2) +
+                        (more * (D / 2) + (D / 8) * g);
     if constexpr (D == 64) {
       const uint2 w = *reinterpret_cast<const uint2*>(at);
       codes[0] = w.x;
@@ -56,12 +60,17 @@ struct Own {
     }
     const uint8_t* s = c.scales + (uint64_t)row * (D / 32);
     if constexpr (D == 256) {
-      const uint32_t w = *reinterpret_cast<const uint16_t*>(s + 2 * g);
+      const uint32_t w =
+          *reinterpret_cast<const uint16_t*>(s + (more * (D / 32) + 2 * g));
       scale[0] = w & 255;
       scale[1] = w >> 8;
     } else {
-      scale[0] = s[D == 64 ? g >> 1 : g];
+      scale[0] = s[more * (D / 32) + (D == 64 ? g >> 1 : g)];
     }
+  }
+  __device__ __forceinline__ bool odd() const {  // whether a block is NaN
+    const uint32_t x = scale[0], y = scale[kScales - 1];
+    return (x > y ? x : y) >= kScaleOdd;
   }
   __device__ __forceinline__ u32x4 values(int i) const {
     return fp4_values(codes[i], scale[i * kScales / kDwords]);
@@ -75,27 +84,39 @@ struct Query {
   typedef Op<uint16_t> O;
   typedef std::conditional_t<sizeof(T) == 2, u32x4, typename O::Wide> Piece;
   Piece q[D / 32];
-  // The row at `row`, or zeros.
-  __device__ __forceinline__ void load(const T* row, bool zero) {
+  // The row at `row`, its signs turned by `flip`, or zeros.
+  __device__ __forceinline__ void load(const T* row, uint32_t flip, bool zero) {
     const T* at = row + (D / 4) * ((threadIdx.x & 63) >> 4);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       u32x4 w[sizeof(T) / 2];
 #pragma unroll
       for (int y = 0; y < (int)sizeof(T) / 2; ++y) {
-        w[y] = reinterpret_cast<const u32x4*>(at + 8 * i)[y];
+        w[y] = reinterpret_cast<const u32x4*>(at + 8 * i)[y] ^ flip;
         if (zero) w[y] = u32x4{0, 0, 0, 0};
       }
       if constexpr (sizeof(T) == 2) q[i] = w[0];
       else q[i] = O::wide(__builtin_bit_cast(f32x4, w[0]), __builtin_bit_cast(f32x4, w[1]));
     }
   }
-  // Scores of 16 positions.
-  __device__ __forceinline__ f32x4 scores(const Own<D>& k) const {
-    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+  // Scores of twice 16 positions (two chains of products).
+  __device__ __forceinline__ void scores(const Own<D> (&k)[2],
+                                         f32x4 (&c)[2]) const {
+    c[0] = c[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) c = O::mul(k.values(i), q[i], c);
-    return c;
+    for (int i = 0; i < D / 32; ++i) {
+      const u32x4 a = k[0].values(i), b = k[1].values(i);
+      if constexpr (sizeof(T) == 2) {
+        c[0] = O::mul(a, q[i], c[0]);
+        c[1] = O::mul(b, q[i], c[1]);
+      } else {
+#pragma unroll
+        for (int y = 0; y < O::kSteps; ++y) {
+          c[0] = O::step(y, a, q[i], c[0]);
+          c[1] = O::step(y, b, q[i], c[1]);
+        }
+      }
+    }
   }
 };
 
@@ -108,11 +129,140 @@ __device__ __forceinline__ const T* query_row(const AttendArgs& p, int lane,
                           hk * group + row % group) * D;
 }
 
+// A V tile as Tile's, with neighbouring pieces swapped in every other eight
+// rows: 16 lanes then write one piece of 16 rows, as they read two of eight,
+// without a conflict (13 % of a wave's time at D = 128).
+template <int D>
+struct VTile {
+  typedef Tile<uint16_t, D, true> Base;
+  static constexpr int kPitch = Base::kPitch;
+  static __device__ __forceinline__ int at(int r, int p) {
+    return Base::at(r, p ^ (r >> 3 & 1));
+  }
+};
+
+// Scores, softmax state and outputs of a wave, as Rows.  The scale is not
+// negative here (a query's signs carry that), so the largest of the raw
+// scores tells whether m is to be raised, and one operation scales a score
+// and subtracts m.
+template <int D, int RT>
+struct Rows4 : Rows<D, uint16_t, RT> {
+  typedef Rows<D, uint16_t, RT> R;
+  float lim[RT];   // raw score from which m is raised
+  float base[RT];  // what is added to a scaled score: -m, 0 before the first
+
+  __device__ __forceinline__ void init(int row0, int rows, int len, int T_n,
+                                       int group) {
+    R::init(row0, rows, len, T_n, group);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      lim[r] = -INFINITY;
+      base[r] = 0.f;
+    }
+  }
+  // As Rows::softmax, on the raw scores in sc.
+  __device__ __forceinline__ void softmax(float scale, bool whole, uint32_t ok,
+                                          int p0) {
+    const int g4 = (threadIdx.x & 63) >> 4;
+    uint32_t sees[RT];  // bit 4 h + e: score [h][e] counts
+    if (!whole) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        sees[r] = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = 16 * h + 4 * g4 + e;
+            const bool on = (ok >> i & 1) && p0 + i < this->end[r];
+            sees[r] |= on << (4 * h + e);
+            if (!on) this->sc[r][h][e] = -INFINITY;
+          }
+      }
+    }
+    bool raise = false;
+    float top[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const f32x4 a = this->sc[r][0], b = this->sc[r][1];
+      top[r] = fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])),
+                     fmaxf(fmaxf(b[0], b[1]), fmaxf(b[2], b[3])));
+      raise |= top[r] > lim[r];
+    }
+    if (__any(raise)) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        float t = top[r];
+        t = fmaxf(t, __shfl_xor(t, 16));
+        t = fmaxf(t, __shfl_xor(t, 32));
+        t = t == -INFINITY ? t : fmaxf(this->m[r], t * scale);
+        if (t > this->m[r]) {
+          const float keep = this->m[r] == -INFINITY
+                                 ? 0.f
+                                 : __builtin_amdgcn_exp2f(this->m[r] - t);
+          this->m[r] = t;
+          base[r] = -t;
+          lim[r] = scale > 0.f ? (t + kSlack) / scale : INFINITY;
+          this->l[r] *= keep;
+#pragma unroll
+          for (int c = 0; c < R::CT; ++c) this->acc[r][c] *= keep;
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          this->sc[r][h][e] = __builtin_amdgcn_exp2f(
+              __builtin_fmaf(this->sc[r][h][e], scale, base[r]));
+    if (!whole) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!(sees[r] >> (4 * h + e) & 1)) this->sc[r][h][e] = 0.f;
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const f32x4 a = this->sc[r][0], b = this->sc[r][1];
+      this->l[r] += ((a[0] + a[1]) + (a[2] + a[3])) + ((b[0] + b[1]) + (b[2] + b[3]));
+    }
+  }
+  // O^T += V^T P^T with V rows r0 .. r0 + 31 of the tile.
+  __device__ __forceinline__ void values(const uint16_t* Vs, int r0) {
+    typedef Op<uint16_t> O;
+    typename O::Wide pw[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      pw[r] = O::wide(this->sc[r][0], this->sc[r][1]);
+    constexpr int kTwo = RT == 1 ? 2 : 1;  // two accumulators at least
+#pragma unroll
+    for (int c = 0; c < R::CT; c += kTwo) {
+      u32x4 vf[kTwo];
+#pragma unroll
+      for (int y = 0; y < kTwo; ++y)
+        vf[y] = O::template column<VTile<D>>(Vs, r0, 16 * (c + y), 4,
+                                             threadIdx.x & 63);
+#pragma unroll
+      for (int i = 0; i < O::kSteps; ++i)
+#pragma unroll
+        for (int y = 0; y < kTwo; ++y)
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            this->acc[r][c + y] = O::step(i, vf[y], pw[r], this->acc[r][c + y]);
+    }
+  }
+};
+
 // Rows that see a position whose value block b is NaN get NaN in its
 // channels; `values` took it as zeros.  What a row sees is a prefix, so the
 // first such position, p0 + first, is enough.
 template <int D, int RT>
-__device__ __forceinline__ void mark_odd(Rows<D, uint16_t, RT>& x, int b,
+__device__ __forceinline__ void mark_odd(Rows4<D, RT>& x, int b,
                                          int pos) {
 #pragma unroll
   for (int r = 0; r < RT; ++r)
@@ -127,8 +277,8 @@ __device__ __forceinline__ void mark_odd(Rows<D, uint16_t, RT>& x, int b,
 // the registers of bf16 ones.
 template <int D, typename T, int RT>
 constexpr int few4_waves() {
-  constexpr int q = D * RT * (int)sizeof(T);  // 128 * 2: one tile in bf16
-  return q <= 256 ? 3 : q <= 512 ? 2 : 1;
+  constexpr int q = D * RT * (int)sizeof(T);
+  return D * RT == 64 ? 4 : q <= 256 ? 3 : q <= 512 ? 2 : 1;
 }
 template <int D, typename T, int NW>
 constexpr int rows4_waves() {
@@ -146,11 +296,13 @@ __device__ __forceinline__ uint32_t cache_row(const KvArgs& a, int page, int h,
 
 // Few rows, as attend_kernel: four waves share out a split's positions, 32 at
 // a step, and lane 16 g + n holds its channels of positions n and 16 + n.
-template <int D, typename T, int RT>
+// EVEN: pages are multiples of 16 positions, so that each half of a step lies
+// in one page, whose number and place are the wave's and not the lanes'.
+template <int D, typename T, int RT, bool EVEN>
 __global__ __launch_bounds__(256, (few4_waves<D, T, RT>())) void attend4_kernel(
     Attend4Args q, gdn::LaneTable tl) {
-  typedef Rows<D, uint16_t, RT> R;
-  typedef typename R::VL VL;
+  typedef Rows4<D, RT> R;
+  typedef VTile<D> VL;
   typedef Own<D> Part;
   constexpr int kRows = 16 * RT;
   constexpr int kTileBytes = 32 * D * 2;
@@ -176,32 +328,39 @@ __global__ __launch_bounds__(256, (few4_waves<D, T, RT>())) void attend4_kernel(
 
   int page[2];     // page numbers of the step after the next
   bool there[2];   // whether the positions of the step in hand are
-  uint32_t at[2];  // and their rows
+  uint32_t at[2];  // and their rows (EVEN: that of the half's first one)
+  const uint32_t more = EVEN ? n : 0;
+  auto pos_of = [&](int step, int h) {
+    return begin + 32 * step + 16 * h + (EVEN ? 0 : n);
+  };
   auto look_up = [&](int step) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int pos = begin + 32 * step + 16 * h + n;
+      const int pos = pos_of(step, h);
       page[h] = pos < stop ? table[page_of(a, pos)] : -1;
     }
   };
   auto place = [&](int step) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      at[h] = cache_row(a, page[h], hk, begin + 32 * step + 16 * h + n, there[h]);
+    for (int h = 0; h < 2; ++h) {
+      const int pos = pos_of(step, h);
+      at[h] = cache_row(a, page[h], hk, pos, there[h]);
+      if (EVEN) there[h] = there[h] && pos + n < stop;
+    }
   };
   Part kp[2], vp[2];
   auto fetch = [&](const Fp4Rows& c, Part (&r)[2]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) r[h].load(c, at[h], g4);
+    for (int h = 0; h < 2; ++h) r[h].load(c, at[h], more, g4);
   };
 
-  if (wave < steps) {
-    look_up(wave);
-    place(wave);
-    fetch(q.k4, kp);
-    fetch(q.v4, vp);
-    look_up(wave + 4);
-  }
+  // (Past the last step a lane loads the cache's first row: a branch around
+  // the loads would have the compiler copy what they return, and wait for it.)
+  look_up(wave);
+  place(wave);
+  fetch(q.k4, kp);
+  fetch(q.v4, vp);
+  look_up(wave + 4);
   R x;
   x.init(0, rows, s.len, T_n, group);
   Query<D, T> query[RT];
@@ -209,24 +368,22 @@ __global__ __launch_bounds__(256, (few4_waves<D, T, RT>())) void attend4_kernel(
   for (int r = 0; r < RT; ++r) {
     // (rows past the last: the first one's channels as zeros)
     const int row = 16 * r + n < rows ? 16 * r + n : 0;
-    query[r].load(query_row<D, T>(p, s.lane, hk, row), 16 * r + n >= rows);
+    query[r].load(query_row<D, T>(p, s.lane, hk, row), q.flip, 16 * r + n >= rows);
   }
   for (int step = wave; step < steps; step += 4) {
     const bool here[2] = {there[0], there[1]};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      if (__any(kp[h].odd()))
 #pragma unroll
-      for (int y = 0; y < Part::kScales; ++y)
-        if (kp[h].scale[y] >= kScaleOdd) kp[h].scale[y] = kScaleNan;
+        for (int y = 0; y < Part::kScales; ++y)
+          if (kp[h].scale[y] >= kScaleOdd) kp[h].scale[y] = kScaleNan;
+    }
 #pragma unroll
-      for (int r = 0; r < RT; ++r) x.sc[r][h] = query[r].scores(kp[h]);
-    }
-    const int next = step + 4;
-    if (next < steps) {
-      place(next);
-      fetch(q.k4, kp);
-      look_up(next + 4);
-    }
+    for (int r = 0; r < RT; ++r) query[r].scores(kp, x.sc[r]);
+    place(step + 4);
+    fetch(q.k4, kp);
+    look_up(step + 8);
     const int p0 = begin + 32 * step;
     const bool whole =
         p0 + 32 <= (open < stop ? open : stop) && __all(here[0] && here[1]);
@@ -235,28 +392,30 @@ __global__ __launch_bounds__(256, (few4_waves<D, T, RT>())) void attend4_kernel(
       ok = ((uint32_t)__ballot(here[0]) & 0xffffu) |
            ((uint32_t)__ballot(here[1]) & 0xffffu) << 16;
     x.softmax(p.scale, whole, ok, p0);
-    // V through LDS.  Rows that are not there count as zeros.
-    bool off[2][Part::kScales], odd = false;
+    // V through LDS.  Rows that are not there and blocks of NaN count as zeros.
+    bool off[2][Part::kScales];
+    const bool is_odd = __any((here[0] & vp[0].odd()) | (here[1] & vp[1].odd()));
+    if (is_odd || !whole) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int y = 0; y < Part::kScales; ++y) {
-        off[h][y] = here[h] && vp[h].scale[y] >= kScaleOdd;
-        odd |= off[h][y];
-        if (off[h][y] || !here[h]) {
-          vp[h].scale[y] = 0;
+        for (int y = 0; y < Part::kScales; ++y) {
+          off[h][y] = here[h] && vp[h].scale[y] >= kScaleOdd;
+          if (off[h][y] || !here[h]) {
+            vp[h].scale[y] = 0;
 #pragma unroll
-          for (int i = 0; i < Part::kDwords; ++i)
-            if (i * Part::kScales / Part::kDwords == y) vp[h].codes[i] = 0;
+            for (int i = 0; i < Part::kDwords; ++i)
+              if (i * Part::kScales / Part::kDwords == y) vp[h].codes[i] = 0;
+          }
         }
-      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < Part::kDwords; ++i)
         *reinterpret_cast<u32x4*>(Vs + VL::at(n, Part::kDwords * g4 + i) +
                                   16 * h * VL::kPitch) = vp[h].values(i);
-    }
-    const bool is_odd = __any(odd);
-    if (next < steps) fetch(q.v4, vp);
+    fetch(q.v4, vp);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -287,8 +446,8 @@ __global__ __launch_bounds__(256, (few4_waves<D, T, RT>())) void attend4_kernel(
 template <int D, typename T, int NW>
 __global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW>())) void rows4_kernel(
     Attend4Args q, gdn::LaneTable tl) {
-  typedef Rows<D, uint16_t, 1> R;
-  typedef typename R::VL VL;
+  typedef Rows4<D, 1> R;
+  typedef VTile<D> VL;
   constexpr int kRows = 16 * NW, kTile = 64, kBlocks = D / 32;
   constexpr int kPieces = kTile * kBlocks;                    // of K, or of V
   constexpr int kThreads = 64 * NW;
@@ -380,7 +539,7 @@ __global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW>())) void rows4_kern
   Query<D, T> query;
   {
     const int row = row0 + 16 * wave + n;
-    query.load(query_row<D, T>(p, s.lane, hk, row < rows ? row : 0), row >= rows);
+    query.load(query_row<D, T>(p, s.lane, hk, row < rows ? row : 0), q.flip, row >= rows);
   }
   __syncthreads();
   if (tiles > 0) {
@@ -410,28 +569,28 @@ __global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW>())) void rows4_kern
     if (row0 + 16 * wave >= rows) continue;
 #pragma unroll 1
     for (int half = 0; half < kTile / 32; ++half) {
+      Own<D> k[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = 32 * half + 16 * h + n;
-        Own<D> k;
         if constexpr (D == 64) {
           const int w = spot(r, g4 >> 1);
           const uint2 y = reinterpret_cast<const uint2*>(&Kc[buf][w])[g4 & 1];
-          k.codes[0] = y.x;
-          k.codes[1] = y.y;
-          k.scale[0] = Ks[buf][w];
+          k[h].codes[0] = y.x;
+          k[h].codes[1] = y.y;
+          k[h].scale[0] = Ks[buf][w];
         } else {
 #pragma unroll
           for (int y = 0; y < D / 128; ++y) {
             const int w = spot(r, D / 128 * g4 + y);
             const u32x4 c = Kc[buf][w];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) k.codes[4 * y + i] = c[i];
-            k.scale[y] = Ks[buf][w];
+            for (int i = 0; i < 4; ++i) k[h].codes[4 * y + i] = c[i];
+            k[h].scale[y] = Ks[buf][w];
           }
         }
-        x.sc[0][h] = query.scores(k);
       }
+      query.scores(k, x.sc[0]);
       const int p0 = t0 + 32 * half;
       x.softmax(p.scale, whole, (uint32_t)(now >> (32 * half)), p0);
       x.values(Vs[buf], 32 * half);
@@ -459,6 +618,14 @@ static Shape shape4_of(const gdn_kv_dims& d) {
   return shape_of(d, kFew4Blocks, kRows4Blocks);
 }
 
+template <int D, typename T, int RT>
+static hipError_t few4(const gdn_kv_dims& d, dim3 grid, const Attend4Args& p,
+                       const gdn::LaneTable& tl, hipStream_t st) {
+  return d.page_size % 16 == 0
+             ? launch(attend4_kernel<D, T, RT, true>, grid, dim3(256), st, p, tl)
+             : launch(attend4_kernel<D, T, RT, false>, grid, dim3(256), st, p, tl);
+}
+
 template <int D, typename T>
 static hipError_t attend4(const gdn_kv_dims& d, const Shape& s,
                           const Attend4Args& p, const gdn::LaneTable& tl,
@@ -474,10 +641,10 @@ static hipError_t attend4(const gdn_kv_dims& d, const Shape& s,
       e = launch(rows4_kernel<D, T, 4>, grid, dim3(256), st, p, tl);
     }
   } else if constexpr (D < 256) {
-    e = s.rt == 2 ? launch(attend4_kernel<D, T, 2>, grid, dim3(256), st, p, tl)
-                  : launch(attend4_kernel<D, T, 1>, grid, dim3(256), st, p, tl);
+    e = s.rt == 2 ? few4<D, T, 2>(d, grid, p, tl, st)
+                  : few4<D, T, 1>(d, grid, p, tl, st);
   } else {
-    e = launch(attend4_kernel<D, T, 1>, grid, dim3(256), st, p, tl);
+    e = few4<D, T, 1>(d, grid, p, tl, st);
   }
   return e != hipSuccess ? e : join<D>(d, s, p.at, tl, st);
 }
@@ -538,10 +705,11 @@ extern "C" int gdn_paged_attention_mxfp(
   p.at.o = o;
   p.at.part_o = (float*)workspace;
   p.at.part_ml = p.at.part_o + (size_t)s.slots * dims->h_kv * s.rows * dims->d;
-  p.at.scale = scale * kLog2e;
+  p.at.scale = fabsf(scale) * kLog2e;
   p.at.target = s.target;
   p.at.rows = s.rows;
   p.at.groups = s.groups;
+  p.flip = !(scale < 0.f) ? 0u : dtype == GDN_BF16 ? 0x80008000u : 0x80000000u;
   p.k4 = {(uint8_t*)k_codes, (uint8_t*)k_scales};
   p.v4 = {(uint8_t*)v_codes, (uint8_t*)v_scales};
   const hipError_t e =
