@@ -10,6 +10,10 @@
 // tokens are then distributed as p says, whatever the drafter's q (Leviathan,
 // Kalman & Matias, "Fast Inference from Transformers via Speculative
 // Decoding", ICML 2023, Sec. 2.3 and appendix A.1).
+//
+// A token is where a running sum passes a given number, so an error d of the
+// sums moves it with a chance of about d times the number of likely tokens:
+// every exponential and sum here is f64.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -25,6 +29,25 @@ using gdn::fail;
 using gdn::launch;
 using gdn::misaligned;
 using gdnt::logit_at;
+using gdnt::round16;
+using gdnt::u32x4;
+
+// What a slice of a row leaves behind: its largest logit (NaN if it holds
+// one), the sum of 2^((x - m) c) with that as m, and the same without the
+// row's draft.
+struct Part {
+  double z, zx;
+  float m;
+  int pad;
+};
+
+// What a lane's window comes to.
+struct Verdict {
+  int m;   // accepted prefix, the anchor included
+  int ok;  // row m - 1 (and the drafter's, if a draft fell) has a distribution
+  double top, z;              // of row m - 1
+  double draft_top, draft_z;  // of the drafter's row m - 1, if a draft fell
+};
 
 struct DraftArgs {
   const void *logits, *draft;
@@ -36,125 +59,511 @@ struct DraftArgs {
   float* accept;
   long stride, draft_stride;
   int lanes, t_max, vocab;
+  int slices;        // of a row, in `parts`
+  int rest_slices;   // of a row, in `rest`
+  Part* parts;       // [target rows, then drafter's rows][slices]
+  double* rest;      // [lanes][rest_slices]: sums of max(p - q, 0)
+  Verdict* verdicts;  // [lanes], of windows with drafts that have a distribution
 };
 
-constexpr int kBlock = 1024;
+constexpr int kThreads = 256;   // of sum_kernel
+constexpr int kWide = 1024;     // of the kernels behind it
+constexpr int kRestSlice = 8192;  // ids of a slice of rest_kernel
 
-__device__ __forceinline__ double block_sum(double x, double* red) {
-  for (int i = 32; i > 0; i /= 2) x += __shfl_xor(x, i);
-  __syncthreads();
-  if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = x;
-  __syncthreads();
-  double s = 0;
-  for (int i = 0; i < kBlock / 64; ++i) s += red[i];
-  return s;
+// 2^y for -1020 <= y <= 1, to 4e-16: a polynomial through the Chebyshev nodes
+// of [-1/2, 1/2] for the fraction (off by 3e-16), the whole part added to the
+// exponent.  (The library's exp takes twice the instructions.)
+__device__ __forceinline__ double exp2_f64(double y) {
+  constexpr double kWhole = 6755399441055744.0;  // 1.5 * 2^52: no fraction left
+  const double t = y + kWhole, f = y - (t - kWhole);
+  double e = 7.07258594926922421e-09;
+  e = __builtin_fma(e, f, 1.02086902999583060e-07);
+  e = __builtin_fma(e, f, 1.32154425879216893e-06);
+  e = __builtin_fma(e, f, 1.52526572602008367e-05);
+  e = __builtin_fma(e, f, 1.54035304417360499e-04);
+  e = __builtin_fma(e, f, 1.33335582301649744e-03);
+  e = __builtin_fma(e, f, 9.61812910760688825e-03);
+  e = __builtin_fma(e, f, 5.55041086644477225e-02);
+  e = __builtin_fma(e, f, 2.40226506959100972e-01);
+  e = __builtin_fma(e, f, 6.93147180559949949e-01);
+  e = __builtin_fma(e, f, 1.0);
+  const uint64_t u = __builtin_bit_cast(uint64_t, e);
+  const uint32_t whole = (uint32_t)__builtin_bit_cast(uint64_t, t);
+  return __builtin_bit_cast(double, u + ((uint64_t)(whole << 20) << 32));
 }
-// The largest logit of a row (NaN if it holds one).
-template <typename T>
-__device__ __forceinline__ float row_max(const T* x, int vocab, float* red) {
-  float m = -INFINITY;
-  for (int i = threadIdx.x; i < vocab; i += kBlock)
-    m = __builtin_elementwise_maximum(m, logit_at(x, i));
-  for (int i = 32; i > 0; i /= 2) m = __builtin_elementwise_maximum(m, __shfl_xor(m, i));
-  __syncthreads();
-  if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = m;
-  __syncthreads();
-  m = red[0];
-  for (int i = 1; i < kBlock / 64; ++i) m = __builtin_elementwise_maximum(m, red[i]);
-  return m;
+// 2^((x - m) c), 0 below 2^-1000 (x = -inf among it).
+constexpr double kLeast = -1000.0;
+__device__ __forceinline__ double weight_of(float x, double m, double c) {
+  const double y = ((double)x - m) * c;
+  const double e = exp2_f64(__builtin_fmax(y, kLeast));
+  return y >= kLeast ? e : 0.0;
+}
+// The same without the zeros, for sums in which 2^-1000 is nothing.
+__device__ __forceinline__ double weight_in_sum(float x, double m, double c) {
+  return exp2_f64(__builtin_fmax(((double)x - m) * c, kLeast));
+}
+// Sums of weights from which a slice counts: its largest one is then above
+// 2^-1000 with any slice's 2^14 ids and a share of a row's 2^30.
+constexpr double kNothing = 0x1p-950;
+__device__ __forceinline__ double or_nothing(double sum) {
+  return sum >= kNothing ? sum : 0.0;
 }
 
-// One workgroup per lane, every sum in f64.
-template <typename T>
-__global__ __launch_bounds__(kBlock) void verify_kernel(DraftArgs p,
-                                                        gdn::LaneTable tl) {
-  __shared__ double red[kBlock];
-  const int n = blockIdx.x, tid = threadIdx.x, V = p.vocab, T_n = tl.v[n];
-  if (T_n == 0) return;
-  const double it = p.it[n];
-  const bool it_ok = p.it[n] >= 1e-30f && p.it[n] <= 1e30f;
-  auto target = [&](int t) { return (const T*)p.logits + ((long)n * p.t_max + t) * p.stride; };
-  auto drafter = [&](int t) { return (const T*)p.draft + ((long)n * (p.t_max - 1) + t) * p.draft_stride; };
-  auto chance = [&](const T* x, long i, double m) { return exp(((double)logit_at(x, i) - m) * it); };
-  // the row's largest logit and the sum of its exponentials; false: it has
-  // no distribution
-  auto sums = [&](const T* x, double& m, double& z) {
-    m = row_max(x, V, (float*)red);
-    if (!it_ok || !(fabs(m) < INFINITY)) return false;
-    double s = 0;
-    for (int i = tid; i < V; i += kBlock) s += chance(x, i, m);
-    z = block_sum(s, red);
-    return true;
-  };
-  int m = 1;
-  bool open = true;
-  double zm, z, dm = 0, dz = 1;
-  for (int t = 0; t < T_n - 1; ++t) {
-    bool ok = sums(target(t), zm, z);
-    if (p.draft) ok &= sums(drafter(t), dm, dz);
-    const int w = p.tokens[(long)n * p.t_max + t + 1];
-    double pw = 0, qw = 1;
-    if ((unsigned)w < (unsigned)V && ok) {
-      pw = chance(target(t), w, zm) / z;
-      if (p.draft) qw = chance(drafter(t), w, dm) / dz;
-    }
-    if (open && ok && (double)p.uniforms[(long)n * p.t_max + t] * qw < pw) ++m;
-    else open = false;
-    if (p.accept && tid == 0)
-      p.accept[(long)n * p.t_max + t] = !ok ? NAN : pw == 0 ? 0.f : pw >= qw ? 1.f : (float)(pw / qw);
+template <int CTRL>
+__device__ __forceinline__ double dpp64(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xf, 0xf, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, 0xf, 0xf, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane_value(double x, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Sum over the 64 lanes, the same in every lane, in a fixed order.
+__device__ __forceinline__ double wave_sum64(double x) {
+  x += dpp64<0xB1>(x);
+  x += dpp64<0x4E>(x);
+  x += dpp64<0x141>(x);
+  x += dpp64<0x140>(x);
+  return (lane_value(x, 0) + lane_value(x, 16)) +
+         (lane_value(x, 32) + lane_value(x, 48));
+}
+__device__ __forceinline__ double wave_scan64(double x) {  // inclusive
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 1; i < 64; i *= 2) {
+    const double o = __shfl_up(x, i);
+    if (lane >= i) x += o;
   }
-  const int t = m - 1;
-  bool ok = sums(target(t), zm, z);
-  const bool fell = m < T_n;
-  if (fell && p.draft) ok &= sums(drafter(t), dm, dz);
-  const int w = fell ? p.tokens[(long)n * p.t_max + t + 1] : -1;
-  if (!ok) {
+  return x;
+}
+__device__ __forceinline__ float nan_max(float a, float b) {
+  return __builtin_elementwise_maximum(a, b);
+}
+__device__ __forceinline__ float wave_nan_max(float x) {
+  x = nan_max(x, gdn::dpp<0xB1>(x));
+  x = nan_max(x, gdn::dpp<0x4E>(x));
+  x = nan_max(x, gdn::dpp<0x141>(x));
+  x = nan_max(x, gdn::dpp<0x140>(x));
+  const int u = __float_as_int(x);
+  return nan_max(nan_max(__int_as_float(__builtin_amdgcn_readlane(u, 0)),
+                         __int_as_float(__builtin_amdgcn_readlane(u, 16))),
+                 nan_max(__int_as_float(__builtin_amdgcn_readlane(u, 32)),
+                         __int_as_float(__builtin_amdgcn_readlane(u, 48))));
+}
+
+// Inverse temperature of a lane times log2 e; 0: out of range.
+__device__ __forceinline__ double exponent_of(const DraftArgs& p, int n) {
+  const float it = p.it[n];
+  return it >= 1e-30f && it <= 1e30f ? (double)it * 1.44269504088896340736 : 0.0;
+}
+template <typename T>
+__device__ __forceinline__ const T* target_row(const DraftArgs& p, int n, int t) {
+  return (const T*)p.logits + ((long)n * p.t_max + t) * p.stride;
+}
+template <typename T>
+__device__ __forceinline__ const T* drafter_row(const DraftArgs& p, int n, int t) {
+  return (const T*)p.draft + ((long)n * (p.t_max - 1) + t) * p.draft_stride;
+}
+// Logits of the row before its first 16-byte line starts (slices start there).
+template <typename T>
+__device__ __forceinline__ int skew_of(const T* x) {
+  return (int)((uintptr_t)x % 16 / sizeof(T));
+}
+
+// One workgroup per slice of a row: 16 V bytes a thread, read once into
+// registers.
+template <typename T, int V>
+__global__ __launch_bounds__(kThreads, 4) void sum_kernel(DraftArgs p,
+                                                          gdn::LaneTable tl) {
+  constexpr int E = 16 / sizeof(T);  // logits per vector
+  __shared__ float tops[4];
+  __shared__ double sums[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int row = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
+  const int targets = p.lanes * p.t_max;
+  const bool drafter = row >= targets;
+  const int per = drafter ? p.t_max - 1 : p.t_max;
+  const int n = (drafter ? row - targets : row) / per;
+  const int t = (drafter ? row - targets : row) % per;
+  if (t >= tl.v[n] - (drafter ? 1 : 0)) return;
+  const T* x = drafter ? drafter_row<T>(p, n, t) : target_row<T>(p, n, t);
+  const int skew = skew_of(x);
+  const u32x4* line = reinterpret_cast<const u32x4*>(x - skew);
+  const int lines = (p.vocab + skew + E - 1) / E;
+  const int first = slice * kThreads * V + tid;
+
+  u32x4 raw[V];
+#pragma unroll
+  for (int c = 0; c < V; ++c) {
+    const int i = first + c * kThreads;
+    raw[c] = line[i < lines ? i : lines - 1];
+  }
+  // (only a row's draft without the drafter's distribution is left out)
+  const int gone = !drafter && !p.draft && t + 1 < tl.v[n]
+                       ? p.tokens[(long)n * p.t_max + t + 1]
+                       : -1;
+  const double c = exponent_of(p, n);
+  float val[V][E];
+  float m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int i = first + k * kThreads;
+    const int id = i < lines ? i * E - skew : p.vocab;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if constexpr (sizeof(T) == 4) val[k][e] = __uint_as_float(raw[k][e]);
+      else
+        val[k][e] = __uint_as_float(e & 1 ? raw[k][e / 2] & 0xffff0000u
+                                          : raw[k][e / 2] << 16);
+    }
+    if (id < 0 || id > p.vocab - E) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if ((unsigned)(id + e) >= (unsigned)p.vocab) val[k][e] = -INFINITY;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) m = nan_max(m, val[k][e]);
+  }
+  m = wave_nan_max(m);
+  if (lane == 0) tops[wave] = m;
+  __syncthreads();
+  m = nan_max(nan_max(tops[0], tops[1]), nan_max(tops[2], tops[3]));
+  const double ref = m == -INFINITY ? 0.0 : (double)m;
+  // the draft is taken out of the sum and added to a second one
+  double own = 0.0;
+  const int from = slice * kThreads * V * E - skew;
+  const bool here = gone >= from && gone < from + kThreads * V * E && gone < p.vocab && gone >= 0;
+  if (here) {
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if ((first + k * kThreads) * E - skew + e == gone) val[k][e] = -INFINITY;
+    own = weight_of(logit_at(x, gone), ref, c);
+  }
+  double z[2] = {0.0, 0.0};
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+#pragma unroll
+    for (int e = 0; e < E; ++e) z[e & 1] += weight_in_sum(val[k][e], ref, c);
+  const double sum = wave_sum64(z[0] + z[1]);
+  if (lane == 0) sums[wave] = sum;
+  __syncthreads();
+  if (tid != 0) return;
+  const double zx = or_nothing((sums[0] + sums[1]) + (sums[2] + sums[3]));
+  p.parts[(long)row * p.slices + slice] = {zx + own, zx, m, 0};
+}
+
+// A workgroup of kWide threads works a lane's verdict out from the slices'
+// sums, a wave a row.
+struct Rows {
+  float m[2][GDN_MAX_T];
+  double z[2][GDN_MAX_T];
+  int accepted;
+};
+template <typename T>
+__device__ __forceinline__ Verdict decide(const DraftArgs& p, int n, int T_n,
+                                          double c, Rows& rows, bool write) {
+  const int lane = threadIdx.x & 63, wave = gdn::uniform(threadIdx.x >> 6);
+  // the first wave's lanes hold a draft each: its logits are on their way
+  // while the rows are summed up
+  const bool drafted = wave == 0 && lane < T_n - 1;
+  bool inside = false;
+  float pw = 0.f, qw = 0.f, u = 0.f;
+  if (drafted) {
+    const int w = p.tokens[(long)n * p.t_max + lane + 1];
+    u = p.uniforms[(long)n * p.t_max + lane];
+    inside = (unsigned)w < (unsigned)p.vocab;
+    const int i = inside ? w : 0;
+    pw = logit_at(target_row<T>(p, n, lane), i);
+    if (p.draft) qw = logit_at(drafter_row<T>(p, n, lane), i);
+  }
+  const int count = T_n + (p.draft ? T_n - 1 : 0);
+  auto parts_of = [&](int r) {
+    const long row = r < T_n ? (long)n * p.t_max + r
+                             : (long)p.lanes * p.t_max +
+                                   (long)n * (p.t_max - 1) + (r - T_n);
+    return p.parts + row * p.slices;
+  };
+  constexpr int kStep = kWide / 64;
+  const Part none = {0.0, 0.0, -INFINITY, 0};
+  Part next = none;
+  if (wave < count && lane < p.slices) next = parts_of(wave)[lane];
+  for (int r = wave; r < count; r += kStep) {
+    const Part* parts = parts_of(r);
+    const Part first = next;
+    next = none;
+    if (r + kStep < count && lane < p.slices) next = parts_of(r + kStep)[lane];
+    float m = first.m;
+    for (int i = lane + 64; i < p.slices; i += 64) m = nan_max(m, parts[i].m);
+    m = wave_nan_max(m);
+    const double ref = m == -INFINITY ? 0.0 : (double)m;
+    double z = first.z * weight_of(first.m, ref, c);
+    for (int i = lane + 64; i < p.slices; i += 64)
+      z += parts[i].z * weight_of(parts[i].m, ref, c);
+    z = wave_sum64(z);
+    if (lane == 0) {
+      const int d = r >= T_n;
+      rows.m[d][d ? r - T_n : r] = m;
+      rows.z[d][d ? r - T_n : r] = z;
+    }
+  }
+  __syncthreads();
+  if (wave == 0) {
+    bool stands = true;  // (lanes past the drafts)
+    if (drafted) {
+      const float m = rows.m[0][lane];
+      bool ok = c > 0.0 && fabsf(m) < INFINITY;
+      if (p.draft) ok = ok && fabsf(rows.m[1][lane]) < INFINITY;
+      double a = 0.0, b = 1.0;  // chances of the draft
+      if (ok && inside) {
+        a = weight_of(pw, m, c) / rows.z[0][lane];
+        if (p.draft) b = weight_of(qw, rows.m[1][lane], c) / rows.z[1][lane];
+      }
+      stands = ok && (double)u * b < a;
+      if (write && p.accept)
+        p.accept[(long)n * p.t_max + lane] =
+            !ok ? NAN : a == 0.0 ? 0.f : a >= b ? 1.f : (float)(a / b);
+    }
+    const uint64_t fell = __ballot(!stands);
+    if (lane == 0) rows.accepted = fell ? __builtin_ctzll(fell) + 1 : T_n;
+  }
+  __syncthreads();
+  Verdict v;
+  v.m = rows.accepted;
+  const int t = v.m - 1;
+  v.top = rows.m[0][t];
+  v.z = rows.z[0][t];
+  v.ok = c > 0.0 && fabsf(rows.m[0][t]) < INFINITY;
+  v.draft_top = v.draft_z = 1.0;
+  if (p.draft && v.m < T_n) {
+    v.draft_top = rows.m[1][t];
+    v.draft_z = rows.z[1][t];
+    v.ok = v.ok && fabsf(rows.m[1][t]) < INFINITY;
+  }
+  return v;
+}
+
+// Weights of row m - 1 that the next token is taken by, apart from a common
+// factor.
+template <typename T>
+struct Weights {
+  const T *x, *y;  // the row and the drafter's, or NULL
+  double top, draft_top, f, draft_f, c;
+  int gone;        // an id of weight 0, or -1
+  __device__ __forceinline__ double at(int i) const {
+    double w = weight_of(logit_at(x, i), top, c) * f;
+    if (y) {
+      w -= weight_of(logit_at(y, i), draft_top, c) * draft_f;
+      w = w > 0.0 ? w : 0.0;
+    }
+    return i == gone ? 0.0 : w;
+  }
+};
+template <typename T>
+__device__ __forceinline__ Weights<T> weights_of(const DraftArgs& p,
+                                                 const Verdict& v, int n,
+                                                 int T_n, double c, bool rest) {
+  const int t = v.m - 1;
+  Weights<T> w = {target_row<T>(p, n, t), nullptr, v.top, v.draft_top,
+                  1.0 / v.z, 1.0 / v.draft_z, c, -1};
+  if (rest && p.draft) w.y = drafter_row<T>(p, n, t);
+  if (rest && !p.draft) w.gone = p.tokens[(long)n * p.t_max + t + 1];
+  return w;
+}
+
+// With a drafter's distribution: the verdicts, and sums of max(p - q, 0) by
+// slices of the row where a draft fell.
+template <typename T>
+__global__ __launch_bounds__(kWide) void rest_kernel(DraftArgs p,
+                                                     gdn::LaneTable tl) {
+  __shared__ Rows rows;
+  __shared__ double sums[kWide / 64];
+  const int n = blockIdx.x / p.rest_slices, slice = blockIdx.x % p.rest_slices;
+  const int T_n = tl.v[n], tid = threadIdx.x;
+  if (T_n < 2) return;
+  const double c = exponent_of(p, n);
+  const Verdict v = decide<T>(p, n, T_n, c, rows, slice == 0);
+  if (slice == 0 && tid == 0) p.verdicts[n] = v;
+  if (!v.ok || v.m == T_n) return;
+  const Weights<T> w = weights_of<T>(p, v, n, T_n, c, true);
+  double sum = 0.0;
+#pragma unroll
+  for (int k = 0; k < kRestSlice / kWide; ++k) {
+    const int i = slice * kRestSlice + k * kWide + tid;
+    if (i < p.vocab) sum += w.at(i);
+  }
+  sum = wave_sum64(sum);
+  if (tid % 64 == 0) sums[tid / 64] = sum;
+  __syncthreads();
+  if (tid != 0) return;
+  for (int i = 1; i < kWide / 64; ++i) sum += sums[i];
+  p.rest[(long)n * p.rest_slices + slice] = sum;
+}
+
+// The next token (and the verdict, where it is not there yet), a workgroup per
+// lane: the slice that the border lies in, then the id within it.
+template <typename T>
+__global__ __launch_bounds__(kWide) void pick_kernel(DraftArgs p,
+                                                     gdn::LaneTable tl,
+                                                     int slice_ids) {
+  __shared__ Rows rows;
+  __shared__ double sums[kWide / 64];
+  __shared__ double found[2];  // the running sum before the slice, and the border
+  __shared__ int which, first_id[kWide / 64], last_id[kWide / 64];
+  const int n = blockIdx.x, T_n = tl.v[n];
+  const int tid = threadIdx.x, lane = tid & 63, wave = gdn::uniform(tid >> 6);
+  if (T_n == 0) return;
+  const double c = exponent_of(p, n);
+  const Verdict v = p.draft && T_n > 1 ? p.verdicts[n]
+                                       : decide<T>(p, n, T_n, c, rows, true);
+  if (!v.ok) {
     if (tid == 0) {
-      p.m[n] = m;
+      p.m[n] = v.m;
       p.next[n] = -1;
     }
     return;
   }
-  bool rest = fell;
-  auto weight = [&](int i) {
-    double x = chance(target(t), i, zm) / z;
-    if (rest) {
-      if (!p.draft) x = i == w ? 0 : x;
-      else x = fmax(x - chance(drafter(t), i, dm) / dz, 0.0);
+  bool rest = v.m < T_n;
+  const int t = v.m - 1;
+  const Part* parts = p.parts + ((long)n * p.t_max + t) * p.slices;
+  const float u = p.uniforms[(long)n * p.t_max + T_n - 1];
+  if (wave == 0) {
+    const double share = u > 0.f ? u < 1.f ? (double)u : 1.0 : 0.0;
+    auto slice_sum = [&](int i, int count) {
+      if (i >= count) return 0.0;
+      if (rest && p.draft) return p.rest[(long)n * p.rest_slices + i];
+      return or_nothing((rest ? parts[i].zx : parts[i].z) *
+                        weight_of(parts[i].m, v.top, c)) / v.z;
+    };
+    for (;;) {
+      const int count = rest && p.draft ? p.rest_slices : p.slices;
+      double whole = 0.0;
+      for (int i0 = 0; i0 < count; i0 += 64)
+        whole += lane_value(wave_scan64(slice_sum(i0 + lane, count)), 63);
+      if (whole == 0.0 && rest) {  // nothing is left: from p
+        rest = false;
+        continue;
+      }
+      const double border = share * whole;
+      double before = 0.0, base = 0.0;
+      int got = -1, last = 0;
+      double last_base = 0.0;
+      for (int i0 = 0; i0 < count && got < 0; i0 += 64) {
+        const double x = slice_sum(i0 + lane, count);
+        const double upto = wave_scan64(x);
+        const uint64_t hit = __ballot(before + upto > border && x > 0.0);
+        const uint64_t some = __ballot(x > 0.0);
+        if (hit) {
+          const int l = __builtin_ctzll(hit);
+          got = i0 + l;
+          base = before + (l > 0 ? lane_value(upto, l - 1) : 0.0);
+        }
+        if (some) {
+          const int l = 63 - __builtin_clzll(some);
+          last = i0 + l;
+          last_base = before + (l > 0 ? lane_value(upto, l - 1) : 0.0);
+        }
+        before += lane_value(upto, 63);
+      }
+      if (lane == 0) {
+        which = (got >= 0 ? got : last) << 1 | (rest ? 1 : 0);
+        found[0] = got >= 0 ? base : last_base;
+        found[1] = border;
+      }
+      break;
     }
-    return x;
-  };
-  // threads sum consecutive ids
-  const int per = (V + kBlock - 1) / kBlock;
-  const int i0 = tid * per < V ? tid * per : V, i1 = i0 + per < V ? i0 + per : V;
-  double mine = 0, all = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    mine = 0;
-    for (int i = i0; i < i1; ++i) mine += weight(i);
-    all = block_sum(mine, red);
-    if (all > 0 || !rest) break;
-    rest = false;
   }
   __syncthreads();
-  red[tid] = mine;
+  rest = which & 1;
+  const int slice = which >> 1;
+  const Weights<T> w = weights_of<T>(p, v, n, T_n, c, rest);
+  // ids of the slice, consecutive ones a thread
+  const bool by_rest = rest && p.draft;
+  const int ids = by_rest ? kRestSlice : slice_ids;
+  const int skew = by_rest ? 0 : skew_of(w.x);
+  const int per = (ids + kWide - 1) / kWide;
+  const int from = slice * ids - skew + tid * per;
+  double mine = 0.0;
+  double x[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int i = from + k;
+    x[k] = k < per && (unsigned)i < (unsigned)p.vocab ? w.at(i) : 0.0;
+    mine += x[k];
+  }
+  const double upto = wave_scan64(mine);
+  if (lane == 63) sums[wave] = upto;
+  __syncthreads();
+  double run = found[0];
+  for (int i = 0; i < wave; ++i) run += sums[i];
+  const double below = __shfl_up(upto, 1);
+  double at = lane > 0 ? run + below : run;
+  int first = -1, last = -1;  // past the border; of any weight
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    at += x[k];
+    if (x[k] > 0.0) {
+      if (at > found[1] && first < 0) first = from + k;
+      last = from + k;
+    }
+  }
+  const uint64_t hit = __ballot(first >= 0), some = __ballot(last >= 0);
+  // (the ids of a wave follow one another)
+  const int by_first = hit ? __shfl(first, __builtin_ctzll(hit)) : -1;
+  const int by_last = some ? __shfl(last, 63 - __builtin_clzll(some)) : -1;
+  if (lane == 0) {
+    first_id[wave] = by_first;
+    last_id[wave] = by_last;
+  }
   __syncthreads();
   if (tid != 0) return;
-  const float u = fminf(fmaxf(p.uniforms[(long)n * p.t_max + T_n - 1], 0.f), 1.f);
-  const double border = u * all;
-  double before = 0;
-  int s = 0, last = 0;
-  for (int i = 0; i < kBlock; ++i)
-    if (red[i] > 0) last = i;
-  for (; s < last && before + red[s] <= border; ++s) before += red[s];
-  int got = 0;
-  for (int i = s * per; i < V && i < (s + 1) * per; ++i) {
-    const double x = weight(i);
-    if (x > 0) got = i;
-    before += x;
-    if (x > 0 && before > border) break;
-  }
-  p.m[n] = m;
-  p.next[n] = got;
+  int token = -1;
+  for (int i = 0; i < kWide / 64 && token < 0; ++i) token = first_id[i];
+  for (int i = kWide / 64 - 1; i >= 0 && token < 0; --i) token = last_id[i];
+  p.m[n] = v.m;
+  p.next[n] = token;
+}
+
+// ---------------------------------------------------------------- host side
+static bool sizes_ok(int32_t n_lanes, int32_t t_max, int32_t vocab) {
+  return n_lanes >= 1 && n_lanes <= GDN_MAX_LANES && t_max >= 1 &&
+         t_max <= GDN_MAX_T && vocab >= 1 && vocab <= 1 << 30;
+}
+// Vectors per thread of a slice: 32 logits a thread, or 8 when that would
+// leave most of the CUs without a slice.
+static int vectors_for(int32_t n_lanes, int32_t t_max, int32_t vocab, int size) {
+  return gdnt::vectors_for(n_lanes * t_max, vocab, size);
+}
+static int rest_slices_for(int32_t vocab) {
+  return (vocab + kRestSlice - 1) / kRestSlice;
+}
+static size_t bytes_for(int32_t n_lanes, int32_t t_max, int32_t vocab,
+                        int slices) {
+  return round16((size_t)n_lanes * (2 * t_max - 1) * slices * sizeof(Part)) +
+         round16((size_t)n_lanes * rest_slices_for(vocab) * sizeof(double)) +
+         round16((size_t)n_lanes * sizeof(Verdict));
+}
+
+template <typename T>
+static hipError_t run(const DraftArgs& p, const gdn::LaneTable& tl, int v,
+                      hipStream_t st) {
+  constexpr int kMany = 32 * sizeof(T) / 16, kFew = 8 * sizeof(T) / 16;
+  const int rows = p.lanes * (p.draft ? 2 * p.t_max - 1 : p.t_max);
+  const dim3 grid((unsigned)((long)rows * p.slices));
+  hipError_t e = v == kMany
+                     ? launch(sum_kernel<T, kMany>, grid, dim3(kThreads), st, p, tl)
+                     : launch(sum_kernel<T, kFew>, grid, dim3(kThreads), st, p, tl);
+  if (e == hipSuccess && p.draft)
+    e = launch(rest_kernel<T>, dim3((unsigned)(p.lanes * p.rest_slices)),
+               dim3(kWide), st, p, tl);
+  if (e != hipSuccess) return e;
+  return launch(pick_kernel<T>, dim3((unsigned)p.lanes), dim3(kWide), st, p, tl,
+                kThreads * v * (int)(16 / sizeof(T)));
 }
 
 }  // namespace gdnv
@@ -162,7 +571,17 @@ __global__ __launch_bounds__(kBlock) void verify_kernel(DraftArgs p,
 extern "C" size_t gdn_draft_verify_workspace_bytes(int32_t n_lanes,
                                                    int32_t t_max,
                                                    int32_t vocab) {
-  return 0;
+  using namespace gdnv;
+  if (!sizes_ok(n_lanes, t_max, vocab)) return 0;
+  // the larger of the two types' needs
+  size_t need = 0;
+  for (int size = 2; size <= 4; size += 2) {
+    const int v = vectors_for(n_lanes, t_max, vocab, size);
+    const size_t n = bytes_for(n_lanes, t_max, vocab,
+                               gdnt::slices_for(vocab, size, v, false));
+    if (n > need) need = n;
+  }
+  return need;
 }
 
 extern "C" int gdn_draft_verify(int32_t n_lanes, int32_t t_max,
@@ -177,8 +596,7 @@ extern "C" int gdn_draft_verify(int32_t n_lanes, int32_t t_max,
                                 void* stream) {
   using namespace gdnv;
   const int64_t most = (int64_t)1 << 40;
-  if (n_lanes < 1 || n_lanes > GDN_MAX_LANES || t_max < 1 ||
-      t_max > GDN_MAX_T || vocab < 1 || vocab > 1 << 30 || row_stride < vocab ||
+  if (!sizes_ok(n_lanes, t_max, vocab) || row_stride < vocab ||
       row_stride > most || (draft_logits && (draft_stride < vocab || draft_stride > most)))
     return fail(GDN_EINVAL, "gdn_draft_verify: sizes out of range");
   if (in_dtype != GDN_BF16 && in_dtype != GDN_F32)
@@ -208,11 +626,25 @@ extern "C" int gdn_draft_verify(int32_t n_lanes, int32_t t_max,
   if (!any) return GDN_OK;
   DraftArgs p = {logits, t_max > 1 ? draft_logits : nullptr, tokens, uniforms,
                  inv_temperature, m_lane, next_token, accept, row_stride,
-                 draft_stride, n_lanes, t_max, vocab};
-  const dim3 grid((unsigned)n_lanes), block(kBlock);
-  const hipError_t e =
-      in_dtype == GDN_BF16
-          ? launch(verify_kernel<uint16_t>, grid, block, (hipStream_t)stream, p, tl)
-          : launch(verify_kernel<float>, grid, block, (hipStream_t)stream, p, tl);
+                 draft_stride, n_lanes, t_max, vocab, 0, rest_slices_for(vocab),
+                 nullptr, nullptr, nullptr};
+  const int v = vectors_for(n_lanes, t_max, vocab, size);
+  const auto in_lines = [&](const void* x, int64_t stride) {
+    return !misaligned(x, 16) && stride * size % 16 == 0;
+  };
+  p.slices = gdnt::slices_for(
+      vocab, size, v,
+      in_lines(logits, row_stride) &&
+          (!p.draft || in_lines(p.draft, draft_stride)));
+  if ((double)n_lanes * (2 * t_max - 1) * p.slices > (double)INT_MAX)
+    return fail(GDN_EINVAL, "gdn_draft_verify: grid too large");
+  p.parts = (Part*)workspace;
+  p.rest = (double*)((char*)workspace +
+                     round16((size_t)n_lanes * (2 * t_max - 1) * p.slices * sizeof(Part)));
+  p.verdicts = (Verdict*)((char*)p.rest + round16((size_t)n_lanes * p.rest_slices *
+                                                  sizeof(double)));
+  const hipError_t e = in_dtype == GDN_BF16
+                           ? run<uint16_t>(p, tl, v, (hipStream_t)stream)
+                           : run<float>(p, tl, v, (hipStream_t)stream);
   return gdn::hip_status(e, "gdn_draft_verify launch");
 }
