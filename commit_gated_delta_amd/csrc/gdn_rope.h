@@ -90,43 +90,6 @@ __device__ __forceinline__ void store_eight(float* p, const Eight& r) {
   *reinterpret_cast<f32x4*>(p) = f32x4{r.x[0], r.x[1], r.x[2], r.x[3]};
   *reinterpret_cast<f32x4*>(p + 4) = f32x4{r.x[4], r.x[5], r.x[6], r.x[7]};
 }
-template <typename T>
-__device__ __forceinline__ void copy_eight(T* to, const T* from) {
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-    reinterpret_cast<u32x4*>(to)[i] = reinterpret_cast<const u32x4*>(from)[i];
-}
-
-// Channels 8 u .. 8 u + 7 of a row after the rotation at position pos.
-template <typename T>
-__device__ __forceinline__ Eight turned(const RopeArgs& p, const T* row, int u,
-                                        int pos) {
-  Eight x = load_eight(row + 8 * u);
-  if (8 * u >= p.rot) return x;
-  if (p.pairs) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float c, s;
-      turn(pos, p.inv_freq[4 * u + i], c, s);
-      const float a = x.x[2 * i], b = x.x[2 * i + 1];
-      x.x[2 * i] = a * c - b * s;
-      x.x[2 * i + 1] = b * c + a * s;
-    }
-    return x;
-  }
-  const int hp = p.rot / 16;  // pieces of half the rotated channels
-  const bool second = u >= hp;
-  const Eight y = load_eight(row + 8 * (second ? u - hp : u + hp));
-  const float* f = p.inv_freq + 8 * (second ? u - hp : u);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float c, s;
-    turn(pos, f[i], c, s);
-    x.x[i] = x.x[i] * c + y.x[i] * (second ? s : -s);
-  }
-  return x;
-}
-
 // Position of token t of lane n in the cache (-1: none) and for the rotation.
 __device__ __forceinline__ int slot_of(const KvArgs& a, int n, int t, int T) {
   const long pos = (long)a.kv_len[n] - T + t;
@@ -137,63 +100,234 @@ __device__ __forceinline__ int turn_of(const RopeArgs& p, int n, int t, int T) {
                      : (int)((unsigned)p.kv.kv_len[n] - T + t);
 }
 
-// One thread per eight channels of a row of q, k or v.
-template <typename T, bool FP4>
-__global__ __launch_bounds__(256) void rope_kernel(RopeArgs p,
-                                                   gdn::LaneTable tl, int d) {
+// Cosines and sines of N pairs from inverse frequency f on.
+template <int N>
+struct Turns {
+  float c[N], s[N];
+  __device__ __forceinline__ void set(int pos, const float* f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) turn(pos, f[i], c[i], s[i]);
+  }
+};
+
+// How a launch is shared out: blocks of threads that turn rows (a thread takes
+// the same channels of every `slots`-th head, so that it works out its angles
+// once), then blocks that copy, then blocks that write 4-bit rows.
+struct RopePlan {
+  int units, slots, heads, blocks;  // turning: units and heads of a token
+  int pieces, copy_blocks;          // copying: 16-byte pieces of a token
+  int slots4;                       // 4-bit rows: as slots
+};
+constexpr int kAhead = 4;  // heads that a thread has on their way at once
+
+struct Token {
+  int n, t, T;
+  long nt;
+};
+__device__ __forceinline__ bool token_of(const KvArgs& a,
+                                         const gdn::LaneTable& tl, int nt,
+                                         Token& k) {
+  if (nt >= a.lanes * a.t_max) return false;
+  k.nt = nt;
+  k.n = nt / a.t_max;
+  k.t = nt - k.n * a.t_max;
+  k.T = tl.v[k.n];
+  return k.t < k.T;
+}
+// The token's page (-1: none) and its place in it; row h of the cache's heads
+// is then that of (page h_kv + h) page_size + place.
+__device__ __forceinline__ int page_for(const KvArgs& a, const Token& k,
+                                        int& place) {
+  place = 0;
+  const int pos = slot_of(a, k.n, k.t, k.T);
+  if (pos < 0) return -1;
+  const int nth = page_of(a, pos);
+  place = pos - nth * a.page;
+  const int page = a.table[(long)k.n * a.max_pages + nth];
+  return (unsigned)page < (unsigned)a.n_pages ? page : -1;
+}
+
+// Rows that are turned: queries, and keys unless they go into 4 bits.  A unit
+// is eight pairs, or of neighbouring channels four.
+template <typename T, bool FP4, bool PAIRS>
+__device__ __forceinline__ void turn_rows(const RopeArgs& p,
+                                          const gdn::LaneTable& tl, int d,
+                                          const RopePlan& g, int i) {
   const KvArgs& a = p.kv;
-  const int units = d / 8, heads = (p.q ? a.h_q : 0) + 2 * a.h_kv;
-  const long i = (long)blockIdx.x * 256 + threadIdx.x;
-  const int u = (int)(i % units);
-  const long row = i / units, nt = row / heads;
-  int h = (int)(row % heads);
-  if (nt >= (long)a.lanes * a.t_max) return;
-  const int n = (int)(nt / a.t_max), t = (int)(nt % a.t_max);
-  const int T_n = tl.v[n];
-  if (t >= T_n) return;
-  const int pos = turn_of(p, n, t, T_n);
-  if (p.q && h < a.h_q) {
-    const T* src = (const T*)p.q + nt * p.qs + (long)h * d;
-    T* dst = (T*)p.q_out + (nt * a.h_q + h) * d;
-    // a thread turns both halves of its pairs, so that q_out may be q
-    const int hp = p.pairs ? 0 : p.rot / 16;
-    if (8 * u >= p.rot) {
-      copy_eight(dst + 8 * u, src + 8 * u);
-    } else if (p.pairs) {
-      store_eight(dst + 8 * u, turned(p, src, u, pos));
-    } else if (u < hp) {
-      const Eight x = turned(p, src, u, pos), y = turned(p, src, u + hp, pos);
-      store_eight(dst + 8 * u, x);
-      store_eight(dst + 8 * (u + hp), y);
+  constexpr int kN = PAIRS ? 4 : 8, kParts = PAIRS ? 1 : 2;
+  const int row = i / g.units, u = i - row * g.units;
+  const int nt = row / g.slots, slot = row - nt * g.slots;
+  Token k;
+  if (!token_of(a, tl, nt, k)) return;
+  const int queries = p.q ? a.h_q : 0;
+  const int c0 = 8 * u, c1 = 8 * u + p.rot / 2;  // channels
+  const T* q = (const T*)p.q + k.nt * p.qs;
+  const T* kk = (const T*)p.k + k.nt * p.ks;
+  auto source = [&](int h) {
+    return h < queries ? q + (long)h * d : kk + (long)(h - queries) * d;
+  };
+  Turns<kN> w;
+  w.set(turn_of(p, k.n, k.t, k.T), p.inv_freq + kN * u);
+  int place, page = -1;
+  if (!FP4) page = page_for(a, k, place);
+#pragma unroll 1
+  for (int h0 = slot; h0 < g.heads; h0 += kAhead * g.slots) {
+    Eight x[kAhead], y[kAhead];
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b) {
+      const int h = h0 + b * g.slots;
+      const T* src = source(h < g.heads ? h : h0);
+      x[b] = load_eight(src + c0);
+      if (!PAIRS) y[b] = load_eight(src + c1);
     }
-    return;
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b) {
+      const int h = h0 + b * g.slots;
+      if (h >= g.heads) break;
+      T* dst;
+      if (FP4 || h < queries) {
+        dst = (T*)p.q_out + (k.nt * a.h_q + h) * d;
+      } else {
+        if (page < 0) break;  // (keys come last)
+        dst = (T*)p.kc + (((long)page * a.h_kv + (h - queries)) * a.page + place) * d;
+      }
+#pragma unroll
+      for (int e = 0; e < kN; ++e) {
+        float& l = x[b].x[PAIRS ? 2 * e : e];
+        float& r = PAIRS ? x[b].x[(2 * e + 1) % 8] : y[b].x[e];
+        const float a0 = l, b0 = r;
+        l = a0 * w.c[e] - b0 * w.s[e];
+        r = b0 * w.c[e] + a0 * w.s[e];
+      }
+      store_eight(dst + c0, x[b]);
+      if (kParts == 2) store_eight(dst + c1, y[b]);
+    }
   }
-  if (p.q) h -= a.h_q;
-  const bool value = h >= a.h_kv;
-  if (value) h -= a.h_kv;
-  const T* src = value ? (const T*)p.v + nt * p.vs + (long)h * d
-                       : (const T*)p.k + nt * p.ks + (long)h * d;
-  const int slot = slot_of(a, n, t, T_n);
-  const long at = slot < 0 ? -1 : row_of(a, n, h, slot, 1);  // row of the cache
-  if constexpr (FP4) {
-    // (the four threads of a block of 32 channels are neighbours)
-    const Eight x = value ? load_eight(src + 8 * u) : turned(p, src, u, pos);
-    const Coded y = fp4_code(x.x);
-    const Fp4Rows& to = value ? p.v4 : p.k4;
-    if (at >= 0) {
-      *reinterpret_cast<uint32_t*>(to.codes + at * (d / 2) + 4 * u) = y.codes;
-      if (u % 4 == 0) to.scales[at * (d / 32) + u / 4] = y.scale;
-    }
-    uint16_t* held = value ? p.v_held : p.k_held;
-    if (held)
-      *reinterpret_cast<u32x4*>(held + (nt * a.h_kv + h) * d + 8 * u) =
-          fp4_values(y.codes, y.scale);
+}
+
+// Pieces that stay as they are: queries' and keys' channels from rot on, and
+// values (keys and values unless they go into 4 bits).
+template <typename T, bool FP4>
+__device__ __forceinline__ void copy_rows(const RopeArgs& p,
+                                          const gdn::LaneTable& tl, int d,
+                                          const RopePlan& g, int i) {
+  const KvArgs& a = p.kv;
+  constexpr int kPer = 16 / sizeof(T);
+  const int nt = i / g.pieces, at = i - nt * g.pieces;
+  Token k;
+  if (!token_of(a, tl, nt, k)) return;
+  const int tail = (d - p.rot) / kPer, whole = d / kPer;
+  const int of_q = p.q ? a.h_q * tail : 0, of_k = FP4 ? 0 : a.h_kv * tail;
+  const T* src;
+  T* dst;
+  if (at < of_q) {
+    const int h = at / tail, c = p.rot + (at - h * tail) * kPer;
+    src = (const T*)p.q + k.nt * p.qs + (long)h * d + c;
+    dst = (T*)p.q_out + (k.nt * a.h_q + h) * d + c;
   } else {
-    if (at < 0) return;
-    T* dst = (T*)(value ? p.vc : p.kc) + at * d + 8 * u;
-    if (value || 8 * u >= p.rot) copy_eight(dst, src + 8 * u);
-    else store_eight(dst, turned(p, src, u, pos));
+    const bool value = at >= of_q + of_k;
+    const int j = value ? at - of_q - of_k : at - of_q;
+    const int per = value ? whole : tail, h = j / per;
+    const int c = (value ? 0 : p.rot) + (j - h * per) * kPer;
+    int place;
+    const int page = page_for(a, k, place);
+    if (page < 0) return;
+    src = (value ? (const T*)p.v + k.nt * p.vs : (const T*)p.k + k.nt * p.ks) +
+          (long)h * d + c;
+    dst = (T*)(value ? p.vc : p.kc) +
+          (((long)page * a.h_kv + h) * a.page + place) * d + c;
   }
+  *reinterpret_cast<u32x4*>(dst) = *reinterpret_cast<const u32x4*>(src);
+}
+
+// Keys and values into 4 bits: eight neighbouring channels a thread, four
+// threads a block of 32.
+template <typename T, bool PAIRS>
+__device__ __forceinline__ void code_rows(const RopeArgs& p,
+                                          const gdn::LaneTable& tl, int d,
+                                          const RopePlan& g, int i) {
+  const KvArgs& a = p.kv;
+  const int units = d / 8, row = i / units, u = i - row * units;
+  const int nt = row / g.slots4, slot = row - nt * g.slots4;
+  Token k;
+  if (!token_of(a, tl, nt, k)) return;
+  const bool turns = 8 * u < p.rot;
+  // channels 8 u .. are turned with those half of rot away
+  const int hp = p.rot / 16;
+  const bool second = !PAIRS && u >= hp;
+  const int other = PAIRS || !turns ? u : second ? u - hp : u + hp;
+  Turns<8> w;
+  if (turns) {
+    const int pos = turn_of(p, k.n, k.t, k.T);
+    if constexpr (PAIRS) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) turn(pos, p.inv_freq[4 * u + e], w.c[e], w.s[e]);
+    } else {
+      w.set(pos, p.inv_freq + 8 * (second ? other : u));
+    }
+  }
+  int place;
+  const int page = page_for(a, k, place);
+  const T* ks = (const T*)p.k + k.nt * p.ks;
+  const T* vs = (const T*)p.v + k.nt * p.vs;
+  auto put = [&](const Fp4Rows& to, uint16_t* held, int h, const float (&x)[8]) {
+    const Coded y = fp4_code(x);
+    if (page >= 0) {
+      const long at = ((long)page * a.h_kv + h) * a.page + place;
+      *reinterpret_cast<uint32_t*>(to.codes + at * (d / 2) + 4 * u) = y.codes;
+      if (u % 4 == 0) to.scales[at * (d / 32) + u / 4] = (uint8_t)y.scale;
+    }
+    if (held)
+      *reinterpret_cast<u32x4*>(held + (k.nt * a.h_kv + h) * d + 8 * u) =
+          fp4_values(y.codes, y.scale);
+  };
+  constexpr int kTwo = 2;  // heads on their way
+#pragma unroll 1
+  for (int h0 = slot; h0 < a.h_kv; h0 += kTwo * g.slots4) {
+    Eight x[kTwo], y[kTwo], z[kTwo];
+#pragma unroll
+    for (int b = 0; b < kTwo; ++b) {
+      const int h = h0 + b * g.slots4 < a.h_kv ? h0 + b * g.slots4 : h0;
+      x[b] = load_eight(ks + (long)h * d + 8 * u);
+      if (!PAIRS) y[b] = load_eight(ks + (long)h * d + 8 * other);
+      z[b] = load_eight(vs + (long)h * d + 8 * u);
+    }
+#pragma unroll
+    for (int b = 0; b < kTwo; ++b) {
+      const int h = h0 + b * g.slots4;
+      if (h >= a.h_kv) break;
+      if (turns) {
+        if constexpr (PAIRS) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float l = x[b].x[2 * e], r = x[b].x[2 * e + 1];
+            x[b].x[2 * e] = l * w.c[e] - r * w.s[e];
+            x[b].x[2 * e + 1] = r * w.c[e] + l * w.s[e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            x[b].x[e] = x[b].x[e] * w.c[e] + y[b].x[e] * (second ? w.s[e] : -w.s[e]);
+        }
+      }
+      put(p.k4, p.k_held, h, x[b].x);
+      put(p.v4, p.v_held, h, z[b].x);
+    }
+  }
+}
+
+template <typename T, bool FP4, bool PAIRS>
+__global__ __launch_bounds__(256) void rope_kernel(RopeArgs p,
+                                                   gdn::LaneTable tl, int d,
+                                                   RopePlan g) {
+  int b = blockIdx.x;
+  if (b < g.blocks)
+    return turn_rows<T, FP4, PAIRS>(p, tl, d, g, b * 256 + threadIdx.x);
+  b -= g.blocks;
+  if (b < g.copy_blocks)
+    return copy_rows<T, FP4>(p, tl, d, g, b * 256 + threadIdx.x);
+  b -= g.copy_blocks;
+  if constexpr (FP4) code_rows<T, PAIRS>(p, tl, d, g, b * 256 + threadIdx.x);
 }
 
 // ---------------------------------------------------------------- host side
@@ -234,26 +368,56 @@ static int check_rope(const char* fn, const gdn_kv_dims* dims,
   return check_lanes(fn, d, t_lane, tl, any);
 }
 
+// Slots of heads for a token's `units` threads each: as many as bring the call
+// to about kEnough threads, the fewest heads a thread.
+constexpr long kEnough = 256 * 1024;
+static int slots_for(long tokens, int units, int heads) {
+  const long n = (kEnough + tokens * units - 1) / (tokens * units);
+  return n < heads ? (int)n : heads;
+}
+
+template <typename T, bool FP4>
+static hipError_t run_rope(const RopeArgs& p, const gdn::LaneTable& tl, int d,
+                           const RopePlan& g, dim3 grid, hipStream_t st) {
+  return p.pairs
+             ? launch(rope_kernel<T, FP4, true>, grid, dim3(256), st, p, tl, d, g)
+             : launch(rope_kernel<T, FP4, false>, grid, dim3(256), st, p, tl, d, g);
+}
+
 static int launch_rope(const char* fn, const gdn_kv_dims& d, RopeArgs& p,
                        const gdn::LaneTable& tl, int dtype, bool fp4,
                        void* stream) {
   char msg[128];
-  const long rows =
-      (long)d.n_lanes * d.t_max * ((p.q ? d.h_q : 0) + 2l * d.h_kv);
-  const long blocks = (rows * (d.d / 8) + 255) / 256;
-  if (blocks > INT_MAX) {
+  const int size = dtype == GDN_BF16 ? 2 : 4;
+  const long tokens = (long)d.n_lanes * d.t_max;
+  const int queries = p.q ? d.h_q : 0;
+  RopePlan g;
+  g.units = p.rot / (p.pairs ? 8 : 16);
+  g.heads = queries + (fp4 ? 0 : d.h_kv);
+  if (g.heads == 0) g.units = 0;
+  g.slots = g.units > 0 ? slots_for(tokens, g.units, g.heads) : 1;
+  const long pieces = ((queries + (fp4 ? 0l : d.h_kv)) * (d.d - p.rot) +
+                       (fp4 ? 0l : (long)d.h_kv * d.d)) * size / 16;
+  g.pieces = (int)pieces;
+  g.slots4 = slots_for(tokens, d.d / 8, d.h_kv);
+  const auto blocks = [](double n) { return (n + 255) / 256; };
+  const double turning = blocks((double)tokens * g.slots * g.units);
+  const double copying = blocks((double)tokens * pieces);
+  const double coding = fp4 ? blocks((double)tokens * g.slots4 * (d.d / 8)) : 0;
+  if ((turning + copying + coding) * 256 > (double)INT_MAX) {
     snprintf(msg, sizeof(msg), "%s: grid too large", fn);
     return fail(GDN_EINVAL, msg);
   }
-  const dim3 grid((unsigned)blocks), block(256);
+  g.blocks = (int)turning;
+  g.copy_blocks = (int)copying;
+  const dim3 grid((unsigned)(g.blocks + g.copy_blocks + (int)coding));
   const hipStream_t st = (hipStream_t)stream;
-  hipError_t e;
-  if (dtype == GDN_BF16)
-    e = fp4 ? launch(rope_kernel<uint16_t, true>, grid, block, st, p, tl, d.d)
-            : launch(rope_kernel<uint16_t, false>, grid, block, st, p, tl, d.d);
-  else
-    e = fp4 ? launch(rope_kernel<float, true>, grid, block, st, p, tl, d.d)
-            : launch(rope_kernel<float, false>, grid, block, st, p, tl, d.d);
+  const hipError_t e =
+      dtype == GDN_BF16
+          ? fp4 ? run_rope<uint16_t, true>(p, tl, d.d, g, grid, st)
+                : run_rope<uint16_t, false>(p, tl, d.d, g, grid, st)
+          : fp4 ? run_rope<float, true>(p, tl, d.d, g, grid, st)
+                : run_rope<float, false>(p, tl, d.d, g, grid, st);
   snprintf(msg, sizeof(msg), "%s launch", fn);
   return gdn::hip_status(e, msg);
 }
