@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # GDN_LIBRARY names another build of the same library (the CPU tests load
@@ -154,19 +155,19 @@ def _load_library():
                                          vp] * 5 + [sz, vp]
     lib.gdn_token_scores.restype = ctypes.c_int
     i64 = ctypes.c_int64
-    rows = [kp, ip, vp, i64, vp, i64, vp, i64, ctypes.c_int, vp, i32, vp, vp]
+    rows = [kp, vp, vp, i64, vp, i64, vp, i64, ctypes.c_int, vp, i32, vp, vp]
     lib.gdn_rope_append.argtypes = rows + [vp] * 4 + [ctypes.c_int, vp]
     lib.gdn_rope_append.restype = ctypes.c_int
     lib.gdn_rope_append_mxfp.argtypes = rows + [vp] * 8 + [ctypes.c_int, vp]
     lib.gdn_rope_append_mxfp.restype = ctypes.c_int
     lib.gdn_paged_attention_mxfp_workspace_bytes.argtypes = [kp]
     lib.gdn_paged_attention_mxfp_workspace_bytes.restype = sz
-    lib.gdn_paged_attention_mxfp.argtypes = [kp, ip, vp, ctypes.c_int] + [
+    lib.gdn_paged_attention_mxfp.argtypes = [kp, vp, vp, ctypes.c_int] + [
         vp] * 8 + [sz, f, vp]
     lib.gdn_paged_attention_mxfp.restype = ctypes.c_int
     lib.gdn_draft_verify_workspace_bytes.argtypes = [i32] * 3
     lib.gdn_draft_verify_workspace_bytes.restype = sz
-    lib.gdn_draft_verify.argtypes = [i32, i32, ip, i32, vp, i64, vp, i64,
+    lib.gdn_draft_verify.argtypes = [i32, i32, vp, i32, vp, i64, vp, i64,
                                      ctypes.c_int] + [vp] * 7 + [sz, vp]
     lib.gdn_draft_verify.restype = ctypes.c_int
     lib.gdn_strerror.argtypes = [ctypes.c_int]
@@ -608,6 +609,15 @@ def token_scores(logits, tokens, n_top, logprob, entropy, top_ids,
     _check(st, "gdn_token_scores")
 
 
+def _lane_ints(t_lane, n):
+    """The lanes' values as an int32 array (``buffer_info`` has its address;
+    made in a third of the time of a ctypes array)."""
+    a = array("i", t_lane)
+    if len(a) != n:
+        raise ValueError("expected %d per-lane values, got %d" % (n, len(a)))
+    return a
+
+
 def _rows(t, name, dtype, n, t_max, h, d, device):
     """Address and token stride of rows [n, t_max, h, d], each token's h rows
     contiguous and the tokens equally far apart (a part of a projection's
@@ -626,19 +636,19 @@ def _rows(t, name, dtype, n, t_max, h, d, device):
                               tuple(t.shape), t.stride(), t.device))
 
 
-def _rope_args(dims, t_lane, q, k, v, inv_freq, rot_dim, q_out, positions,
+def _rope_args(dims, lanes, q, k, v, inv_freq, rot_dim, q_out, positions,
                dev):
     """The arguments that both writers begin with."""
-    n, tm, d, kind = dims.n_lanes, dims.t_max, dims.d, k.dtype
-    lanes, code = _lanes(t_lane, n), _code(kind)
-    qp, qs = (None, 0) if q is None else _rows(q, "q", kind, n, tm, dims.h_q,
-                                               d, dev)
-    kp, ks = _rows(k, "k", kind, n, tm, dims.h_kv, d, dev)
-    vp, vs = _rows(v, "v", kind, n, tm, dims.h_kv, d, dev)
-    return (ctypes.byref(dims), lanes, qp, qs, kp, ks, vp, vs, code,
+    n, tm, hq, hk, d = dims.n_lanes, dims.t_max, dims.h_q, dims.h_kv, dims.d
+    kind = k.dtype
+    qp, qs = (None, 0) if q is None else _rows(q, "q", kind, n, tm, hq, d, dev)
+    kp, ks = _rows(k, "k", kind, n, tm, hk, d, dev)
+    vp, vs = _rows(v, "v", kind, n, tm, hk, d, dev)
+    return (ctypes.byref(dims), lanes.buffer_info()[0], qp, qs, kp, ks, vp, vs,
+            _code(kind),
             _optional(inv_freq, "inv_freq", _F32, rot_dim // 2, dev), rot_dim,
             _optional(positions, "positions", _I32, n * tm, dev),
-            _optional(q_out, "q_out", kind, n * tm * dims.h_q * d, dev))
+            _optional(q_out, "q_out", kind, n * tm * hq * d, dev))
 
 
 def rope_append(dims: KvDims, t_lane, q, k, v, inv_freq, rot_dim, q_out,
@@ -647,9 +657,10 @@ def rope_append(dims: KvDims, t_lane, q, k, v, inv_freq, rot_dim, q_out,
     """gdn_rope_append on torch tensors.  q, k, v may be views of one
     projection's output; interleaved=True sets GDN_FLAG_ROPE_PAIRS."""
     n, kind, dev = dims.n_lanes, k.dtype, torch.cuda.current_device()
+    lanes = _lane_ints(t_lane, n)
     nc = dims.n_pages * dims.page_size * dims.h_kv * dims.d
     st = lib.gdn_rope_append(
-        *_rope_args(dims, t_lane, q, k, v, inv_freq, rot_dim, q_out,
+        *_rope_args(dims, lanes, q, k, v, inv_freq, rot_dim, q_out,
                     positions, dev),
         _tensor(k_cache, "k_cache", kind, nc, dev),
         _tensor(v_cache, "v_cache", kind, nc, dev),
@@ -676,9 +687,10 @@ def rope_append_mxfp(dims: KvDims, t_lane, q, k, v, inv_freq, rot_dim, q_out,
                     interleaved=False, stream=None, raw_status=False):
     """gdn_rope_append_mxfp on torch tensors."""
     n, dev = dims.n_lanes, torch.cuda.current_device()
+    lanes = _lane_ints(t_lane, n)
     nr = n * dims.t_max * dims.h_kv * dims.d
     st = lib.gdn_rope_append_mxfp(
-        *_rope_args(dims, t_lane, q, k, v, inv_freq, rot_dim, q_out,
+        *_rope_args(dims, lanes, q, k, v, inv_freq, rot_dim, q_out,
                     positions, dev),
         *_fp4_cache(dims, k_codes, k_scales, v_codes, v_scales, dev),
         _tensor(page_table, "page_table", _I32, n * dims.max_pages, dev),
@@ -700,11 +712,11 @@ def paged_attention_mxfp(dims: KvDims, t_lane, q, k_codes, k_scales, v_codes,
                         stream=None, raw_status=False):
     """gdn_paged_attention_mxfp on torch tensors."""
     n, kind = dims.n_lanes, q.dtype
-    lanes, code, dev = _lanes(t_lane, n), _code(kind), torch.cuda.current_device()
+    lanes, code, dev = _lane_ints(t_lane, n), _code(kind), torch.cuda.current_device()
     nq = n * dims.t_max * dims.h_q * dims.d
     ws, ws_bytes = _workspace(workspace, dev)
     st = lib.gdn_paged_attention_mxfp(
-        ctypes.byref(dims), lanes, _tensor(q, "q", kind, nq, dev), code,
+        ctypes.byref(dims), lanes.buffer_info()[0], _tensor(q, "q", kind, nq, dev), code,
         *_fp4_cache(dims, k_codes, k_scales, v_codes, v_scales, dev),
         _tensor(page_table, "page_table", _I32, n * dims.max_pages, dev),
         _tensor(kv_len, "kv_len", _I32, n, dev),
@@ -743,13 +755,13 @@ def draft_verify(t_lane, logits, draft_logits, tokens, uniforms,
     draft_logits [n_lanes, t_max - 1, vocab] or None."""
     n, tm, vocab = logits.shape
     kind = logits.dtype
-    lanes, code, dev = _lanes(t_lane, n), _code(kind), torch.cuda.current_device()
+    lanes, code, dev = _lane_ints(t_lane, n), _code(kind), torch.cuda.current_device()
     lp, ls = _logit_rows(logits, "logits", kind, n, tm, vocab, dev)
     dp, ds = (None, 0) if draft_logits is None or tm == 1 else _logit_rows(
         draft_logits, "draft_logits", kind, n, tm - 1, vocab, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     st = lib.gdn_draft_verify(
-        n, tm, lanes, vocab, lp, ls, dp, ds, code,
+        n, tm, lanes.buffer_info()[0], vocab, lp, ls, dp, ds, code,
         _tensor(tokens, "tokens", _I32, n * tm, dev),
         _tensor(uniforms, "uniforms", _F32, n * tm, dev),
         _tensor(inv_temperature, "inv_temperature", _F32, n, dev),

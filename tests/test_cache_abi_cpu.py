@@ -149,6 +149,13 @@ def test_verify_refusals():
 
 # ------------------------------------------------------------------ binding
 def test_binding_refuses_rows_that_do_not_fit():
+    with pytest.raises(ValueError):
+        gdn._lane_ints([1, 2, 3], 2)
+    with pytest.raises(OverflowError):
+        gdn._lane_ints([1, 1 << 31], 2)
+    with pytest.raises(TypeError):
+        gdn._lane_ints([1, 0.5], 2)
+    assert list(gdn._lane_ints((3, -1), 2)) == [3, -1]
     rows = torch.zeros(2, 4, 6 * 64, dtype=torch.bfloat16)
     take = lambda t, dev=-1, **o: gdn._rows(t, "q", torch.bfloat16, *[o.get(a, b) for a, b in (
         ("n", 2), ("T", 4), ("h", 2), ("d", 64))], dev)
