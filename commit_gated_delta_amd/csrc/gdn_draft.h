@@ -32,6 +32,8 @@ using gdnt::logit_at;
 using gdnt::round16;
 using gdnt::u32x4;
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
 // What a slice of a row leaves behind: its largest logit (NaN if it holds
 // one), the sum of 2^((x - m) c) with that as m, and the same without the
 // row's draft.
@@ -59,37 +61,37 @@ struct DraftArgs {
   float* accept;
   long stride, draft_stride;
   int lanes, t_max, vocab;
-  int slices;        // of a row, in `parts`
-  int rest_slices;   // of a row, in `rest`
+  int slices;        // of a row, in `parts`, from its first 16-byte line on
+  int rest_slices;   // of a row, in `rest`, from its first id on
   Part* parts;       // [target rows, then drafter's rows][slices]
   double* rest;      // [lanes][rest_slices]: sums of max(p - q, 0)
   Verdict* verdicts;  // [lanes], of windows with drafts that have a distribution
 };
 
-constexpr int kThreads = 256;   // of sum_kernel
-constexpr int kWide = 1024;     // of the kernels behind it
-constexpr int kRestSlice = 8192;  // ids of a slice of rest_kernel
+constexpr int kSlice = 2048;   // ids of a slice
+constexpr int kThreads = 256;  // of sum_kernel
+constexpr int kWide = 1024;    // of the kernels behind it
+constexpr int kRestSlices = 2;  // of a workgroup of rest_kernel
 
-// 2^y for -1020 <= y <= 1, to 4e-16: a polynomial through the Chebyshev nodes
-// of [-1/2, 1/2] for the fraction (off by 3e-16), the whole part added to the
-// exponent.  (The library's exp takes twice the instructions.)
+// 2^y for -1020 <= y <= 1, to 2e-14: a polynomial through the Chebyshev nodes
+// of [-1/2, 1/2] for the fraction, the whole part added to the exponent.  (The
+// library's exp takes twice the instructions.)
 __device__ __forceinline__ double exp2_f64(double y) {
   constexpr double kWhole = 6755399441055744.0;  // 1.5 * 2^52: no fraction left
   const double t = y + kWhole, f = y - (t - kWhole);
-  double e = 7.07258594926922421e-09;
-  e = __builtin_fma(e, f, 1.02086902999583060e-07);
-  e = __builtin_fma(e, f, 1.32154425879216893e-06);
-  e = __builtin_fma(e, f, 1.52526572602008367e-05);
-  e = __builtin_fma(e, f, 1.54035304417360499e-04);
-  e = __builtin_fma(e, f, 1.33335582301649744e-03);
-  e = __builtin_fma(e, f, 9.61812910760688825e-03);
-  e = __builtin_fma(e, f, 5.55041086644477225e-02);
-  e = __builtin_fma(e, f, 2.40226506959100972e-01);
-  e = __builtin_fma(e, f, 6.93147180559949949e-01);
-  e = __builtin_fma(e, f, 1.0);
-  const uint64_t u = __builtin_bit_cast(uint64_t, e);
-  const uint32_t whole = (uint32_t)__builtin_bit_cast(uint64_t, t);
-  return __builtin_bit_cast(double, u + ((uint64_t)(whole << 20) << 32));
+  double e = 1.02059054137655955e-07;
+  e = __builtin_fma(e, f, 1.32596452448871106e-06);
+  e = __builtin_fma(e, f, 1.52526729248507372e-05);
+  e = __builtin_fma(e, f, 1.54034337512510097e-04);
+  e = __builtin_fma(e, f, 1.33335582007945925e-03);
+  e = __builtin_fma(e, f, 9.61812919393431262e-03);
+  e = __builtin_fma(e, f, 5.55041086646516704e-02);
+  e = __builtin_fma(e, f, 2.40226506956403407e-01);
+  e = __builtin_fma(e, f, 6.93147180559946174e-01);
+  e = __builtin_fma(e, f, 1.00000000000001354e+00);
+  u32x2 w = __builtin_bit_cast(u32x2, e);
+  w[1] += __builtin_bit_cast(u32x2, t)[0] << 20;
+  return __builtin_bit_cast(double, w);
 }
 // 2^((x - m) c), 0 below 2^-1000 (x = -inf among it).
 constexpr double kLeast = -1000.0;
@@ -102,8 +104,8 @@ __device__ __forceinline__ double weight_of(float x, double m, double c) {
 __device__ __forceinline__ double weight_in_sum(float x, double m, double c) {
   return exp2_f64(__builtin_fmax(((double)x - m) * c, kLeast));
 }
-// Sums of weights from which a slice counts: its largest one is then above
-// 2^-1000 with any slice's 2^14 ids and a share of a row's 2^30.
+// Sums of weights from which a slice counts: the largest of its 2^11 weights
+// is then above 2^-1000, and so not 0 where an id is looked up.
 constexpr double kNothing = 0x1p-950;
 __device__ __forceinline__ double or_nothing(double sum) {
   return sum >= kNothing ? sum : 0.0;
@@ -111,16 +113,18 @@ __device__ __forceinline__ double or_nothing(double sum) {
 
 template <int CTRL>
 __device__ __forceinline__ double dpp64(double x) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xf, 0xf, true);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, 0xf, 0xf, true);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+  u32x2 w = __builtin_bit_cast(u32x2, x);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    w[i] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[i], CTRL, 0xf, 0xf, true);
+  return __builtin_bit_cast(double, w);
 }
 __device__ __forceinline__ double lane_value(double x, int lane) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), lane);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+  u32x2 w = __builtin_bit_cast(u32x2, x);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    w[i] = (uint32_t)__builtin_amdgcn_readlane((int)w[i], lane);
+  return __builtin_bit_cast(double, w);
 }
 // Sum over the 64 lanes, the same in every lane, in a fixed order.
 __device__ __forceinline__ double wave_sum64(double x) {
@@ -174,16 +178,18 @@ __device__ __forceinline__ int skew_of(const T* x) {
   return (int)((uintptr_t)x % 16 / sizeof(T));
 }
 
-// One workgroup per slice of a row: 16 V bytes a thread, read once into
-// registers.
-template <typename T, int V>
+// One workgroup per G slices of a row, read once into registers.
+template <typename T, int G>
 __global__ __launch_bounds__(kThreads, 4) void sum_kernel(DraftArgs p,
-                                                          gdn::LaneTable tl) {
-  constexpr int E = 16 / sizeof(T);  // logits per vector
+                                                          gdn::LaneTable tl,
+                                                          int groups) {
+  constexpr int E = 16 / sizeof(T);              // logits per vector
+  constexpr int VS = kSlice / (kThreads * E);    // vectors of a slice
+  constexpr int V = G * VS;
   __shared__ float tops[4];
-  __shared__ double sums[4];
+  __shared__ double sums[G][kThreads];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int row = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
+  const int row = blockIdx.x / groups, part = blockIdx.x % groups;
   const int targets = p.lanes * p.t_max;
   const bool drafter = row >= targets;
   const int per = drafter ? p.t_max - 1 : p.t_max;
@@ -194,13 +200,13 @@ __global__ __launch_bounds__(kThreads, 4) void sum_kernel(DraftArgs p,
   const int skew = skew_of(x);
   const u32x4* line = reinterpret_cast<const u32x4*>(x - skew);
   const int lines = (p.vocab + skew + E - 1) / E;
-  const int first = slice * kThreads * V + tid;
+  const int first = part * kThreads * V + tid;
 
   u32x4 raw[V];
 #pragma unroll
-  for (int c = 0; c < V; ++c) {
-    const int i = first + c * kThreads;
-    raw[c] = line[i < lines ? i : lines - 1];
+  for (int k = 0; k < V; ++k) {
+    const int i = first + k * kThreads;
+    raw[k] = line[i < lines ? i : lines - 1];
   }
   // (only a row's draft without the drafter's distribution is left out)
   const int gone = !drafter && !p.draft && t + 1 < tl.v[n]
@@ -233,11 +239,10 @@ __global__ __launch_bounds__(kThreads, 4) void sum_kernel(DraftArgs p,
   __syncthreads();
   m = nan_max(nan_max(tops[0], tops[1]), nan_max(tops[2], tops[3]));
   const double ref = m == -INFINITY ? 0.0 : (double)m;
-  // the draft is taken out of the sum and added to a second one
+  // the draft is taken out of its slice's sum, and added for a second one
   double own = 0.0;
-  const int from = slice * kThreads * V * E - skew;
-  const bool here = gone >= from && gone < from + kThreads * V * E && gone < p.vocab && gone >= 0;
-  if (here) {
+  const int own_slice = gone < 0 || gone >= p.vocab ? -1 : (gone + skew) / kSlice;
+  if (own_slice >= part * G && own_slice < (part + 1) * G) {
 #pragma unroll
     for (int k = 0; k < V; ++k)
 #pragma unroll
@@ -245,17 +250,25 @@ __global__ __launch_bounds__(kThreads, 4) void sum_kernel(DraftArgs p,
         if ((first + k * kThreads) * E - skew + e == gone) val[k][e] = -INFINITY;
     own = weight_of(logit_at(x, gone), ref, c);
   }
-  double z[2] = {0.0, 0.0};
 #pragma unroll
-  for (int k = 0; k < V; ++k)
+  for (int g = 0; g < G; ++g) {
+    double z[2] = {0.0, 0.0};
 #pragma unroll
-    for (int e = 0; e < E; ++e) z[e & 1] += weight_in_sum(val[k][e], ref, c);
-  const double sum = wave_sum64(z[0] + z[1]);
-  if (lane == 0) sums[wave] = sum;
+    for (int k = 0; k < VS; ++k)
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        z[e & 1] += weight_in_sum(val[g * VS + k][e], ref, c);
+    sums[g][tid] = z[0] + z[1];
+  }
   __syncthreads();
-  if (tid != 0) return;
-  const double zx = or_nothing((sums[0] + sums[1]) + (sums[2] + sums[3]));
-  p.parts[(long)row * p.slices + slice] = {zx + own, zx, m, 0};
+  const int slice = part * G + wave;  // a wave adds one up
+  if (wave >= G || slice >= p.slices) return;
+  const double* of = sums[wave] + lane;
+  const double zx =
+      or_nothing(wave_sum64((of[0] + of[64]) + (of[128] + of[192])));
+  if (lane == 0)
+    p.parts[(long)row * p.slices + slice] = {
+        slice == own_slice ? zx + own : zx, zx, m, 0};
 }
 
 // A workgroup of kWide threads works a lane's verdict out from the slices'
@@ -380,28 +393,34 @@ __device__ __forceinline__ Weights<T> weights_of(const DraftArgs& p,
 // slices of the row where a draft fell.
 template <typename T>
 __global__ __launch_bounds__(kWide) void rest_kernel(DraftArgs p,
-                                                     gdn::LaneTable tl) {
+                                                     gdn::LaneTable tl,
+                                                     int groups) {
   __shared__ Rows rows;
-  __shared__ double sums[kWide / 64];
-  const int n = blockIdx.x / p.rest_slices, slice = blockIdx.x % p.rest_slices;
+  __shared__ double sums[kRestSlices][kWide / 64];
+  const int n = blockIdx.x / groups, part = blockIdx.x % groups;
   const int T_n = tl.v[n], tid = threadIdx.x;
   if (T_n < 2) return;
   const double c = exponent_of(p, n);
-  const Verdict v = decide<T>(p, n, T_n, c, rows, slice == 0);
-  if (slice == 0 && tid == 0) p.verdicts[n] = v;
+  const Verdict v = decide<T>(p, n, T_n, c, rows, part == 0);
+  if (part == 0 && tid == 0) p.verdicts[n] = v;
   if (!v.ok || v.m == T_n) return;
   const Weights<T> w = weights_of<T>(p, v, n, T_n, c, true);
-  double sum = 0.0;
 #pragma unroll
-  for (int k = 0; k < kRestSlice / kWide; ++k) {
-    const int i = slice * kRestSlice + k * kWide + tid;
-    if (i < p.vocab) sum += w.at(i);
+  for (int g = 0; g < kRestSlices; ++g) {
+    double sum = 0.0;
+#pragma unroll
+    for (int k = 0; k < kSlice / kWide; ++k) {
+      const int i = (part * kRestSlices + g) * kSlice + k * kWide + tid;
+      if (i < p.vocab) sum += w.at(i);
+    }
+    sum = wave_sum64(sum);
+    if (tid % 64 == 0) sums[g][tid / 64] = sum;
   }
-  sum = wave_sum64(sum);
-  if (tid % 64 == 0) sums[tid / 64] = sum;
   __syncthreads();
-  if (tid != 0) return;
-  for (int i = 1; i < kWide / 64; ++i) sum += sums[i];
+  const int slice = part * kRestSlices + tid;
+  if (tid >= kRestSlices || slice >= p.rest_slices) return;
+  double sum = sums[tid][0];
+  for (int i = 1; i < kWide / 64; ++i) sum += sums[tid][i];
   p.rest[(long)n * p.rest_slices + slice] = sum;
 }
 
@@ -409,8 +428,7 @@ __global__ __launch_bounds__(kWide) void rest_kernel(DraftArgs p,
 // lane: the slice that the border lies in, then the id within it.
 template <typename T>
 __global__ __launch_bounds__(kWide) void pick_kernel(DraftArgs p,
-                                                     gdn::LaneTable tl,
-                                                     int slice_ids) {
+                                                     gdn::LaneTable tl) {
   __shared__ Rows rows;
   __shared__ double sums[kWide / 64];
   __shared__ double found[2];  // the running sum before the slice, and the border
@@ -483,17 +501,15 @@ __global__ __launch_bounds__(kWide) void pick_kernel(DraftArgs p,
   const int slice = which >> 1;
   const Weights<T> w = weights_of<T>(p, v, n, T_n, c, rest);
   // ids of the slice, consecutive ones a thread
-  const bool by_rest = rest && p.draft;
-  const int ids = by_rest ? kRestSlice : slice_ids;
-  const int skew = by_rest ? 0 : skew_of(w.x);
-  const int per = (ids + kWide - 1) / kWide;
-  const int from = slice * ids - skew + tid * per;
+  constexpr int kPer = kSlice / kWide;
+  const int skew = rest && p.draft ? 0 : skew_of(w.x);
+  const int from = slice * kSlice - skew + tid * kPer;
   double mine = 0.0;
-  double x[8];
+  double x[kPer];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < kPer; ++k) {
     const int i = from + k;
-    x[k] = k < per && (unsigned)i < (unsigned)p.vocab ? w.at(i) : 0.0;
+    x[k] = (unsigned)i < (unsigned)p.vocab ? w.at(i) : 0.0;
     mine += x[k];
   }
   const double upto = wave_scan64(mine);
@@ -505,7 +521,7 @@ __global__ __launch_bounds__(kWide) void pick_kernel(DraftArgs p,
   double at = lane > 0 ? run + below : run;
   int first = -1, last = -1;  // past the border; of any weight
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < kPer; ++k) {
     at += x[k];
     if (x[k] > 0.0) {
       if (at > found[1] && first < 0) first = from + k;
@@ -534,36 +550,34 @@ static bool sizes_ok(int32_t n_lanes, int32_t t_max, int32_t vocab) {
   return n_lanes >= 1 && n_lanes <= GDN_MAX_LANES && t_max >= 1 &&
          t_max <= GDN_MAX_T && vocab >= 1 && vocab <= 1 << 30;
 }
-// Vectors per thread of a slice: 32 logits a thread, or 8 when that would
-// leave most of the CUs without a slice.
-static int vectors_for(int32_t n_lanes, int32_t t_max, int32_t vocab, int size) {
-  return gdnt::vectors_for(n_lanes * t_max, vocab, size);
-}
-static int rest_slices_for(int32_t vocab) {
-  return (vocab + kRestSlice - 1) / kRestSlice;
-}
+static int slices_for(int32_t vocab) { return (vocab + kSlice - 1) / kSlice; }
 static size_t bytes_for(int32_t n_lanes, int32_t t_max, int32_t vocab,
                         int slices) {
   return round16((size_t)n_lanes * (2 * t_max - 1) * slices * sizeof(Part)) +
-         round16((size_t)n_lanes * rest_slices_for(vocab) * sizeof(double)) +
+         round16((size_t)n_lanes * slices_for(vocab) * sizeof(double)) +
          round16((size_t)n_lanes * sizeof(Verdict));
 }
 
+// Four slices a workgroup (8 logits a thread each), or one where that would
+// leave most of the CUs without any.
 template <typename T>
-static hipError_t run(const DraftArgs& p, const gdn::LaneTable& tl, int v,
+static hipError_t run(const DraftArgs& p, const gdn::LaneTable& tl,
                       hipStream_t st) {
-  constexpr int kMany = 32 * sizeof(T) / 16, kFew = 8 * sizeof(T) / 16;
   const int rows = p.lanes * (p.draft ? 2 * p.t_max - 1 : p.t_max);
-  const dim3 grid((unsigned)((long)rows * p.slices));
-  hipError_t e = v == kMany
-                     ? launch(sum_kernel<T, kMany>, grid, dim3(kThreads), st, p, tl)
-                     : launch(sum_kernel<T, kFew>, grid, dim3(kThreads), st, p, tl);
-  if (e == hipSuccess && p.draft)
-    e = launch(rest_kernel<T>, dim3((unsigned)(p.lanes * p.rest_slices)),
-               dim3(kWide), st, p, tl);
+  const long fours = (long)rows * ((p.slices + 3) / 4);
+  const bool few = fours < 256;
+  const int groups = few ? p.slices : (p.slices + 3) / 4;
+  const dim3 grid((unsigned)((long)rows * groups));
+  hipError_t e =
+      few ? launch(sum_kernel<T, 1>, grid, dim3(kThreads), st, p, tl, groups)
+          : launch(sum_kernel<T, 4>, grid, dim3(kThreads), st, p, tl, groups);
+  if (e == hipSuccess && p.draft) {
+    const int parts = (p.rest_slices + kRestSlices - 1) / kRestSlices;
+    e = launch(rest_kernel<T>, dim3((unsigned)((long)p.lanes * parts)),
+               dim3(kWide), st, p, tl, parts);
+  }
   if (e != hipSuccess) return e;
-  return launch(pick_kernel<T>, dim3((unsigned)p.lanes), dim3(kWide), st, p, tl,
-                kThreads * v * (int)(16 / sizeof(T)));
+  return launch(pick_kernel<T>, dim3((unsigned)p.lanes), dim3(kWide), st, p, tl);
 }
 
 }  // namespace gdnv
@@ -573,15 +587,7 @@ extern "C" size_t gdn_draft_verify_workspace_bytes(int32_t n_lanes,
                                                    int32_t vocab) {
   using namespace gdnv;
   if (!sizes_ok(n_lanes, t_max, vocab)) return 0;
-  // the larger of the two types' needs
-  size_t need = 0;
-  for (int size = 2; size <= 4; size += 2) {
-    const int v = vectors_for(n_lanes, t_max, vocab, size);
-    const size_t n = bytes_for(n_lanes, t_max, vocab,
-                               gdnt::slices_for(vocab, size, v, false));
-    if (n > need) need = n;
-  }
-  return need;
+  return bytes_for(n_lanes, t_max, vocab, slices_for(vocab) + 1);
 }
 
 extern "C" int gdn_draft_verify(int32_t n_lanes, int32_t t_max,
@@ -626,16 +632,17 @@ extern "C" int gdn_draft_verify(int32_t n_lanes, int32_t t_max,
   if (!any) return GDN_OK;
   DraftArgs p = {logits, t_max > 1 ? draft_logits : nullptr, tokens, uniforms,
                  inv_temperature, m_lane, next_token, accept, row_stride,
-                 draft_stride, n_lanes, t_max, vocab, 0, rest_slices_for(vocab),
+                 draft_stride, n_lanes, t_max, vocab, 0, slices_for(vocab),
                  nullptr, nullptr, nullptr};
-  const int v = vectors_for(n_lanes, t_max, vocab, size);
+  // a row that starts within a line may reach into one slice more
   const auto in_lines = [&](const void* x, int64_t stride) {
     return !misaligned(x, 16) && stride * size % 16 == 0;
   };
-  p.slices = gdnt::slices_for(
-      vocab, size, v,
-      in_lines(logits, row_stride) &&
-          (!p.draft || in_lines(p.draft, draft_stride)));
+  p.slices = slices_for(vocab) +
+             (in_lines(logits, row_stride) &&
+                      (!p.draft || in_lines(p.draft, draft_stride))
+                  ? 0
+                  : 1);
   if ((double)n_lanes * (2 * t_max - 1) * p.slices > (double)INT_MAX)
     return fail(GDN_EINVAL, "gdn_draft_verify: grid too large");
   p.parts = (Part*)workspace;
@@ -644,7 +651,7 @@ extern "C" int gdn_draft_verify(int32_t n_lanes, int32_t t_max,
   p.verdicts = (Verdict*)((char*)p.rest + round16((size_t)n_lanes * p.rest_slices *
                                                   sizeof(double)));
   const hipError_t e = in_dtype == GDN_BF16
-                           ? run<uint16_t>(p, tl, v, (hipStream_t)stream)
-                           : run<float>(p, tl, v, (hipStream_t)stream);
+                           ? run<uint16_t>(p, tl, (hipStream_t)stream)
+                           : run<float>(p, tl, (hipStream_t)stream);
   return gdn::hip_status(e, "gdn_draft_verify launch");
 }
