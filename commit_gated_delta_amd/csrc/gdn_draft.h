@@ -11,13 +11,14 @@
 // Kalman & Matias, "Fast Inference from Transformers via Speculative
 // Decoding", ICML 2023, Sec. 2.3 and appendix A.1).
 //
-// A token is where a running sum passes a given number, so an error d of the
-// sums moves it with a chance of about d times the number of likely tokens:
-// every exponential and sum here is f64.
+// Which drafts stand needs every row but the last, so their sums are f32 at
+// the memory's rate.  The next token is where a running sum passes a given
+// number, and an error d of the sums moves it with a chance of about d times
+// the number of likely tokens: the one row that it is sampled from is summed
+// up again in f64.
 #pragma once
 #include <hip/hip_runtime.h>
 
-#include <cfloat>
 #include <cmath>
 
 #include "gdn.h"
@@ -35,20 +36,28 @@ using gdnt::u32x4;
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // What a slice of a row leaves behind: its largest logit (NaN if it holds
-// one), the sum of 2^((x - m) c) with that as m, and the same without the
-// row's draft.
+// one) and the sum of 2^((x - m) c) with that as m.
 struct Part {
-  double z, zx;
+  float m, z;
+};
+// The same of a slice of the row that the next token is sampled from, without
+// the id that it cannot be.
+struct Exact {
+  double z;
   float m;
   int pad;
 };
 
-// What a lane's window comes to.
+// What a lane's drafts come to.
 struct Verdict {
   int m;   // accepted prefix, the anchor included
-  int ok;  // row m - 1 (and the drafter's, if a draft fell) has a distribution
-  double top, z;              // of row m - 1
-  double draft_top, draft_z;  // of the drafter's row m - 1, if a draft fell
+  int ok;  // the rows that a draft fell at have distributions
+};
+
+// Of the rows that a fallen draft and its drafter's distribution leave: the
+// largest logits and the reciprocals of the sums.
+struct Left {
+  double top, draft_top, f, draft_f;
 };
 
 struct DraftArgs {
@@ -61,17 +70,20 @@ struct DraftArgs {
   float* accept;
   long stride, draft_stride;
   int lanes, t_max, vocab;
-  int slices;        // of a row, in `parts`, from its first 16-byte line on
-  int rest_slices;   // of a row, in `rest`, from its first id on
-  Part* parts;       // [target rows, then drafter's rows][slices]
-  double* rest;      // [lanes][rest_slices]: sums of max(p - q, 0)
-  Verdict* verdicts;  // [lanes], of windows with drafts that have a distribution
+  int groups;      // slices of a row in `parts`, of kGroup ids
+  int slices;      // slices of a row in `exact`, of kSlice ids; both count from
+                   // the 16-byte line that a row starts in
+  Part* parts;     // [target rows 0 .. t_max - 2, then drafter's rows][groups]
+  Exact* exact;    // [lanes][target's row, drafter's][slices]
+  double* rest;    // [lanes][slices]: sums of max(p - q, 0), from the first id on
+  Verdict* verdicts;  // [lanes]
+  Left* left;         // [lanes]
 };
 
-constexpr int kSlice = 2048;   // ids of a slice
-constexpr int kThreads = 256;  // of sum_kernel
-constexpr int kWide = 1024;    // of the kernels behind it
-constexpr int kRestSlices = 2;  // of a workgroup of rest_kernel
+constexpr int kSlice = 2048, kGroup = 8192;
+constexpr int kThreads = 256;  // of sum_kernel and rest_kernel
+constexpr int kExact = 512;    // of exact_kernel
+constexpr int kPick = 1024;    // of pick_kernel
 
 // 2^y for -1020 <= y <= 1, to 2e-14: a polynomial through the Chebyshev nodes
 // of [-1/2, 1/2] for the fraction, the whole part added to the exponent.  (The
@@ -178,113 +190,117 @@ __device__ __forceinline__ int skew_of(const T* x) {
   return (int)((uintptr_t)x % 16 / sizeof(T));
 }
 
-// One workgroup per G slices of a row, read once into registers.
-template <typename T, int G>
-__global__ __launch_bounds__(kThreads, 4) void sum_kernel(DraftArgs p,
-                                                          gdn::LaneTable tl,
-                                                          int groups) {
-  constexpr int E = 16 / sizeof(T);              // logits per vector
-  constexpr int VS = kSlice / (kThreads * E);    // vectors of a slice
-  constexpr int V = G * VS;
-  __shared__ float tops[4];
-  __shared__ double sums[G][kThreads];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int row = blockIdx.x / groups, part = blockIdx.x % groups;
-  const int targets = p.lanes * p.t_max;
-  const bool drafter = row >= targets;
-  const int per = drafter ? p.t_max - 1 : p.t_max;
-  const int n = (drafter ? row - targets : row) / per;
-  const int t = (drafter ? row - targets : row) % per;
-  if (t >= tl.v[n] - (drafter ? 1 : 0)) return;
-  const T* x = drafter ? drafter_row<T>(p, n, t) : target_row<T>(p, n, t);
-  const int skew = skew_of(x);
-  const u32x4* line = reinterpret_cast<const u32x4*>(x - skew);
-  const int lines = (p.vocab + skew + E - 1) / E;
-  const int first = part * kThreads * V + tid;
+// A workgroup's share of a row: N logits a thread from line `first_line` on
+// (threads take vectors in turn), masked past the row's ends.
+template <typename T, int N, int THREADS>
+struct Share {
+  static constexpr int E = 16 / sizeof(T), V = N / E;
+  float x[V][E];
+  int first, skew;  // this thread's first line
 
-  u32x4 raw[V];
+  __device__ __forceinline__ void load(const T* row, int vocab, int first_line) {
+    skew = skew_of(row);
+    first = first_line + threadIdx.x;
+    const u32x4* line = reinterpret_cast<const u32x4*>(row - skew);
+    const int lines = (vocab + skew + E - 1) / E;
+    u32x4 raw[V];
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
-    const int i = first + k * kThreads;
-    raw[k] = line[i < lines ? i : lines - 1];
-  }
-  // (only a row's draft without the drafter's distribution is left out)
-  const int gone = !drafter && !p.draft && t + 1 < tl.v[n]
-                       ? p.tokens[(long)n * p.t_max + t + 1]
-                       : -1;
-  const double c = exponent_of(p, n);
-  float val[V][E];
-  float m = -INFINITY;
+    for (int k = 0; k < V; ++k) {
+      const int i = first + k * THREADS;
+      raw[k] = line[i < lines ? i : lines - 1];
+    }
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
-    const int i = first + k * kThreads;
-    const int id = i < lines ? i * E - skew : p.vocab;
+    for (int k = 0; k < V; ++k) {
+      const int i = first + k * THREADS;
+      const int id = i < lines ? i * E - skew : vocab;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if constexpr (sizeof(T) == 4) val[k][e] = __uint_as_float(raw[k][e]);
-      else
-        val[k][e] = __uint_as_float(e & 1 ? raw[k][e / 2] & 0xffff0000u
+      for (int e = 0; e < E; ++e) {
+        if constexpr (sizeof(T) == 4) x[k][e] = __uint_as_float(raw[k][e]);
+        else
+          x[k][e] = __uint_as_float(e & 1 ? raw[k][e / 2] & 0xffff0000u
                                           : raw[k][e / 2] << 16);
-    }
-    if (id < 0 || id > p.vocab - E) {
+      }
+      if (id < 0 || id > vocab - E) {
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if ((unsigned)(id + e) >= (unsigned)p.vocab) val[k][e] = -INFINITY;
+        for (int e = 0; e < E; ++e)
+          if ((unsigned)(id + e) >= (unsigned)vocab) x[k][e] = -INFINITY;
+      }
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) m = nan_max(m, val[k][e]);
   }
-  m = wave_nan_max(m);
-  if (lane == 0) tops[wave] = m;
-  __syncthreads();
-  m = nan_max(nan_max(tops[0], tops[1]), nan_max(tops[2], tops[3]));
-  const double ref = m == -INFINITY ? 0.0 : (double)m;
-  // the draft is taken out of its slice's sum, and added for a second one
-  double own = 0.0;
-  const int own_slice = gone < 0 || gone >= p.vocab ? -1 : (gone + skew) / kSlice;
-  if (own_slice >= part * G && own_slice < (part + 1) * G) {
+  __device__ __forceinline__ float most() const {
+    float m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int e = 0; e < E; ++e) m = nan_max(m, x[k][e]);
+    return m;
+  }
+  __device__ __forceinline__ void leave_out(int id) {
 #pragma unroll
     for (int k = 0; k < V; ++k)
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if ((first + k * kThreads) * E - skew + e == gone) val[k][e] = -INFINITY;
-    own = weight_of(logit_at(x, gone), ref, c);
+        if ((first + k * THREADS) * E - skew + e == id) x[k][e] = -INFINITY;
   }
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    double z[2] = {0.0, 0.0};
-#pragma unroll
-    for (int k = 0; k < VS; ++k)
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        z[e & 1] += weight_in_sum(val[g * VS + k][e], ref, c);
-    sums[g][tid] = z[0] + z[1];
-  }
+};
+
+// Sums of the rows that decide about the drafts: a workgroup per kGroup ids,
+// read once into registers.  Bound by HBM.
+template <typename T>
+__global__ __launch_bounds__(kThreads, 4) void sum_kernel(DraftArgs p,
+                                                          gdn::LaneTable tl) {
+  constexpr int N = kGroup / kThreads;
+  __shared__ float tops[4], sums[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int row = blockIdx.x / p.groups, part = blockIdx.x % p.groups;
+  const int per = p.t_max - 1, targets = p.lanes * per;
+  const bool drafter = row >= targets;
+  const int n = (drafter ? row - targets : row) / per;
+  const int t = (drafter ? row - targets : row) % per;
+  if (t >= tl.v[n] - 1) return;
+  Share<T, N, kThreads> s;
+  s.load(drafter ? drafter_row<T>(p, n, t) : target_row<T>(p, n, t), p.vocab,
+         part * (kGroup / Share<T, N, kThreads>::E));
+  const double c = exponent_of(p, n);
+  float m = wave_nan_max(s.most());
+  if (lane == 0) tops[wave] = m;
   __syncthreads();
-  const int slice = part * G + wave;  // a wave adds one up
-  if (wave >= G || slice >= p.slices) return;
-  const double* of = sums[wave] + lane;
-  const double zx =
-      or_nothing(wave_sum64((of[0] + of[64]) + (of[128] + of[192])));
-  if (lane == 0)
-    p.parts[(long)row * p.slices + slice] = {
-        slice == own_slice ? zx + own : zx, zx, m, 0};
+  m = nan_max(nan_max(tops[0], tops[1]), nan_max(tops[2], tops[3]));
+  // c in two parts: rounded to one it would tilt the exponents of far logits
+  const float ref = m == -INFINITY ? 0.f : m;
+  const float hi = (float)c, lo = (float)(c - (double)hi);
+  const float far = -512.f / hi;  // (2^-512 is 0; a -inf is cut off there)
+  float z = 0.f;
+#pragma unroll
+  for (int k = 0; k < s.V; ++k)
+#pragma unroll
+    for (int e = 0; e < s.E; ++e) {
+      const float d = nan_max(s.x[k][e] - ref, far);
+      z += __builtin_amdgcn_exp2f(__builtin_fmaf(d, hi, d * lo));
+    }
+  z = gdn::wave_sum(z);
+  if (lane == 0) sums[wave] = z;
+  __syncthreads();
+  if (tid == 0)
+    p.parts[(long)row * p.groups + part] = {
+        m, (sums[0] + sums[1]) + (sums[2] + sums[3])};
 }
 
-// A workgroup of kWide threads works a lane's verdict out from the slices'
+// A workgroup of kExact threads works a lane's verdict out from the slices'
 // sums, a wave a row.
 struct Rows {
   float m[2][GDN_MAX_T];
   double z[2][GDN_MAX_T];
-  int accepted;
+  Verdict verdict;
 };
 template <typename T>
 __device__ __forceinline__ Verdict decide(const DraftArgs& p, int n, int T_n,
                                           double c, Rows& rows, bool write) {
   const int lane = threadIdx.x & 63, wave = gdn::uniform(threadIdx.x >> 6);
+  const int drafts = T_n - 1;
   // the first wave's lanes hold a draft each: its logits are on their way
   // while the rows are summed up
-  const bool drafted = wave == 0 && lane < T_n - 1;
+  const bool drafted = wave == 0 && lane < drafts;
   bool inside = false;
   float pw = 0.f, qw = 0.f, u = 0.f;
   if (drafted) {
@@ -295,42 +311,40 @@ __device__ __forceinline__ Verdict decide(const DraftArgs& p, int n, int T_n,
     pw = logit_at(target_row<T>(p, n, lane), i);
     if (p.draft) qw = logit_at(drafter_row<T>(p, n, lane), i);
   }
-  const int count = T_n + (p.draft ? T_n - 1 : 0);
+  const int count = p.draft ? 2 * drafts : drafts;
   auto parts_of = [&](int r) {
-    const long row = r < T_n ? (long)n * p.t_max + r
-                             : (long)p.lanes * p.t_max +
-                                   (long)n * (p.t_max - 1) + (r - T_n);
-    return p.parts + row * p.slices;
+    const int d = r >= drafts ? 1 : 0;
+    return p.parts + (((long)d * p.lanes + n) * (p.t_max - 1) + r - d * drafts) * p.groups;
   };
-  constexpr int kStep = kWide / 64;
-  const Part none = {0.0, 0.0, -INFINITY, 0};
+  constexpr int kStep = kExact / 64;
+  const Part none = {-INFINITY, 0.f};
   Part next = none;
-  if (wave < count && lane < p.slices) next = parts_of(wave)[lane];
+  if (wave < count && lane < p.groups) next = parts_of(wave)[lane];
   for (int r = wave; r < count; r += kStep) {
     const Part* parts = parts_of(r);
     const Part first = next;
     next = none;
-    if (r + kStep < count && lane < p.slices) next = parts_of(r + kStep)[lane];
+    if (r + kStep < count && lane < p.groups) next = parts_of(r + kStep)[lane];
     float m = first.m;
-    for (int i = lane + 64; i < p.slices; i += 64) m = nan_max(m, parts[i].m);
+    for (int i = lane + 64; i < p.groups; i += 64) m = nan_max(m, parts[i].m);
     m = wave_nan_max(m);
     const double ref = m == -INFINITY ? 0.0 : (double)m;
     double z = first.z * weight_of(first.m, ref, c);
-    for (int i = lane + 64; i < p.slices; i += 64)
+    for (int i = lane + 64; i < p.groups; i += 64)
       z += parts[i].z * weight_of(parts[i].m, ref, c);
     z = wave_sum64(z);
     if (lane == 0) {
-      const int d = r >= T_n;
-      rows.m[d][d ? r - T_n : r] = m;
-      rows.z[d][d ? r - T_n : r] = z;
+      const int d = r >= drafts;
+      rows.m[d][r - d * drafts] = m;
+      rows.z[d][r - d * drafts] = z;
     }
   }
   __syncthreads();
   if (wave == 0) {
-    bool stands = true;  // (lanes past the drafts)
+    bool stands = true, ok = true;  // (lanes past the drafts)
     if (drafted) {
       const float m = rows.m[0][lane];
-      bool ok = c > 0.0 && fabsf(m) < INFINITY;
+      ok = c > 0.0 && fabsf(m) < INFINITY;
       if (p.draft) ok = ok && fabsf(rows.m[1][lane]) < INFINITY;
       double a = 0.0, b = 1.0;  // chances of the draft
       if (ok && inside) {
@@ -342,137 +356,187 @@ __device__ __forceinline__ Verdict decide(const DraftArgs& p, int n, int T_n,
         p.accept[(long)n * p.t_max + lane] =
             !ok ? NAN : a == 0.0 ? 0.f : a >= b ? 1.f : (float)(a / b);
     }
-    const uint64_t fell = __ballot(!stands);
-    if (lane == 0) rows.accepted = fell ? __builtin_ctzll(fell) + 1 : T_n;
+    const uint64_t fell = __ballot(!stands), good = __ballot(ok);
+    if (lane == 0) {
+      const int first = fell ? __builtin_ctzll(fell) : drafts;
+      rows.verdict = {first + 1, (int)(good >> first & 1)};
+    }
   }
   __syncthreads();
-  Verdict v;
-  v.m = rows.accepted;
-  const int t = v.m - 1;
-  v.top = rows.m[0][t];
-  v.z = rows.z[0][t];
-  v.ok = c > 0.0 && fabsf(rows.m[0][t]) < INFINITY;
-  v.draft_top = v.draft_z = 1.0;
-  if (p.draft && v.m < T_n) {
-    v.draft_top = rows.m[1][t];
-    v.draft_z = rows.z[1][t];
-    v.ok = v.ok && fabsf(rows.m[1][t]) < INFINITY;
-  }
-  return v;
+  return rows.verdict;
 }
 
-// Weights of row m - 1 that the next token is taken by, apart from a common
-// factor.
+// The verdicts, and f64 sums by slices of the row that the next token is
+// sampled from (leaving the fallen draft out, where it has no distribution),
+// or of the drafter's row beside it.  A workgroup takes kGroup ids.
 template <typename T>
-struct Weights {
-  const T *x, *y;  // the row and the drafter's, or NULL
-  double top, draft_top, f, draft_f, c;
-  int gone;        // an id of weight 0, or -1
-  __device__ __forceinline__ double at(int i) const {
-    double w = weight_of(logit_at(x, i), top, c) * f;
-    if (y) {
-      w -= weight_of(logit_at(y, i), draft_top, c) * draft_f;
-      w = w > 0.0 ? w : 0.0;
-    }
-    return i == gone ? 0.0 : w;
-  }
-};
-template <typename T>
-__device__ __forceinline__ Weights<T> weights_of(const DraftArgs& p,
-                                                 const Verdict& v, int n,
-                                                 int T_n, double c, bool rest) {
-  const int t = v.m - 1;
-  Weights<T> w = {target_row<T>(p, n, t), nullptr, v.top, v.draft_top,
-                  1.0 / v.z, 1.0 / v.draft_z, c, -1};
-  if (rest && p.draft) w.y = drafter_row<T>(p, n, t);
-  if (rest && !p.draft) w.gone = p.tokens[(long)n * p.t_max + t + 1];
-  return w;
-}
-
-// With a drafter's distribution: the verdicts, and sums of max(p - q, 0) by
-// slices of the row where a draft fell.
-template <typename T>
-__global__ __launch_bounds__(kWide) void rest_kernel(DraftArgs p,
-                                                     gdn::LaneTable tl,
-                                                     int groups) {
+__global__ __launch_bounds__(kExact) void exact_kernel(DraftArgs p,
+                                                      gdn::LaneTable tl,
+                                                      int sides) {
+  constexpr int N = kGroup / kExact, kSlices = kGroup / kSlice;
+  typedef Share<T, N, kExact> S;
+  constexpr int kVectors = kSlice / S::E;  // of a slice
   __shared__ Rows rows;
-  __shared__ double sums[kRestSlices][kWide / 64];
-  const int n = blockIdx.x / groups, part = blockIdx.x % groups;
-  const int T_n = tl.v[n], tid = threadIdx.x;
-  if (T_n < 2) return;
+  __shared__ float tops[kExact / 64];
+  __shared__ double sums[kSlices][kVectors];
+  const int part = blockIdx.x % p.groups;
+  const int side = blockIdx.x / p.groups % sides;
+  const int n = blockIdx.x / p.groups / sides, T_n = tl.v[n];
+  if (T_n == 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = gdn::uniform(tid >> 6);
   const double c = exponent_of(p, n);
-  const Verdict v = decide<T>(p, n, T_n, c, rows, part == 0);
-  if (part == 0 && tid == 0) p.verdicts[n] = v;
-  if (!v.ok || v.m == T_n) return;
-  const Weights<T> w = weights_of<T>(p, v, n, T_n, c, true);
+  Verdict v = {1, 1};
+  if (T_n > 1) v = decide<T>(p, n, T_n, c, rows, part == 0 && side == 0);
+  if (part == 0 && side == 0 && tid == 0) p.verdicts[n] = v;
+  const bool fell = v.m < T_n;
+  if (!v.ok || (side == 1 && !fell)) return;
+  S s;
+  s.load(side ? drafter_row<T>(p, n, v.m - 1) : target_row<T>(p, n, v.m - 1),
+         p.vocab, part * (kGroup / S::E));
+  float m = wave_nan_max(s.most());
+  if (lane == 0) tops[wave] = m;
+  __syncthreads();
 #pragma unroll
-  for (int g = 0; g < kRestSlices; ++g) {
-    double sum = 0.0;
+  for (int i = 0; i < kExact / 64; ++i) m = nan_max(m, tops[i]);
+  const double ref = m == -INFINITY ? 0.0 : (double)m;
+  if (fell && !p.draft) s.leave_out(p.tokens[(long)n * p.t_max + v.m]);
 #pragma unroll
-    for (int k = 0; k < kSlice / kWide; ++k) {
-      const int i = (part * kRestSlices + g) * kSlice + k * kWide + tid;
-      if (i < p.vocab) sum += w.at(i);
-    }
-    sum = wave_sum64(sum);
-    if (tid % 64 == 0) sums[g][tid / 64] = sum;
+  for (int k = 0; k < S::V; ++k) {
+    double z[2] = {0.0, 0.0};
+#pragma unroll
+    for (int e = 0; e < S::E; ++e)
+      z[e & 1] += weight_in_sum(s.x[k][e], ref, c);
+    const int at = k * kExact + tid;  // of the group's vectors
+    sums[at / kVectors][at % kVectors] = z[0] + z[1];
   }
   __syncthreads();
-  const int slice = part * kRestSlices + tid;
-  if (tid >= kRestSlices || slice >= p.rest_slices) return;
-  double sum = sums[tid][0];
-  for (int i = 1; i < kWide / 64; ++i) sum += sums[tid][i];
-  p.rest[(long)n * p.rest_slices + slice] = sum;
+  const int slice = part * kSlices + wave;  // a wave adds one up
+  if (wave >= kSlices || slice >= p.slices) return;
+  double z = 0.0;
+#pragma unroll
+  for (int i = 0; i < kVectors / 64; ++i) z += sums[wave][64 * i + lane];
+  z = or_nothing(wave_sum64(z));
+  if (lane == 0)
+    p.exact[((long)n * 2 + side) * p.slices + slice] = {z, m, 0};
 }
 
-// The next token (and the verdict, where it is not there yet), a workgroup per
-// lane: the slice that the border lies in, then the id within it.
+// A row of `exact`: its largest logit and the sum of its weights to that.
+// Every wave works it out for itself.
+__device__ __forceinline__ void whole_row(const Exact* e, int slices, double c,
+                                          float& m, double& z) {
+  const int lane = threadIdx.x & 63;
+  m = -INFINITY;
+  for (int i = lane; i < slices; i += 64) m = nan_max(m, e[i].m);
+  m = wave_nan_max(m);
+  const double ref = m == -INFINITY ? 0.0 : (double)m;
+  z = 0.0;
+  for (int i = lane; i < slices; i += 64) z += e[i].z * weight_of(e[i].m, ref, c);
+  z = wave_sum64(z);
+}
+
+// max(p - q, 0) of an id.
+__device__ __forceinline__ double weight_left(const Left& r, float x, float y,
+                                              double c) {
+  const double w = weight_of(x, r.top, c) * r.f -
+                   weight_of(y, r.draft_top, c) * r.draft_f;
+  return w > 0.0 ? w : 0.0;
+}
+
+// With a drafter's distribution: sums of max(p - q, 0) by slices of the row
+// where a draft fell.
 template <typename T>
-__global__ __launch_bounds__(kWide) void pick_kernel(DraftArgs p,
+__global__ __launch_bounds__(kThreads) void rest_kernel(DraftArgs p,
+                                                        gdn::LaneTable tl) {
+  constexpr int N = kSlice / kThreads;
+  __shared__ double sums[kThreads / 64];
+  const int n = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
+  const int tid = threadIdx.x;
+  if (tl.v[n] < 2) return;
+  const Verdict v = p.verdicts[n];
+  if (!v.ok || v.m == tl.v[n]) return;
+  const T* row = target_row<T>(p, n, v.m - 1);
+  const T* drafter = drafter_row<T>(p, n, v.m - 1);
+  float x[N], y[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int i = slice * kSlice + k * kThreads + tid;
+    x[k] = y[k] = -INFINITY;
+    if (i < p.vocab) {
+      x[k] = logit_at(row, i);
+      y[k] = logit_at(drafter, i);
+    }
+  }
+  const double c = exponent_of(p, n);
+  const Exact* e = p.exact + (long)n * 2 * p.slices;
+  float m, dm;
+  double z, dz;
+  whole_row(e, p.slices, c, m, z);
+  whole_row(e + p.slices, p.slices, c, dm, dz);
+  const Left r = {m, dm, 1.0 / z, 1.0 / dz};
+  if (slice == 0 && tid == 0) p.left[n] = r;
+  double sum = 0.0;
+#pragma unroll
+  for (int k = 0; k < N; ++k) sum += weight_left(r, x[k], y[k], c);
+  sum = wave_sum64(sum);
+  if (tid % 64 == 0) sums[tid / 64] = sum;
+  __syncthreads();
+  if (tid == 0)
+    p.rest[(long)n * p.slices + slice] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+}
+
+// The next token, a workgroup per lane: the slice that the border lies in,
+// then the id within it.
+template <typename T>
+__global__ __launch_bounds__(kPick) void pick_kernel(DraftArgs p,
                                                      gdn::LaneTable tl) {
-  __shared__ Rows rows;
-  __shared__ double sums[kWide / 64];
+  __shared__ double sums[kPick / 64];
   __shared__ double found[2];  // the running sum before the slice, and the border
-  __shared__ int which, first_id[kWide / 64], last_id[kWide / 64];
+  __shared__ int which, first_id[kPick / 64], last_id[kPick / 64];
   const int n = blockIdx.x, T_n = tl.v[n];
   const int tid = threadIdx.x, lane = tid & 63, wave = gdn::uniform(tid >> 6);
   if (T_n == 0) return;
   const double c = exponent_of(p, n);
-  const Verdict v = p.draft && T_n > 1 ? p.verdicts[n]
-                                       : decide<T>(p, n, T_n, c, rows, true);
-  if (!v.ok) {
+  const Verdict v = p.verdicts[n];
+  const bool fell = v.m < T_n;
+  const Exact* e = p.exact + (long)n * 2 * p.slices;
+  Left r;
+  float top = NAN;
+  if (v.ok && fell && p.draft) {
+    r = p.left[n];
+    top = (float)r.top;
+  } else if (v.ok) {
+    double z;
+    whole_row(e, p.slices, c, top, z);
+  }
+  if (!v.ok || !(c > 0.0) || !(fabsf(top) < INFINITY)) {
     if (tid == 0) {
       p.m[n] = v.m;
       p.next[n] = -1;
     }
     return;
   }
-  bool rest = v.m < T_n;
-  const int t = v.m - 1;
-  const Part* parts = p.parts + ((long)n * p.t_max + t) * p.slices;
-  const float u = p.uniforms[(long)n * p.t_max + T_n - 1];
   if (wave == 0) {
+    bool rest = fell && p.draft;
+    const float u = p.uniforms[(long)n * p.t_max + T_n - 1];
     const double share = u > 0.f ? u < 1.f ? (double)u : 1.0 : 0.0;
-    auto slice_sum = [&](int i, int count) {
-      if (i >= count) return 0.0;
-      if (rest && p.draft) return p.rest[(long)n * p.rest_slices + i];
-      return or_nothing((rest ? parts[i].zx : parts[i].z) *
-                        weight_of(parts[i].m, v.top, c)) / v.z;
+    auto slice_sum = [&](int i) {
+      if (i >= p.slices) return 0.0;
+      if (rest) return p.rest[(long)n * p.slices + i];
+      return or_nothing(e[i].z * weight_of(e[i].m, top, c));
     };
     for (;;) {
-      const int count = rest && p.draft ? p.rest_slices : p.slices;
       double whole = 0.0;
-      for (int i0 = 0; i0 < count; i0 += 64)
-        whole += lane_value(wave_scan64(slice_sum(i0 + lane, count)), 63);
+      for (int i0 = 0; i0 < p.slices; i0 += 64)
+        whole += lane_value(wave_scan64(slice_sum(i0 + lane)), 63);
       if (whole == 0.0 && rest) {  // nothing is left: from p
         rest = false;
         continue;
       }
       const double border = share * whole;
-      double before = 0.0, base = 0.0;
-      int got = -1, last = 0;
-      double last_base = 0.0;
-      for (int i0 = 0; i0 < count && got < 0; i0 += 64) {
-        const double x = slice_sum(i0 + lane, count);
+      double before = 0.0, base = 0.0, last_base = 0.0;
+      int got = -1, last = -1;
+      for (int i0 = 0; i0 < p.slices && got < 0; i0 += 64) {
+        const double x = slice_sum(i0 + lane);
         const double upto = wave_scan64(x);
         const uint64_t hit = __ballot(before + upto > border && x > 0.0);
         const uint64_t some = __ballot(x > 0.0);
@@ -489,7 +553,7 @@ __global__ __launch_bounds__(kWide) void pick_kernel(DraftArgs p,
         before += lane_value(upto, 63);
       }
       if (lane == 0) {
-        which = (got >= 0 ? got : last) << 1 | (rest ? 1 : 0);
+        which = (got >= 0 ? got : last) * 2 + (rest ? 1 : 0);
         found[0] = got >= 0 ? base : last_base;
         found[1] = border;
       }
@@ -497,19 +561,29 @@ __global__ __launch_bounds__(kWide) void pick_kernel(DraftArgs p,
     }
   }
   __syncthreads();
-  rest = which & 1;
-  const int slice = which >> 1;
-  const Weights<T> w = weights_of<T>(p, v, n, T_n, c, rest);
+  if (which < 0) {  // p is nothing but the draft that fell to rounding
+    if (tid == 0) {
+      p.m[n] = v.m;
+      p.next[n] = p.tokens[(long)n * p.t_max + v.m];
+    }
+    return;
+  }
+  const bool rest = which & 1;
+  const T* row = target_row<T>(p, n, v.m - 1);
+  const int gone = fell && !p.draft ? p.tokens[(long)n * p.t_max + v.m] : -1;
   // ids of the slice, consecutive ones a thread
-  constexpr int kPer = kSlice / kWide;
-  const int skew = rest && p.draft ? 0 : skew_of(w.x);
-  const int from = slice * kSlice - skew + tid * kPer;
+  constexpr int kPer = kSlice / kPick;
+  const int from = (which >> 1) * kSlice - (rest ? 0 : skew_of(row)) + tid * kPer;
   double mine = 0.0;
   double x[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int i = from + k;
-    x[k] = (unsigned)i < (unsigned)p.vocab ? w.at(i) : 0.0;
+    x[k] = 0.0;
+    if ((unsigned)i < (unsigned)p.vocab && i != gone)
+      x[k] = rest ? weight_left(r, logit_at(row, i),
+                                logit_at(drafter_row<T>(p, n, v.m - 1), i), c)
+                  : weight_of(logit_at(row, i), top, c);
     mine += x[k];
   }
   const double upto = wave_scan64(mine);
@@ -539,8 +613,8 @@ __global__ __launch_bounds__(kWide) void pick_kernel(DraftArgs p,
   __syncthreads();
   if (tid != 0) return;
   int token = -1;
-  for (int i = 0; i < kWide / 64 && token < 0; ++i) token = first_id[i];
-  for (int i = kWide / 64 - 1; i >= 0 && token < 0; --i) token = last_id[i];
+  for (int i = 0; i < kPick / 64 && token < 0; ++i) token = first_id[i];
+  for (int i = kPick / 64 - 1; i >= 0 && token < 0; --i) token = last_id[i];
   p.m[n] = v.m;
   p.next[n] = token;
 }
@@ -550,34 +624,43 @@ static bool sizes_ok(int32_t n_lanes, int32_t t_max, int32_t vocab) {
   return n_lanes >= 1 && n_lanes <= GDN_MAX_LANES && t_max >= 1 &&
          t_max <= GDN_MAX_T && vocab >= 1 && vocab <= 1 << 30;
 }
-static int slices_for(int32_t vocab) { return (vocab + kSlice - 1) / kSlice; }
-static size_t bytes_for(int32_t n_lanes, int32_t t_max, int32_t vocab,
-                        int slices) {
-  return round16((size_t)n_lanes * (2 * t_max - 1) * slices * sizeof(Part)) +
-         round16((size_t)n_lanes * slices_for(vocab) * sizeof(double)) +
-         round16((size_t)n_lanes * sizeof(Verdict));
+static int slices_for(int32_t vocab, int ids) { return (vocab + ids - 1) / ids; }
+// Offsets of the workspace's parts, with `more` slices a row than its ids fill
+// (a row that starts within a line may reach into one more).
+struct Layout {
+  int groups, slices;
+  size_t exact, rest, verdicts, left, all;
+};
+static Layout layout_of(int32_t n_lanes, int32_t t_max, int32_t vocab,
+                        int more) {
+  Layout l;
+  l.groups = slices_for(vocab, kGroup) + more;
+  l.slices = slices_for(vocab, kSlice) + more;
+  l.exact = round16((size_t)n_lanes * 2 * (t_max - 1) * l.groups * sizeof(Part));
+  l.rest = l.exact + round16((size_t)n_lanes * 2 * l.slices * sizeof(Exact));
+  l.verdicts = l.rest + round16((size_t)n_lanes * l.slices * sizeof(double));
+  l.left = l.verdicts + round16((size_t)n_lanes * sizeof(Verdict));
+  l.all = l.left + round16((size_t)n_lanes * sizeof(Left));
+  return l;
 }
 
-// Four slices a workgroup (8 logits a thread each), or one where that would
-// leave most of the CUs without any.
 template <typename T>
 static hipError_t run(const DraftArgs& p, const gdn::LaneTable& tl,
                       hipStream_t st) {
-  const int rows = p.lanes * (p.draft ? 2 * p.t_max - 1 : p.t_max);
-  const long fours = (long)rows * ((p.slices + 3) / 4);
-  const bool few = fours < 256;
-  const int groups = few ? p.slices : (p.slices + 3) / 4;
-  const dim3 grid((unsigned)((long)rows * groups));
-  hipError_t e =
-      few ? launch(sum_kernel<T, 1>, grid, dim3(kThreads), st, p, tl, groups)
-          : launch(sum_kernel<T, 4>, grid, dim3(kThreads), st, p, tl, groups);
-  if (e == hipSuccess && p.draft) {
-    const int parts = (p.rest_slices + kRestSlices - 1) / kRestSlices;
-    e = launch(rest_kernel<T>, dim3((unsigned)((long)p.lanes * parts)),
-               dim3(kWide), st, p, tl, parts);
-  }
+  const int sides = p.draft ? 2 : 1;
+  hipError_t e = hipSuccess;
+  if (p.t_max > 1)
+    e = launch(sum_kernel<T>,
+               dim3((unsigned)((long)p.lanes * (p.t_max - 1) * sides * p.groups)),
+               dim3(kThreads), st, p, tl);
+  if (e == hipSuccess)
+    e = launch(exact_kernel<T>, dim3((unsigned)((long)p.lanes * sides * p.groups)),
+               dim3(kExact), st, p, tl, sides);
+  if (e == hipSuccess && p.draft)
+    e = launch(rest_kernel<T>, dim3((unsigned)((long)p.lanes * p.slices)),
+               dim3(kThreads), st, p, tl);
   if (e != hipSuccess) return e;
-  return launch(pick_kernel<T>, dim3((unsigned)p.lanes), dim3(kWide), st, p, tl);
+  return launch(pick_kernel<T>, dim3((unsigned)p.lanes), dim3(kPick), st, p, tl);
 }
 
 }  // namespace gdnv
@@ -587,7 +670,7 @@ extern "C" size_t gdn_draft_verify_workspace_bytes(int32_t n_lanes,
                                                    int32_t vocab) {
   using namespace gdnv;
   if (!sizes_ok(n_lanes, t_max, vocab)) return 0;
-  return bytes_for(n_lanes, t_max, vocab, slices_for(vocab) + 1);
+  return layout_of(n_lanes, t_max, vocab, 1).all;
 }
 
 extern "C" int gdn_draft_verify(int32_t n_lanes, int32_t t_max,
@@ -632,24 +715,26 @@ extern "C" int gdn_draft_verify(int32_t n_lanes, int32_t t_max,
   if (!any) return GDN_OK;
   DraftArgs p = {logits, t_max > 1 ? draft_logits : nullptr, tokens, uniforms,
                  inv_temperature, m_lane, next_token, accept, row_stride,
-                 draft_stride, n_lanes, t_max, vocab, 0, slices_for(vocab),
+                 draft_stride, n_lanes, t_max, vocab, 0, 0, nullptr, nullptr,
                  nullptr, nullptr, nullptr};
-  // a row that starts within a line may reach into one slice more
   const auto in_lines = [&](const void* x, int64_t stride) {
     return !misaligned(x, 16) && stride * size % 16 == 0;
   };
-  p.slices = slices_for(vocab) +
-             (in_lines(logits, row_stride) &&
-                      (!p.draft || in_lines(p.draft, draft_stride))
-                  ? 0
-                  : 1);
-  if ((double)n_lanes * (2 * t_max - 1) * p.slices > (double)INT_MAX)
+  const Layout l = layout_of(
+      n_lanes, t_max, vocab,
+      in_lines(logits, row_stride) &&
+              (!p.draft || in_lines(p.draft, draft_stride))
+          ? 0
+          : 1);
+  if ((double)n_lanes * 2 * t_max * l.slices > (double)INT_MAX)
     return fail(GDN_EINVAL, "gdn_draft_verify: grid too large");
+  p.groups = l.groups;
+  p.slices = l.slices;
   p.parts = (Part*)workspace;
-  p.rest = (double*)((char*)workspace +
-                     round16((size_t)n_lanes * (2 * t_max - 1) * p.slices * sizeof(Part)));
-  p.verdicts = (Verdict*)((char*)p.rest + round16((size_t)n_lanes * p.rest_slices *
-                                                  sizeof(double)));
+  p.exact = (Exact*)((char*)workspace + l.exact);
+  p.rest = (double*)((char*)workspace + l.rest);
+  p.verdicts = (Verdict*)((char*)workspace + l.verdicts);
+  p.left = (Left*)((char*)workspace + l.left);
   const hipError_t e = in_dtype == GDN_BF16
                            ? run<uint16_t>(p, tl, (hipStream_t)stream)
                            : run<float>(p, tl, (hipStream_t)stream);

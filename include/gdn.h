@@ -722,7 +722,8 @@ int gdn_token_scores(int32_t n_rows, int32_t vocab, int64_t row_stride,
  * inverse temperature is out of range: a draft falls there (accept NaN), and
  * next_token is -1 when it would be sampled there.  Where p - q leaves
  * nothing (p = q to rounding) the token is sampled from p.
- * Exponentials, sums and comparisons are f64.
+ * Chances of drafts are exact to a few steps of f32; the sums that the next
+ * token is looked up in are f64.
  *   workspace   device, 16-byte aligned, ws_bytes >=
  *               gdn_draft_verify_workspace_bytes(...); calls that overlap in
  *               time need workspaces of their own

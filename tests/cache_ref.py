@@ -143,7 +143,7 @@ def usable(it):
 def verify(t_lane, logits, draft, tokens, uniforms, it):
     """Per lane (m, next token, [chances], near): from the definition in f64,
     id by id.  near: a decision lies within what the kernels' rounding may
-    turn (a chance within 1e-10 relative of its uniform, a running sum within
+    turn (a chance within 2^-16 relative of its uniform, a running sum within
     1e-12 of its border)."""
     out = []
     V = logits.shape[2]
@@ -176,7 +176,7 @@ def verify(t_lane, logits, draft, tokens, uniforms, it):
             qw = (float(q[w]) if inside else 1.0) if draft is not None else 1.0
             chances.append(0.0 if pw == 0 else min(1.0, pw / qw) if qw > 0 else 1.0)
             if open_:
-                near |= pw > 0 and abs(u * qw - pw) <= 1e-10 * pw
+                near |= pw > 0 and abs(u * qw - pw) <= 2.0 ** -16 * pw
                 if u * qw < pw:
                     m += 1
                 else:
@@ -209,7 +209,18 @@ def verify(t_lane, logits, draft, tokens, uniforms, it):
     return out
 
 
-def chance_bound():
-    """Relative error of a chance p / q: f64 sums and exponentials (below 1e-10
-    for logits up to a few thousand apart) rounded to f32 once."""
-    return U32 + 1e-10
+def chance_bound(logits, draft, it):
+    """Relative error of a chance p / q whose sums are f32: each side's
+    exponentials are exact to 4 steps plus the rounding of their arguments (at
+    most the spread of the logits that count, 104), 32 are added up a thread
+    and six times two halves, one step each; the chance's own exponentials are
+    f64, and it is rounded once."""
+    spread = 0.0
+    it = torch.where(usable(it), it.cpu(), 0.0)
+    for x in (logits, draft):
+        if x is not None:
+            x = x.double()
+            x = torch.where(torch.isfinite(x), x, 0.0)
+            if x.numel():
+                spread = max(spread, float((x.amax() - x.amin()) * it.max()))
+    return (2 * (4 + 2 * min(spread, 104.0) + 32 + 8) + 1) * U32

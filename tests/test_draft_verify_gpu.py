@@ -58,7 +58,7 @@ def _run(s, stream=None):
 def _check(s, got, at_least=0.9):
     m, token, accept = got
     want = ref.verify(s["t_lane"], s["logits"], s["draft"], s["tokens"], s["uniforms"], s["it"])
-    tol = ref.chance_bound()
+    tol = ref.chance_bound(s["logits"], s["draft"], s["it"])
     sure = 0
     for n, w in enumerate(want):
         if w is None:
@@ -222,6 +222,40 @@ def test_logits_far_apart():
         s["draft"][:, :, ::5] = -big
         s["logits"][1, 0, 1] = big
         _check(s, _run(s), 0.5)
+
+
+@pytest.mark.parametrize("drafted", [False, True])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_greedy_limit_beside_masked_logits(kind, drafted):
+    """Inverse temperatures that leave one token, and -inf beside it: the
+    drafts that are it stand, the next one is it."""
+    s = _case([4, 3, 4, 2], 9000, kind, drafted, right=1.0)
+    out = torch.rand(4, 4, 9000, device="cuda") < 0.5
+    best = s["logits"].float().argmax(2, keepdim=True)
+    out.scatter_(2, best, False)
+    s["logits"].masked_fill_(out, -math.inf)
+    if drafted:
+        s["draft"].masked_fill_(out[:, :-1], -math.inf)
+        s["draft"].scatter_(2, best[:, :-1], 200.0)
+    s["logits"].scatter_(2, best, 100.0)
+    s["it"].copy_(torch.tensor([1e3, 1e8, 1e12, 1e30]))
+    got = _run(s)
+    assert got[0] == s["t_lane"]
+    assert got[1] == [int(best[n, m - 1]) for n, m in enumerate(got[0])]
+    _check(s, got, 0.5)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_a_draft_that_is_all_there_is(kind):
+    """The one token with any probability, drafted: with a uniform of 1 it
+    falls and is sampled again."""
+    s = _case([2, 2], 5000, kind, False)
+    s["logits"].fill_(-math.inf)
+    s["logits"][:, :, 77] = 1.0
+    s["tokens"][:, 1] = 77
+    s["uniforms"][0, 0], s["uniforms"][1, 0] = 1.0, 0.99
+    m, token, accept = _run(s)
+    assert (m, token) == ([1, 2], [77, 77]) and (accept[:, 0] == 1).all()
 
 
 @pytest.mark.parametrize("drafted", [False, True])
