@@ -950,7 +950,8 @@ static size_t attend_bytes(const gdn_kv_dims& d) {
   return slot_bytes(d, shape_of(d, 2));
 }
 
-template <int D>
+// MOST: waves that join one row where there are few rows and many splits.
+template <int D, int MOST = 16>
 static hipError_t join(const gdn_kv_dims& d, const Shape& s,
                        const AttendArgs& p, const gdn::LaneTable& tl,
                        hipStream_t st) {
@@ -962,7 +963,7 @@ static hipError_t join(const gdn_kv_dims& d, const Shape& s,
     return launch(join_kernel<D, 1, kFewBlocks>, rows, dim3(64), st, p, tl);
   if (units <= kFewSplits || s.target <= kFewSplits)
     return launch(join_kernel<D, 4, kFewSplits>, rows, dim3(256), st, p, tl);
-  return launch(join_kernel<D, 16, kFewBlocks>, rows, dim3(1024), st, p, tl);
+  return launch(join_kernel<D, MOST, kFewBlocks>, rows, dim3(64 * MOST), st, p, tl);
 }
 
 template <int D, typename T>

@@ -120,6 +120,41 @@ struct Query {
   }
 };
 
+// bf16 rows that lie in LDS and are read as they are needed: where eight waves
+// share a tile, 128 registers a lane have no room for them (with 16 spilled
+// ones 8 lanes x 16 windows over 16k took 81 us instead of 77).
+template <int D>
+struct QueryLds {
+  const uint16_t* rows;  // this wave's 16
+  static __device__ __forceinline__ int at(int r, int p) {
+    // 16 rows' piece p lie apart
+    return r * D + (p ^ (D == 64 ? r >> 1 & 7 : r & 15)) * 8;
+  }
+  __device__ __forceinline__ void load(uint16_t* to, const uint16_t* row,
+                                       uint32_t flip, bool zero) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    Query<D, uint16_t> q;
+    q.load(row, flip, zero);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+      *reinterpret_cast<u32x4*>(to + at(n, D / 32 * g + i)) = q.q[i];
+    rows = to;
+  }
+  __device__ __forceinline__ void scores(const Own<D> (&k)[2],
+                                         f32x4 (&c)[2]) const {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    typedef Op<uint16_t> O;
+    asm volatile("" ::: "memory");  // (not kept from one use to the next)
+    c[0] = c[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const u32x4 q = *reinterpret_cast<const u32x4*>(rows + at(n, D / 32 * g + i));
+      c[0] = O::mul(k[0].values(i), q, c[0]);
+      c[1] = O::mul(k[1].values(i), q, c[1]);
+    }
+  }
+};
+
 // The row of q at row `row` of key-value head hk.
 template <int D, typename T>
 __device__ __forceinline__ const T* query_row(const AttendArgs& p, int lane,
@@ -298,6 +333,15 @@ __device__ __forceinline__ uint32_t cache_row(const KvArgs& a, int page, int h,
 // a step, and lane 16 g + n holds its channels of positions n and 16 + n.
 // EVEN: pages are multiples of 16 positions, so that each half of a step lies
 // in one page, whose number and place are the wave's and not the lanes'.
+//
+// A cache of this kind is read once, 17 bytes for 32 channels, so memory is
+// what bounds it: 32 lanes of up to 32k positions, 8 heads of 128 under four
+// queries each, take 177 us, 5.0 TB/s, where the loads alone take 164.  The
+// loads of a step are given out a whole step ahead, each into the registers
+// that the step in hand has just used up; with a branch around the last ones
+// it was 200 us.  A short cache is bound by one workgroup's chain of look-up,
+// loads, products and sums: 8 lanes of up to 1k positions 8.6 us and 4.3 for
+// the join.
 template <int D, typename T, int RT, bool EVEN>
 __global__ __launch_bounds__(256, (few4_waves<D, T, RT>())) void attend4_kernel(
     Attend4Args q, gdn::LaneTable tl) {
@@ -441,8 +485,15 @@ __global__ __launch_bounds__(256, (few4_waves<D, T, RT>())) void attend4_kernel(
 
 // Many rows, as rows_kernel: NW waves take 16 rows each of the same tile of
 // 64 positions, whose K lies in LDS as it is in the cache and whose V is
-// widened once for all of them.  Two tiles take turns, so that one barrier a
-// tile is enough.
+// widened once for all of them.
+//
+// Vector instructions bound it: to widen K once per wave and to cut each
+// probability into the three bf16 parts that hold its 24 bits.  8 lanes x 16
+// tokens x 32 heads of 128 over up to 16k positions: 75 us, the vector units
+// busy 68 % of it, the matrix units 35 % (four products a score, one for K
+// and three for V), LDS 26 %.  With two tiles in turn and one barrier each it
+// was 78, the registers for it spilled; with K widened once for all waves, as
+// V is, 84, bound by the reads from LDS.
 template <int D, typename T, int NW>
 __global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW>())) void rows4_kernel(
     Attend4Args q, gdn::LaneTable tl) {
@@ -452,10 +503,12 @@ __global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW>())) void rows4_kern
   constexpr int kPieces = kTile * kBlocks;                    // of K, or of V
   constexpr int kThreads = 64 * NW;
   constexpr int kN = (kPieces + kThreads - 1) / kThreads;     // of a thread
-  __shared__ __attribute__((aligned(16))) u32x4 Kc[2][kPieces];
-  __shared__ uint8_t Ks[2][kPieces];
-  __shared__ __attribute__((aligned(16))) uint16_t Vs[2][kTile * D];
-  __shared__ int odd_first[3][kBlocks];  // of a tile's rows, by block; kTile: none
+  __shared__ __attribute__((aligned(16))) u32x4 Kc[kPieces];
+  __shared__ uint8_t Ks[kPieces];
+  __shared__ __attribute__((aligned(16))) uint16_t Vs[kTile * D];
+  constexpr bool kLds = sizeof(T) == 2 && NW == 8;
+  __shared__ __attribute__((aligned(16))) uint16_t Qs[kLds ? kRows * D : 8];
+  __shared__ int odd_first[2][kBlocks];  // of a tile's rows, by block; kTile: none
   const AttendArgs& p = q.at;
   const KvArgs& a = p.kv;
   const int per_item = a.h_kv * p.groups;
@@ -508,64 +561,49 @@ __global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW>())) void rows4_kern
     return r * kBlocks + (b ^ (r / (16 / kBlocks)) % kBlocks);
   };
   auto put = [&](int tile, uint64_t here) {
-    const int buf = tile & 1;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int r = piece_of(i) / kBlocks, b = piece_of(i) % kBlocks;
       const bool is_there = here >> r & 1, off = vs[i] >= kScaleOdd;
-      if (is_there && off) atomicMin(&odd_first[tile % 3][b], r);
+      if (is_there && off) atomicMin(&odd_first[tile & 1][b], r);
       if (!is_there || off) {
         vr[i] = u32x4{0, 0, 0, 0};
         vs[i] = 0;
       }
-      Kc[buf][spot(r, b)] = kr[i];
-      Ks[buf][spot(r, b)] = (uint8_t)(ks[i] >= kScaleOdd ? kScaleNan : ks[i]);
+      Kc[spot(r, b)] = kr[i];
+      Ks[spot(r, b)] = (uint8_t)(ks[i] >= kScaleOdd ? kScaleNan : ks[i]);
 #pragma unroll
       for (int y = 0; y < 4; ++y)
-        *reinterpret_cast<u32x4*>(Vs[buf] + VL::at(r, 4 * b + y)) =
+        *reinterpret_cast<u32x4*>(Vs + VL::at(r, 4 * b + y)) =
             fp4_values(vr[i][y], vs[i]);
     }
   };
-  if (tid < 3 * kBlocks) odd_first[tid / kBlocks][tid % kBlocks] = kTile;
-  uint64_t here = 0;
-  if (tiles > 0) {
-    look_up(0);
-    place(0);
-    fetch();
-    look_up(1);
-  }
+  if (tid < 2 * kBlocks) odd_first[tid / kBlocks][tid % kBlocks] = kTile;
+  // (past the last tile, loads of the cache's first row, as in attend4_kernel)
+  look_up(0);
+  place(0);
+  fetch();
+  look_up(1);
   R x;
   x.init(row0 + 16 * wave, rows, s.len, T_n, group);
-  Query<D, T> query;
+  std::conditional_t<kLds, QueryLds<D>, Query<D, T>> query;
   {
     const int row = row0 + 16 * wave + n;
-    query.load(query_row<D, T>(p, s.lane, hk, row < rows ? row : 0), q.flip, row >= rows);
-  }
-  __syncthreads();
-  if (tiles > 0) {
-    here = ok;
-    put(0, here);
-    if (tiles > 1) {
-      place(1);
-      fetch();
-      look_up(2);
-    }
+    const T* src = query_row<D, T>(p, s.lane, hk, row < rows ? row : 0);
+    if constexpr (kLds) query.load(Qs + 16 * wave * D, src, q.flip, row >= rows);
+    else query.load(src, q.flip, row >= rows);
   }
   for (int tile = 0; tile < tiles; ++tile) {
-    const int t0 = begin + tile * kTile, buf = tile & 1;
-    const uint64_t now = here;
-    const bool whole = t0 + kTile <= (open < stop ? open : stop) && now == ~0ull;
-    __syncthreads();  // this tile is there, and the one before has been read
-    if (tid < kBlocks) odd_first[(tile + 2) % 3][tid] = kTile;
-    if (tile + 1 < tiles) {
-      here = ok;
-      put(tile + 1, here);
-      if (tile + 2 < tiles) {
-        place(tile + 2);
-        fetch();
-        look_up(tile + 3);
-      }
-    }
+    const int t0 = begin + tile * kTile;
+    const uint64_t here = ok;
+    const bool whole = t0 + kTile <= (open < stop ? open : stop) && here == ~0ull;
+    __syncthreads();  // the tile before has been read
+    put(tile, here);
+    place(tile + 1);
+    fetch();
+    look_up(tile + 2);
+    __syncthreads();
+    if (tid < kBlocks) odd_first[~tile & 1][tid] = kTile;
     if (row0 + 16 * wave >= rows) continue;
 #pragma unroll 1
     for (int half = 0; half < kTile / 32; ++half) {
@@ -575,29 +613,29 @@ __global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW>())) void rows4_kern
         const int r = 32 * half + 16 * h + n;
         if constexpr (D == 64) {
           const int w = spot(r, g4 >> 1);
-          const uint2 y = reinterpret_cast<const uint2*>(&Kc[buf][w])[g4 & 1];
+          const uint2 y = reinterpret_cast<const uint2*>(&Kc[w])[g4 & 1];
           k[h].codes[0] = y.x;
           k[h].codes[1] = y.y;
-          k[h].scale[0] = Ks[buf][w];
+          k[h].scale[0] = Ks[w];
         } else {
 #pragma unroll
           for (int y = 0; y < D / 128; ++y) {
             const int w = spot(r, D / 128 * g4 + y);
-            const u32x4 c = Kc[buf][w];
+            const u32x4 c = Kc[w];
 #pragma unroll
             for (int i = 0; i < 4; ++i) k[h].codes[4 * y + i] = c[i];
-            k[h].scale[y] = Ks[buf][w];
+            k[h].scale[y] = Ks[w];
           }
         }
       }
       query.scores(k, x.sc[0]);
       const int p0 = t0 + 32 * half;
-      x.softmax(p.scale, whole, (uint32_t)(now >> (32 * half)), p0);
-      x.values(Vs[buf], 32 * half);
+      x.softmax(p.scale, whole, (uint32_t)(here >> (32 * half)), p0);
+      x.values(Vs, 32 * half);
     }
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
-      const int first = gdn::uniform(odd_first[tile % 3][b]);
+      const int first = gdn::uniform(odd_first[tile & 1][b]);
       if (first < kTile) mark_odd(x, b, t0 + first);
     }
   }
@@ -612,7 +650,17 @@ __global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW>())) void rows4_kern
 }
 
 // ---------------------------------------------------------------- host side
+// Workgroups of a launch, as kFewBlocks and kRowsBlocks of the wider cache.
+// 32 lanes of up to 32k, 8 heads of 128: 280, 198, 197, 176, 177 us with 512,
+// 768, 1024, 1536, 2048; f32 queries, 13 lanes of up to 10k, 3 heads of 64:
+// 14.4, 14.5, 14.8, 16.0, 15.7; 8 lanes of up to 1k have fewer splits than any
+// of these.  Windows of 16, 8 lanes of up to 16k: 88 and 7 us (the join) with
+// 256, 76 and 9 with 512, 87 and 11 with 768, 86 and 13 with 1024.
 constexpr int kFew4Blocks = 2048, kRows4Blocks = 512;
+// From this many rows on four waves join a row that may have many splits: 585
+// rows of up to 79 splits take 4.7 us, and 8.6 with the 16 waves that a few
+// rows of many splits need.
+constexpr long kFewRows = 256;
 
 static Shape shape4_of(const gdn_kv_dims& d) {
   return shape_of(d, kFew4Blocks, kRows4Blocks);
@@ -646,7 +694,9 @@ static hipError_t attend4(const gdn_kv_dims& d, const Shape& s,
   } else {
     e = few4<D, T, 1>(d, grid, p, tl, st);
   }
-  return e != hipSuccess ? e : join<D>(d, s, p.at, tl, st);
+  if (e != hipSuccess) return e;
+  return (long)d.n_lanes * d.h_kv * s.rows >= kFewRows ? join<D, 4>(d, s, p.at, tl, st)
+                                                       : join<D>(d, s, p.at, tl, st);
 }
 
 template <typename T>
