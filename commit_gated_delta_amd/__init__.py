@@ -682,9 +682,9 @@ def _fp4_cache(dims, k_codes, k_scales, v_codes, v_scales, dev):
 
 
 def rope_append_mxfp(dims: KvDims, t_lane, q, k, v, inv_freq, rot_dim, q_out,
-                    k_codes, k_scales, v_codes, v_scales, page_table, kv_len,
-                    k_held=None, v_held=None, positions=None,
-                    interleaved=False, stream=None, raw_status=False):
+                     k_codes, k_scales, v_codes, v_scales, page_table, kv_len,
+                     k_held=None, v_held=None, positions=None,
+                     interleaved=False, stream=None, raw_status=False):
     """gdn_rope_append_mxfp on torch tensors."""
     n, dev = dims.n_lanes, torch.cuda.current_device()
     lanes = _lane_ints(t_lane, n)
@@ -708,8 +708,8 @@ def paged_attention_mxfp_workspace_bytes(dims: KvDims) -> int:
 
 
 def paged_attention_mxfp(dims: KvDims, t_lane, q, k_codes, k_scales, v_codes,
-                        v_scales, page_table, kv_len, o, workspace, scale=1.0,
-                        stream=None, raw_status=False):
+                         v_scales, page_table, kv_len, o, workspace, scale=1.0,
+                         stream=None, raw_status=False):
     """gdn_paged_attention_mxfp on torch tensors."""
     n, kind = dims.n_lanes, q.dtype
     lanes, code, dev = _lane_ints(t_lane, n), _code(kind), torch.cuda.current_device()
