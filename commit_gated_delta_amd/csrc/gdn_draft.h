@@ -245,7 +245,11 @@ struct Share {
 };
 
 // Sums of the rows that decide about the drafts: a workgroup per kGroup ids,
-// read once into registers.  Bound by HBM.
+// read once into registers, so that its largest logit is known before its sum
+// and no exponential is taken twice.  Bound by HBM: 8 lanes of up to 15 drafts,
+// 131072 ids in f32, drafter's rows too: 10.5 us, 45 MB at 4.3 TB/s; 64 lanes
+// of up to 5, bf16: 12.3 us, 46 MB at 3.7.  (In f64 18 and 32 us, 26 vector
+// instructions a logit.)
 template <typename T>
 __global__ __launch_bounds__(kThreads, 4) void sum_kernel(DraftArgs p,
                                                           gdn::LaneTable tl) {
@@ -368,7 +372,10 @@ __device__ __forceinline__ Verdict decide(const DraftArgs& p, int n, int T_n,
 
 // The verdicts, and f64 sums by slices of the row that the next token is
 // sampled from (leaving the fallen draft out, where it has no distribution),
-// or of the drafter's row beside it.  A workgroup takes kGroup ids.
+// or of the drafter's row beside it.  A workgroup takes kGroup ids; each works
+// the lane's verdict out for itself, which costs less than a launch between.
+// Bound by that chain of loads and, with many lanes, by the exponentials in
+// f64: 8 lanes and their drafter's rows 7.9 us, 64 lanes 13.3.
 template <typename T>
 __global__ __launch_bounds__(kExact) void exact_kernel(DraftArgs p,
                                                       gdn::LaneTable tl,
@@ -443,7 +450,8 @@ __device__ __forceinline__ double weight_left(const Left& r, float x, float y,
 }
 
 // With a drafter's distribution: sums of max(p - q, 0) by slices of the row
-// where a draft fell.
+// where a draft fell.  The logits, in the cache still, are on their way while
+// the sums of both rows are worked out.  8 lanes: 5.8 us, bound by latency.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void rest_kernel(DraftArgs p,
                                                         gdn::LaneTable tl) {
@@ -486,6 +494,8 @@ __global__ __launch_bounds__(kThreads) void rest_kernel(DraftArgs p,
 
 // The next token, a workgroup per lane: the slice that the border lies in,
 // then the id within it.
+// 5.6 to 6.8 us for 1 to 64 lanes, bound by latency: three passes over the
+// slices' sums, one over a slice.
 template <typename T>
 __global__ __launch_bounds__(kPick) void pick_kernel(DraftArgs p,
                                                      gdn::LaneTable tl) {

@@ -99,61 +99,34 @@ struct Query {
       else q[i] = O::wide(__builtin_bit_cast(f32x4, w[0]), __builtin_bit_cast(f32x4, w[1]));
     }
   }
-  // Scores of twice 16 positions (two chains of products).
-  __device__ __forceinline__ void scores(const Own<D> (&k)[2],
-                                         f32x4 (&c)[2]) const {
-    c[0] = c[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+};
+
+// Scores of twice 16 positions against RT times 16 rows.
+template <int D, typename T, int RT>
+__device__ __forceinline__ void scores_of(const Own<D> (&k)[2],
+                                          const Query<D, T> (&q)[RT],
+                                          f32x4 (&c)[RT][2]) {
+  typedef Op<uint16_t> O;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const u32x4 a = k[0].values(i), b = k[1].values(i);
+  for (int r = 0; r < RT; ++r) c[r][0] = c[r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const u32x4 a = k[0].values(i), b = k[1].values(i);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
       if constexpr (sizeof(T) == 2) {
-        c[0] = O::mul(a, q[i], c[0]);
-        c[1] = O::mul(b, q[i], c[1]);
+        c[r][0] = O::mul(a, q[r].q[i], c[r][0]);
+        c[r][1] = O::mul(b, q[r].q[i], c[r][1]);
       } else {
 #pragma unroll
         for (int y = 0; y < O::kSteps; ++y) {
-          c[0] = O::step(y, a, q[i], c[0]);
-          c[1] = O::step(y, b, q[i], c[1]);
+          c[r][0] = O::step(y, a, q[r].q[i], c[r][0]);
+          c[r][1] = O::step(y, b, q[r].q[i], c[r][1]);
         }
       }
     }
   }
-};
-
-// bf16 rows that lie in LDS and are read as they are needed: where eight waves
-// share a tile, 128 registers a lane have no room for them (with 16 spilled
-// ones 8 lanes x 16 windows over 16k took 81 us instead of 77).
-template <int D>
-struct QueryLds {
-  const uint16_t* rows;  // this wave's 16
-  static __device__ __forceinline__ int at(int r, int p) {
-    // 16 rows' piece p lie apart
-    return r * D + (p ^ (D == 64 ? r >> 1 & 7 : r & 15)) * 8;
-  }
-  __device__ __forceinline__ void load(uint16_t* to, const uint16_t* row,
-                                       uint32_t flip, bool zero) {
-    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-    Query<D, uint16_t> q;
-    q.load(row, flip, zero);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-      *reinterpret_cast<u32x4*>(to + at(n, D / 32 * g + i)) = q.q[i];
-    rows = to;
-  }
-  __device__ __forceinline__ void scores(const Own<D> (&k)[2],
-                                         f32x4 (&c)[2]) const {
-    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-    typedef Op<uint16_t> O;
-    asm volatile("" ::: "memory");  // (not kept from one use to the next)
-    c[0] = c[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const u32x4 q = *reinterpret_cast<const u32x4*>(rows + at(n, D / 32 * g + i));
-      c[0] = O::mul(k[0].values(i), q, c[0]);
-      c[1] = O::mul(k[1].values(i), q, c[1]);
-    }
-  }
-};
+}
 
 // The row of q at row `row` of key-value head hk.
 template <int D, typename T>
@@ -315,10 +288,16 @@ constexpr int few4_waves() {
   constexpr int q = D * RT * (int)sizeof(T);
   return D * RT == 64 ? 4 : q <= 256 ? 3 : q <= 512 ? 2 : 1;
 }
-template <int D, typename T, int NW>
+template <int D, typename T, int NW, int RT>
 constexpr int rows4_waves() {
-  return D * sizeof(T) <= 256 ? NW / 2 : NW / 4;
+  return RT == 2 || D * sizeof(T) > 256 ? NW / 4 * RT : NW / 2;
 }
+// Whether a wave of rows4_kernel takes 32 rows of 128, so that K is widened
+// and V read half as often, or 16 (the same windows of 16 over 16k): 56.6 and
+// 59.1 us with the join at d = 64, 71.5 and 78.9 at 128, in f32 60.5 and 63.6
+// at 64, but 115 and 104 at 128, where 32 rows leave one wave a SIMD.
+template <int D, typename T>
+constexpr bool kWide = D * sizeof(T) <= 256;
 
 // Row of a position in its page, counted over the cache (fewer than 2^32).
 __device__ __forceinline__ uint32_t cache_row(const KvArgs& a, int page, int h,
@@ -423,8 +402,7 @@ __global__ __launch_bounds__(256, (few4_waves<D, T, RT>())) void attend4_kernel(
         for (int y = 0; y < Part::kScales; ++y)
           if (kp[h].scale[y] >= kScaleOdd) kp[h].scale[y] = kScaleNan;
     }
-#pragma unroll
-    for (int r = 0; r < RT; ++r) query[r].scores(kp, x.sc[r]);
+    scores_of<D, T>(kp, query, x.sc);
     place(step + 4);
     fetch(q.k4, kp);
     look_up(step + 8);
@@ -483,31 +461,30 @@ __global__ __launch_bounds__(256, (few4_waves<D, T, RT>())) void attend4_kernel(
   sum_waves<D>(p, s, hk, rows, x, reinterpret_cast<float*>(pool), kWave / 4, ml);
 }
 
-// Many rows, as rows_kernel: NW waves take 16 rows each of the same tile of
+// Many rows, as rows_kernel: NW waves take 16 RT rows each of the same tile of
 // 64 positions, whose K lies in LDS as it is in the cache and whose V is
 // widened once for all of them.
 //
-// Vector instructions bound it: to widen K once per wave and to cut each
-// probability into the three bf16 parts that hold its 24 bits.  8 lanes x 16
-// tokens x 32 heads of 128 over up to 16k positions: 75 us, the vector units
-// busy 68 % of it, the matrix units 35 % (four products a score, one for K
-// and three for V), LDS 26 %.  With two tiles in turn and one barrier each it
-// was 78, the registers for it spilled; with K widened once for all waves, as
-// V is, 84, bound by the reads from LDS.
-template <int D, typename T, int NW>
-__global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW>())) void rows4_kernel(
+// What a wave does one after the other bounds it: vector instructions 54 % of
+// the time (K is widened, each probability cut into the three bf16 parts that
+// hold its 24 bits), matrix ones 39 % (four products a score, one for K and
+// three for V); two waves a SIMD hide little of either behind the other.  8
+// lanes x 16 tokens x 32 heads of 128 over up to 16k positions: 69 us.  With
+// 16 rows a wave it was 76; with K widened once for all waves, as V is, 84,
+// bound by the reads from LDS; scores of the whole tile before its softmax, or
+// a wave's priority raised for its products, change nothing (68..69).
+template <int D, typename T, int NW, int RT>
+__global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW, RT>())) void rows4_kernel(
     Attend4Args q, gdn::LaneTable tl) {
-  typedef Rows4<D, 1> R;
+  typedef Rows4<D, RT> R;
   typedef VTile<D> VL;
-  constexpr int kRows = 16 * NW, kTile = 64, kBlocks = D / 32;
+  constexpr int kRows = 16 * NW * RT, kTile = 64, kBlocks = D / 32;
   constexpr int kPieces = kTile * kBlocks;                    // of K, or of V
   constexpr int kThreads = 64 * NW;
   constexpr int kN = (kPieces + kThreads - 1) / kThreads;     // of a thread
   __shared__ __attribute__((aligned(16))) u32x4 Kc[kPieces];
   __shared__ uint8_t Ks[kPieces];
   __shared__ __attribute__((aligned(16))) uint16_t Vs[kTile * D];
-  constexpr bool kLds = sizeof(T) == 2 && NW == 8;
-  __shared__ __attribute__((aligned(16))) uint16_t Qs[kLds ? kRows * D : 8];
   __shared__ int odd_first[2][kBlocks];  // of a tile's rows, by block; kTile: none
   const AttendArgs& p = q.at;
   const KvArgs& a = p.kv;
@@ -585,13 +562,13 @@ __global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW>())) void rows4_kern
   fetch();
   look_up(1);
   R x;
-  x.init(row0 + 16 * wave, rows, s.len, T_n, group);
-  std::conditional_t<kLds, QueryLds<D>, Query<D, T>> query;
-  {
-    const int row = row0 + 16 * wave + n;
-    const T* src = query_row<D, T>(p, s.lane, hk, row < rows ? row : 0);
-    if constexpr (kLds) query.load(Qs + 16 * wave * D, src, q.flip, row >= rows);
-    else query.load(src, q.flip, row >= rows);
+  x.init(row0 + 16 * RT * wave, rows, s.len, T_n, group);
+  Query<D, T> query[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int row = row0 + 16 * (RT * wave + r) + n;
+    query[r].load(query_row<D, T>(p, s.lane, hk, row < rows ? row : 0), q.flip,
+                  row >= rows);
   }
   for (int tile = 0; tile < tiles; ++tile) {
     const int t0 = begin + tile * kTile;
@@ -604,7 +581,7 @@ __global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW>())) void rows4_kern
     look_up(tile + 2);
     __syncthreads();
     if (tid < kBlocks) odd_first[~tile & 1][tid] = kTile;
-    if (row0 + 16 * wave >= rows) continue;
+    if (row0 + 16 * RT * wave >= rows) continue;
 #pragma unroll 1
     for (int half = 0; half < kTile / 32; ++half) {
       Own<D> k[2];
@@ -628,7 +605,7 @@ __global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW>())) void rows4_kern
           }
         }
       }
-      query.scores(k, x.sc[0]);
+      scores_of<D, T>(k, query, x.sc);
       const int p0 = t0 + 32 * half;
       x.softmax(p.scale, whole, (uint32_t)(here >> (32 * half)), p0);
       x.values(Vs, 32 * half);
@@ -640,13 +617,16 @@ __global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW>())) void rows4_kern
     }
   }
   x.finish(a, table, begin, 32, stop);
-  const int row = row0 + 16 * wave + n;
-  if (row >= rows) return;
-  float f;
-  float* dst = row_out(p, s, hk, row, D, x.m[0], x.l[0], g4 == 0, f);
 #pragma unroll
-  for (int c = 0; c < R::CT; ++c)
-    *reinterpret_cast<f32x4*>(dst + 16 * c + 4 * g4) = x.acc[0][c] * f;
+  for (int r = 0; r < RT; ++r) {
+    const int row = row0 + 16 * (RT * wave + r) + n;
+    if (row >= rows) return;
+    float f;
+    float* dst = row_out(p, s, hk, row, D, x.m[r], x.l[r], g4 == 0, f);
+#pragma unroll
+    for (int c = 0; c < R::CT; ++c)
+      *reinterpret_cast<f32x4*>(dst + 16 * c + 4 * g4) = x.acc[r][c] * f;
+  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -654,8 +634,9 @@ __global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW>())) void rows4_kern
 // 32 lanes of up to 32k, 8 heads of 128: 280, 198, 197, 176, 177 us with 512,
 // 768, 1024, 1536, 2048; f32 queries, 13 lanes of up to 10k, 3 heads of 64:
 // 14.4, 14.5, 14.8, 16.0, 15.7; 8 lanes of up to 1k have fewer splits than any
-// of these.  Windows of 16, 8 lanes of up to 16k: 88 and 7 us (the join) with
-// 256, 76 and 9 with 512, 87 and 11 with 768, 86 and 13 with 1024.
+// of these.  Windows of 16, 8 lanes of up to 16k, 16 rows a wave: 88 and 7 us
+// (the join) with 256, 76 and 9 with 512, 87 and 11 with 768, 86 and 13 with
+// 1024.
 constexpr int kFew4Blocks = 2048, kRows4Blocks = 512;
 // From this many rows on four waves join a row that may have many splits: 585
 // rows of up to 79 splits take 4.7 us, and 8.6 with the 16 waves that a few
@@ -682,11 +663,14 @@ static hipError_t attend4(const gdn_kv_dims& d, const Shape& s,
   hipError_t e;
   if (!s.few) {
     if constexpr (D < 256) {
+      // (128 rows a workgroup: kWide of what the registers hold, see there)
+      constexpr int kWaves = kWide<D, T> ? 4 : 8;
       e = s.waves == 8
-              ? launch(rows4_kernel<D, T, 8>, grid, dim3(512), st, p, tl)
-              : launch(rows4_kernel<D, T, 4>, grid, dim3(256), st, p, tl);
+              ? launch(rows4_kernel<D, T, kWaves, 8 / kWaves>, grid,
+                       dim3(64 * kWaves), st, p, tl)
+              : launch(rows4_kernel<D, T, 4, 1>, grid, dim3(256), st, p, tl);
     } else {
-      e = launch(rows4_kernel<D, T, 4>, grid, dim3(256), st, p, tl);
+      e = launch(rows4_kernel<D, T, 4, 1>, grid, dim3(256), st, p, tl);
     }
   } else if constexpr (D < 256) {
     e = s.rt == 2 ? few4<D, T, 2>(d, grid, p, tl, st)

@@ -8,6 +8,15 @@
 // p f_i has at most 31 + 24 significant bits, so its product in f64 is exact
 // to half a step, and it is reduced to a fraction of a turn there: the angle
 // is as good at the far end of a long cache as at its start.
+//
+// Every row is read and written once; memory bounds a large call, the launch
+// and what the caller does for it a small one (3.3 us of kernel for 8 lanes
+// of one token, 18 heads of 256; 4.2 into 4 bits).  128 lanes x 64 tokens, 48
+// heads of 128, bf16: 46 us, 201 MB at 4.4 TB/s, a large copy runs at 4.8; the
+// same into 4 bits, the decoded rows written as well: 46 us, 211 MB at 4.6.
+// What it took: a thread that turns one head works out eight angles in f64
+// for it, 102 and 107 us; with the angles kept for the same channels of
+// several heads (see slots_for) they cost nothing.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -369,7 +378,9 @@ static int check_rope(const char* fn, const gdn_kv_dims* dims,
 }
 
 // Slots of heads for a token's `units` threads each: as many as bring the call
-// to about kEnough threads, the fewest heads a thread.
+// to about kEnough threads (four rounds of 256 a CU), the fewest heads a thread:
+// a small call has no work to spare for threads with many heads, a large one
+// none for angles worked out again.
 constexpr long kEnough = 256 * 1024;
 static int slots_for(long tokens, int units, int heads) {
   const long n = (kEnough + tokens * units - 1) / (tokens * units);
