@@ -106,6 +106,12 @@ def test_attention(t_lane, lens, h_q, h_kv, d, page, kind):
     ([1] * 18, [200] * 17 + [9000], 64, 2, 128, "bf16"),
     ([16], [7001], 8, 1, 128, "bf16"),
     ([9, 2], [5000, 2600], 16, 1, 256, "f32"),
+    ([1] * 10, [20000] + [30] * 9, 32, 1, 64, "bf16"),   # and of some hundred
+    ([1] * 10, [9999] + [300] * 9, 32, 1, 128, "f32"),
+    ([1] * 20, [9001] + [30] * 19, 16, 1, 256, "bf16"),
+    ([17, 9], [3001, 700], 5, 1, 128, "bf16"),           # rows past a wave's last
+    ([23, 3], [2500, 70], 3, 1, 64, "f32"),
+    ([22, 30], [900, 2100], 3, 1, 128, "f32"),
 ])
 def test_many_splits(t_lane, lens, h_q, h_kv, d, kind):
     x = _case(t_lane, lens, h_q, h_kv, d, 64, kind)
