@@ -247,9 +247,9 @@ struct Share {
 // Sums of the rows that decide about the drafts: a workgroup per kGroup ids,
 // read once into registers, so that its largest logit is known before its sum
 // and no exponential is taken twice.  Bound by HBM: 8 lanes of up to 15 drafts,
-// 131072 ids in f32, drafter's rows too: 10.5 us, 45 MB at 4.3 TB/s; 64 lanes
-// of up to 5, bf16: 12.3 us, 46 MB at 3.7.  (In f64 18 and 32 us, 26 vector
-// instructions a logit.)
+// 131072 ids in f32, drafter's rows too: 10.4 us, 45 MB at 4.3 TB/s; 64 lanes
+// of up to 5, bf16: 11.6 us, 46 MB at 4.0, the vector units nearly full.
+// (In f64 18 and 32 us, 26 vector instructions a logit.)
 template <typename T>
 __global__ __launch_bounds__(kThreads, 4) void sum_kernel(DraftArgs p,
                                                           gdn::LaneTable tl) {
@@ -270,16 +270,18 @@ __global__ __launch_bounds__(kThreads, 4) void sum_kernel(DraftArgs p,
   if (lane == 0) tops[wave] = m;
   __syncthreads();
   m = nan_max(nan_max(tops[0], tops[1]), nan_max(tops[2], tops[3]));
-  // c in two parts: rounded to one it would tilt the exponents of far logits
+  // c in two parts: rounded to one it would tilt the exponents of far logits.
+  // Both are positive, so that a logit of -inf stays one.
   const float ref = m == -INFINITY ? 0.f : m;
-  const float hi = (float)c, lo = (float)(c - (double)hi);
-  const float far = -512.f / hi;  // (2^-512 is 0; a -inf is cut off there)
+  float hi = (float)c;
+  if ((double)hi > c) hi = __uint_as_float(__float_as_uint(hi) - 1);
+  const float lo = fmaxf((float)(c - (double)hi), 1.17549435e-38f);
   float z = 0.f;
 #pragma unroll
   for (int k = 0; k < s.V; ++k)
 #pragma unroll
     for (int e = 0; e < s.E; ++e) {
-      const float d = nan_max(s.x[k][e] - ref, far);
+      const float d = s.x[k][e] - ref;
       z += __builtin_amdgcn_exp2f(__builtin_fmaf(d, hi, d * lo));
     }
   z = gdn::wave_sum(z);
@@ -736,7 +738,12 @@ extern "C" int gdn_draft_verify(int32_t n_lanes, int32_t t_max,
               (!p.draft || in_lines(p.draft, draft_stride))
           ? 0
           : 1);
-  if ((double)n_lanes * 2 * t_max * l.slices > (double)INT_MAX)
+  // threads of the largest launch (of sum_kernel, exact_kernel, rest_kernel)
+  const double groups = (double)n_lanes * (p.draft ? 2 : 1) * l.groups;
+  const double threads = fmax(fmax(groups * (t_max - 1) * kThreads, groups * kExact),
+                              (double)n_lanes * l.slices * kThreads);
+  if (threads > (double)UINT32_MAX ||
+      (double)n_lanes * 2 * t_max * l.slices > (double)INT_MAX)
     return fail(GDN_EINVAL, "gdn_draft_verify: grid too large");
   p.groups = l.groups;
   p.slices = l.slices;

@@ -629,14 +629,14 @@ int gdn_rope_append(const gdn_kv_dims* dims, const int32_t* t_lane,
  * aligned.
  */
 int gdn_rope_append_mxfp(const gdn_kv_dims* dims, const int32_t* t_lane,
-                        const void* q, int64_t q_stride, const void* k,
-                        int64_t k_stride, const void* v, int64_t v_stride,
-                        int dtype, const float* inv_freq, int32_t rot_dim,
-                        const int32_t* positions, void* q_out,
-                        uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
-                        uint8_t* v_scales, const int32_t* page_table,
-                        const int32_t* kv_len, void* k_held, void* v_held,
-                        int flags, void* stream);
+                         const void* q, int64_t q_stride, const void* k,
+                         int64_t k_stride, const void* v, int64_t v_stride,
+                         int dtype, const float* inv_freq, int32_t rot_dim,
+                         const int32_t* positions, void* q_out,
+                         uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
+                         uint8_t* v_scales, const int32_t* page_table,
+                         const int32_t* kv_len, void* k_held, void* v_held,
+                         int flags, void* stream);
 
 /*
  * gdn_paged_attention over that cache (or any in its layout: scale byte 0 is
@@ -649,11 +649,11 @@ int gdn_rope_append_mxfp(const gdn_kv_dims* dims, const int32_t* t_lane,
  */
 size_t gdn_paged_attention_mxfp_workspace_bytes(const gdn_kv_dims* dims);
 int gdn_paged_attention_mxfp(const gdn_kv_dims* dims, const int32_t* t_lane,
-                            const void* q, int dtype, const uint8_t* k_codes,
-                            const uint8_t* k_scales, const uint8_t* v_codes,
-                            const uint8_t* v_scales, const int32_t* page_table,
-                            const int32_t* kv_len, float* o, void* workspace,
-                            size_t ws_bytes, float scale, void* stream);
+                             const void* q, int dtype, const uint8_t* k_codes,
+                             const uint8_t* k_scales, const uint8_t* v_codes,
+                             const uint8_t* v_scales, const int32_t* page_table,
+                             const int32_t* kv_len, float* o, void* workspace,
+                             size_t ws_bytes, float scale, void* stream);
 
 /*
  * Log probabilities of given tokens, with entropy and top alternatives, for

@@ -143,6 +143,10 @@ def test_verify_refusals():
             a = dict(n=n, T=T, t=(1,) * n, V=V, xs=V, ys=V)
             assert _verify(ws_bytes=need - 1, **a) == EWORK
             assert _verify(ws=None, **a) == EWORK
+    # more threads than a launch may have
+    a = dict(n=256, T=64, t=(1,) * 256, V=2**23, xs=2**23, ys=2**23)
+    assert _verify(ws_bytes=gdn.draft_verify_workspace_bytes(256, 64, 2**23), **a) == EINVAL
+    assert b"grid too large" in gdn.lib.gdn_last_error()
     for sizes in ((0, 1, 1), (1, 0, 1), (1, 1, 0), (257, 1, 1), (1, 65, 1), (1, 1, 2**30 + 1)):
         assert gdn.draft_verify_workspace_bytes(*sizes) == 0
 
