@@ -6,6 +6,7 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "gdn.h"
@@ -53,6 +54,17 @@ __device__ __forceinline__ codes_u32x4 fp4_values(uint32_t codes,
   r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 2));
   r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 3));
   return r;
+}
+
+// f64 to f32 with an odd last bit wherever something is cut off: rounded once
+// more, to fewer bits, it comes out as the f64 number itself would (borders
+// between codes and scales have even last bits).  Past f32 the largest number,
+// not an infinity.
+__device__ __forceinline__ float to_odd(double x) {
+  const float f = (float)x;
+  uint32_t u = __float_as_uint(f);
+  if ((double)f != x) u = (u - (fabs((double)f) > fabs(x) ? 1 : 0)) | 1;
+  return __uint_as_float(u);
 }
 
 // Codes of eight channels of a block whose other 24 are in the neighbouring

@@ -11,9 +11,10 @@
 //
 // Every row is read and written once; memory bounds a large call, the launch
 // and what the caller does for it a small one (3.3 us of kernel for 8 lanes
-// of one token, 18 heads of 256; 4.2 into 4 bits).  128 lanes x 64 tokens, 48
+// of one token, 18 heads of 256; 4.5 into 4 bits).  128 lanes x 64 tokens, 48
 // heads of 128, bf16: 46 us, 201 MB at 4.4 TB/s, a large copy runs at 4.8; the
-// same into 4 bits, the decoded rows written as well: 46 us, 211 MB at 4.6.
+// same into 4 bits, the decoded rows written as well: 47.5 us, 211 MB at 4.4 (and
+// 46.2 with keys turned in f32, see code_rows).
 // What it took: a thread that turns one head works out eight angles in f64
 // for it, 102 and 107 us; with the angles kept for the same channels of
 // several heads (see slots_for) they cost nothing.
@@ -42,10 +43,8 @@ struct RopeArgs {
   bool pairs;  // neighbouring channels form pairs, else channels rot / 2 apart
 };
 
-// cos and sin of p f.  The turn's fraction within [-1/8, 1/8] of the nearest
-// quarter goes through the Taylor series of sine and cosine, whose next terms
-// are below 2^-25 at pi / 4.
-__device__ __forceinline__ void turn(int p, float f, float& c, float& s) {
+// An angle p f as quarter turns and a rest x of at most an eighth of a turn.
+__device__ __forceinline__ int reduced(int p, float f, double& x) {
   const double a = (double)p * (double)f;
   // 1 / (2 pi) in two parts
   constexpr double kHi = 0.15915494309189534561, kLo = -9.8393383375912e-18;
@@ -53,8 +52,22 @@ __device__ __forceinline__ void turn(int p, float f, float& c, float& s) {
   const double r =
       __builtin_fma(a, kHi, -whole) + a * kLo;  // -1/2 .. 1/2
   const double quarter = __builtin_rint(4.0 * r);
-  const float x = (float)((r - 0.25 * quarter) * 6.28318530717958647693);
-  const float y = x * x;
+  x = (r - 0.25 * quarter) * 6.28318530717958647693;
+  return (int)quarter & 3;
+}
+// Cosine and sine of x and k quarter turns from those of x.
+template <typename F>
+__device__ __forceinline__ void turned(int k, F cs, F sn, F& c, F& s) {
+  const F u = k & 1 ? sn : cs, v = k & 1 ? cs : sn;
+  c = k == 1 || k == 2 ? -u : u;
+  s = k >= 2 ? -v : v;
+}
+// cos and sin of p f in f32: Taylor series whose next terms are below 2^-25 at
+// pi / 4.
+__device__ __forceinline__ void turn(int p, float f, float& c, float& s) {
+  double rest;
+  const int k = reduced(p, f, rest);
+  const float x = (float)rest, y = x * x;
   float sn = __builtin_fmaf(y, 2.75573192e-6f, -1.98412698e-4f);
   sn = __builtin_fmaf(y, sn, 8.33333333e-3f);
   sn = __builtin_fmaf(y, sn, -1.66666667e-1f);
@@ -64,10 +77,27 @@ __device__ __forceinline__ void turn(int p, float f, float& c, float& s) {
   cs = __builtin_fmaf(y, cs, 4.16666667e-2f);
   cs = __builtin_fmaf(y, cs, -0.5f);
   cs = __builtin_fmaf(y, cs, 1.f);
-  const int k = (int)quarter & 3;  // quarter turns
-  const float u = k & 1 ? sn : cs, v = k & 1 ? cs : sn;
-  c = k == 1 || k == 2 ? -u : u;
-  s = k >= 2 ? -v : v;
+  turned(k, cs, sn, c, s);
+}
+// The same in f64, the next terms 2e-14 and 1e-15 at pi / 4.
+__device__ __forceinline__ void turn(int p, float f, double& c, double& s) {
+  double x;
+  const int k = reduced(p, f, x);
+  const double y = x * x;
+  double sn = __builtin_fma(y, 1.0 / 6227020800.0, -1.0 / 39916800.0);
+  sn = __builtin_fma(y, sn, 1.0 / 362880.0);
+  sn = __builtin_fma(y, sn, -1.0 / 5040.0);
+  sn = __builtin_fma(y, sn, 1.0 / 120.0);
+  sn = __builtin_fma(y, sn, -1.0 / 6.0);
+  sn = __builtin_fma(x * y, sn, x);
+  double cs = __builtin_fma(y, -1.0 / 87178291200.0, 1.0 / 479001600.0);
+  cs = __builtin_fma(y, cs, -1.0 / 3628800.0);
+  cs = __builtin_fma(y, cs, 1.0 / 40320.0);
+  cs = __builtin_fma(y, cs, -1.0 / 720.0);
+  cs = __builtin_fma(y, cs, 1.0 / 24.0);
+  cs = __builtin_fma(y, cs, -0.5);
+  cs = __builtin_fma(y, cs, 1.0);
+  turned(k, cs, sn, c, s);
 }
 
 // Eight channels of a row.
@@ -110,9 +140,9 @@ __device__ __forceinline__ int turn_of(const RopeArgs& p, int n, int t, int T) {
 }
 
 // Cosines and sines of N pairs from inverse frequency f on.
-template <int N>
+template <int N, typename F = float>
 struct Turns {
-  float c[N], s[N];
+  F c[N], s[N];
   __device__ __forceinline__ void set(int pos, const float* f) {
 #pragma unroll
     for (int i = 0; i < N; ++i) turn(pos, f[i], c[i], s[i]);
@@ -250,7 +280,9 @@ __device__ __forceinline__ void copy_rows(const RopeArgs& p,
 }
 
 // Keys and values into 4 bits: eight neighbouring channels a thread, four
-// threads a block of 32.
+// threads a block of 32.  Keys are turned in f64: a code is half its value
+// apart from the next, and of 10^7 keys off by steps of f32 a few would lie on
+// the other side of the border between two.
 template <typename T, bool PAIRS>
 __device__ __forceinline__ void code_rows(const RopeArgs& p,
                                           const gdn::LaneTable& tl, int d,
@@ -265,7 +297,7 @@ __device__ __forceinline__ void code_rows(const RopeArgs& p,
   const int hp = p.rot / 16;
   const bool second = !PAIRS && u >= hp;
   const int other = PAIRS || !turns ? u : second ? u - hp : u + hp;
-  Turns<8> w;
+  Turns<8, double> w;
   if (turns) {
     const int pos = turn_of(p, k.n, k.t, k.T);
     if constexpr (PAIRS) {
@@ -309,14 +341,15 @@ __device__ __forceinline__ void code_rows(const RopeArgs& p,
         if constexpr (PAIRS) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float l = x[b].x[2 * e], r = x[b].x[2 * e + 1];
-            x[b].x[2 * e] = l * w.c[e] - r * w.s[e];
-            x[b].x[2 * e + 1] = r * w.c[e] + l * w.s[e];
+            const double l = x[b].x[2 * e], r = x[b].x[2 * e + 1];
+            x[b].x[2 * e] = to_odd(l * w.c[e] - r * w.s[e]);
+            x[b].x[2 * e + 1] = to_odd(r * w.c[e] + l * w.s[e]);
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            x[b].x[e] = x[b].x[e] * w.c[e] + y[b].x[e] * (second ? w.s[e] : -w.s[e]);
+            x[b].x[e] = to_odd((double)x[b].x[e] * w.c[e] +
+                               (double)y[b].x[e] * (second ? w.s[e] : -w.s[e]));
         }
       }
       put(p.k4, p.k_held, h, x[b].x);

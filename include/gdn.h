@@ -617,8 +617,8 @@ int gdn_rope_append(const gdn_kv_dims* dims, const int32_t* t_lane,
  *   k_scales, v_scales  device uint8 [n_pages][h_kv][page_size][d / 32]
  * A block's scale is the smallest power of two with max |x| <= 6 s, 2^-126 at
  * least and 2^124 at most (magnitudes past 6 * 2^124 become that), and every
- * value the nearest one that the codes have, ties to the even code; rounding
- * is from the turned f32 row.  A block that holds an infinity or a NaN has
+ * value the nearest one that the codes have, ties to the even code; keys are
+ * turned in f64 and rounded once.  A block that holds an infinity or a NaN has
  * b = 255 and codes 0: all of it reads as NaN.
  *   k_held, v_held  device bf16 [n_lanes][t_max][h_kv][d] or NULL: the new
  *               tokens' rows as the cache holds them (exact in bf16), for a

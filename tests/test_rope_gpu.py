@@ -312,6 +312,20 @@ def test_every_code_and_border():
             assert torch.equal(x[c + "_codes"][p, :, r].cpu(), codes[i, 0]), i
 
 
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_turned_keys_are_rounded_once(kind, pairs):
+    """Four million turned keys come out as the nearest codes of the keys in 64
+    bits, every one: keys off by 2^-24 of their size would give about one in a
+    million the neighbouring code.  (The kernel's sines and the reference's are
+    2e-14 apart, which would do that to one in 10^13.)"""
+    x = _case([64] * 64, [64] * 64, 8, 8, 128, 16, kind, 128)
+    given = torch.randint(0, 1 << 20, (64, 64), dtype=torch.int32, device="cuda")
+    _, k, _ = _run4(x, pairs, given)
+    want, _ = ref.turned(x["k"], _positions(x, given), x["inv_freq"], 128, pairs)
+    assert torch.equal(k.double().cpu(), ref.decode(*ref.encode(want)))
+
+
 def test_values_past_the_largest_scale_and_non_finite_blocks():
     x = _case([1], [1], 1, 1, 128, 1, "f32", 0, fused=False)
     big = 6 * 2.0 ** 124
