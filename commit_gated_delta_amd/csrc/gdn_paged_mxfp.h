@@ -153,10 +153,20 @@ struct VTile {
 // negative here (a query's signs carry that), so the largest of the raw
 // scores tells whether m is to be raised, and one operation scales a score
 // and subtracts m.
+//
+// m is rounded, the scaled score in that operation is not, so the largest
+// weight is not 1 but 2 to the half step that m is off by: nothing to a
+// softmax, whose sum has the same factor, while it is a small power of two.
+// With a row past kFar the scaled scores are rounded as m is (in f32, scores of
+// that size are whole octaves apart in any case), and m is raised without slack,
+// which would be lost in it.  Such a row's lim lets every step through to where
+// m is raised, so that the other steps need not ask.  (A raw score of +inf
+// needs none of this: it gives NaN in either way.)
+constexpr float kFar = 16777216.f;  // 2^24: m is off by one at most
 template <int D, int RT>
 struct Rows4 : Rows<D, uint16_t, RT> {
   typedef Rows<D, uint16_t, RT> R;
-  float lim[RT];   // raw score from which m is raised
+  float lim[RT];   // raw score above which m is raised
   float base[RT];  // what is added to a scaled score: -m, 0 before the first
 
   __device__ __forceinline__ void init(int row0, int rows, int len, int T_n,
@@ -203,6 +213,7 @@ struct Rows4 : Rows<D, uint16_t, RT> {
         float t = top[r];
         t = fmaxf(t, __shfl_xor(t, 16));
         t = fmaxf(t, __shfl_xor(t, 32));
+        const bool rounds = t < INFINITY && fabsf(t * scale) > kFar;
         t = t == -INFINITY ? t : fmaxf(this->m[r], t * scale);
         if (t > this->m[r]) {
           const float keep = this->m[r] == -INFINITY
@@ -210,11 +221,24 @@ struct Rows4 : Rows<D, uint16_t, RT> {
                                  : __builtin_amdgcn_exp2f(this->m[r] - t);
           this->m[r] = t;
           base[r] = -t;
-          lim[r] = scale > 0.f ? (t + kSlack) / scale : INFINITY;
+          lim[r] = rounds        ? -INFINITY
+                   : scale > 0.f ? (t + kSlack) / scale
+                                 : INFINITY;
           this->l[r] *= keep;
 #pragma unroll
           for (int c = 0; c < R::CT; ++c) this->acc[r][c] *= keep;
         }
+      }
+      bool past = false;
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        past |= lim[r] == -INFINITY && this->m[r] != -INFINITY;
+      if (__any(past)) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) this->sc[r][h] *= scale;
+        scale = 1.f;
       }
     }
 #pragma unroll
