@@ -292,6 +292,15 @@ __global__ __launch_bounds__(kThreads, 4) void sum_kernel(DraftArgs p,
         m, (sums[0] + sums[1]) + (sums[2] + sums[3])};
 }
 
+// Slices of kGroup ids a row from which the verdicts and both rows' sums are
+// worked out once a lane, by launches of their own (2^20 ids).  Below, every
+// workgroup that needs them works them out for itself: that saves launches, but
+// its work grows with the square of the vocabulary.  With and without launches
+// of their own, drafter's rows given, bf16: one lane of one draft over 2^19,
+// 2^20, 2^21 ids 22, 27, 42 and 19, 24, 58 us; 8 lanes of 15 73, 136, 256 and 83,
+// 182, 440; 64 lanes of 5 225, 444, 867 and 308, 741, 1923.
+constexpr int kManyGroups = 128;
+
 // A workgroup of kExact threads works a lane's verdict out from the slices'
 // sums, a wave a row.
 struct Rows {
@@ -372,13 +381,24 @@ __device__ __forceinline__ Verdict decide(const DraftArgs& p, int n, int T_n,
   return rows.verdict;
 }
 
-// The verdicts, and f64 sums by slices of the row that the next token is
-// sampled from (leaving the fallen draft out, where it has no distribution),
-// or of the drafter's row beside it.  A workgroup takes kGroup ids; each works
-// the lane's verdict out for itself, which costs less than a launch between.
-// Bound by that chain of loads and, with many lanes, by the exponentials in
-// f64: 8 lanes and their drafter's rows 7.9 us, 64 lanes 13.3.
+// The verdicts alone, a workgroup per lane.
 template <typename T>
+__global__ __launch_bounds__(kExact) void verdict_kernel(DraftArgs p,
+                                                         gdn::LaneTable tl) {
+  __shared__ Rows rows;
+  const int n = blockIdx.x, T_n = tl.v[n];
+  if (T_n == 0) return;
+  Verdict v = {1, 1};
+  if (T_n > 1) v = decide<T>(p, n, T_n, exponent_of(p, n), rows, true);
+  if (threadIdx.x == 0) p.verdicts[n] = v;
+}
+
+// f64 sums by slices of the row that the next token is sampled from (leaving
+// the fallen draft out, where it has no distribution), or of the drafter's row
+// beside it, and unless they are KNOWN the verdicts.  A workgroup takes kGroup
+// ids.  Bound by the verdicts' chain of loads and, with many lanes, by the
+// exponentials in f64: 8 lanes and their drafter's rows 7.9 us, 64 lanes 13.3.
+template <typename T, bool KNOWN>
 __global__ __launch_bounds__(kExact) void exact_kernel(DraftArgs p,
                                                       gdn::LaneTable tl,
                                                       int sides) {
@@ -395,8 +415,12 @@ __global__ __launch_bounds__(kExact) void exact_kernel(DraftArgs p,
   const int tid = threadIdx.x, lane = tid & 63, wave = gdn::uniform(tid >> 6);
   const double c = exponent_of(p, n);
   Verdict v = {1, 1};
-  if (T_n > 1) v = decide<T>(p, n, T_n, c, rows, part == 0 && side == 0);
-  if (part == 0 && side == 0 && tid == 0) p.verdicts[n] = v;
+  if constexpr (KNOWN) {
+    v = p.verdicts[n];
+  } else {
+    if (T_n > 1) v = decide<T>(p, n, T_n, c, rows, part == 0 && side == 0);
+    if (part == 0 && side == 0 && tid == 0) p.verdicts[n] = v;
+  }
   const bool fell = v.m < T_n;
   if (!v.ok || (side == 1 && !fell)) return;
   S s;
@@ -451,10 +475,54 @@ __device__ __forceinline__ double weight_left(const Left& r, float x, float y,
   return w > 0.0 ? w : 0.0;
 }
 
+// Both rows' largest logits and sums alone, a workgroup per lane: one half of
+// it for the target's row, the other for the drafter's.
+template <typename T>
+__global__ __launch_bounds__(kPick) void left_kernel(DraftArgs p,
+                                                     gdn::LaneTable tl) {
+  constexpr int kHalf = kPick / 2, kWaves = kHalf / 64;
+  __shared__ float tops[2][kWaves];
+  __shared__ double sums[2][kWaves];
+  const int n = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+  const int side = gdn::uniform(tid / kHalf), wave = gdn::uniform(tid % kHalf >> 6);
+  if (tl.v[n] < 2) return;
+  const Verdict v = p.verdicts[n];
+  if (!v.ok || v.m == tl.v[n]) return;
+  const double c = exponent_of(p, n);
+  const Exact* e = p.exact + ((long)n * 2 + side) * p.slices;
+  float m = -INFINITY;
+  for (int i = tid % kHalf; i < p.slices; i += kHalf) m = nan_max(m, e[i].m);
+  m = wave_nan_max(m);
+  if (lane == 0) tops[side][wave] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) m = nan_max(m, tops[side][i]);
+  const double ref = m == -INFINITY ? 0.0 : (double)m;
+  double z = 0.0;
+  for (int i = tid % kHalf; i < p.slices; i += kHalf)
+    z += e[i].z * weight_of(e[i].m, ref, c);
+  z = wave_sum64(z);
+  if (lane == 0) sums[side][wave] = z;
+  __syncthreads();
+  if (tid % kHalf != 0) return;
+  z = 0.0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) z += sums[side][i];
+  Left& r = p.left[n];
+  if (side == 0) {
+    r.top = m;
+    r.f = 1.0 / z;
+  } else {
+    r.draft_top = m;
+    r.draft_f = 1.0 / z;
+  }
+}
+
 // With a drafter's distribution: sums of max(p - q, 0) by slices of the row
 // where a draft fell.  The logits, in the cache still, are on their way while
-// the sums of both rows are worked out.  8 lanes: 5.8 us, bound by latency.
-template <typename T>
+// the sums of both rows are worked out, unless these are KNOWN.  8 lanes: 5.8
+// us, bound by latency.
+template <typename T, bool KNOWN>
 __global__ __launch_bounds__(kThreads) void rest_kernel(DraftArgs p,
                                                         gdn::LaneTable tl) {
   constexpr int N = kSlice / kThreads;
@@ -477,13 +545,18 @@ __global__ __launch_bounds__(kThreads) void rest_kernel(DraftArgs p,
     }
   }
   const double c = exponent_of(p, n);
-  const Exact* e = p.exact + (long)n * 2 * p.slices;
-  float m, dm;
-  double z, dz;
-  whole_row(e, p.slices, c, m, z);
-  whole_row(e + p.slices, p.slices, c, dm, dz);
-  const Left r = {m, dm, 1.0 / z, 1.0 / dz};
-  if (slice == 0 && tid == 0) p.left[n] = r;
+  Left r;
+  if constexpr (KNOWN) {
+    r = p.left[n];
+  } else {
+    const Exact* e = p.exact + (long)n * 2 * p.slices;
+    float m, dm;
+    double z, dz;
+    whole_row(e, p.slices, c, m, z);
+    whole_row(e + p.slices, p.slices, c, dm, dz);
+    r = {m, dm, 1.0 / z, 1.0 / dz};
+    if (slice == 0 && tid == 0) p.left[n] = r;
+  }
   double sum = 0.0;
 #pragma unroll
   for (int k = 0; k < N; ++k) sum += weight_left(r, x[k], y[k], c);
@@ -665,12 +738,23 @@ static hipError_t run(const DraftArgs& p, const gdn::LaneTable& tl,
     e = launch(sum_kernel<T>,
                dim3((unsigned)((long)p.lanes * (p.t_max - 1) * sides * p.groups)),
                dim3(kThreads), st, p, tl);
+  const bool known = p.t_max > 1 && p.groups >= kManyGroups;
+  if (e == hipSuccess && known)
+    e = launch(verdict_kernel<T>, dim3((unsigned)p.lanes), dim3(kExact), st, p, tl);
+  const dim3 exact((unsigned)((long)p.lanes * sides * p.groups));
   if (e == hipSuccess)
-    e = launch(exact_kernel<T>, dim3((unsigned)((long)p.lanes * sides * p.groups)),
-               dim3(kExact), st, p, tl, sides);
-  if (e == hipSuccess && p.draft)
-    e = launch(rest_kernel<T>, dim3((unsigned)((long)p.lanes * p.slices)),
-               dim3(kThreads), st, p, tl);
+    e = known ? launch(exact_kernel<T, true>, exact, dim3(kExact), st, p, tl, sides)
+              : launch(exact_kernel<T, false>, exact, dim3(kExact), st, p, tl, sides);
+  if (e == hipSuccess && p.draft) {
+    const dim3 rest((unsigned)((long)p.lanes * p.slices));
+    if (known) {
+      e = launch(left_kernel<T>, dim3((unsigned)p.lanes), dim3(kPick), st, p, tl);
+      if (e == hipSuccess)
+        e = launch(rest_kernel<T, true>, rest, dim3(kThreads), st, p, tl);
+    } else {
+      e = launch(rest_kernel<T, false>, rest, dim3(kThreads), st, p, tl);
+    }
+  }
   if (e != hipSuccess) return e;
   return launch(pick_kernel<T>, dim3((unsigned)p.lanes), dim3(kPick), st, p, tl);
 }
