@@ -12,7 +12,7 @@
 // Decoding", ICML 2023, Sec. 2.3 and appendix A.1).
 //
 // Which drafts stand needs every row but the last, so their sums are f32 at
-// the memory's rate.  The next token is where a running sum passes a given
+// the memory's rate (a chance is 2 steps of 2^-24 off, rms, and 1e-8 in f64).  The next token is where a running sum passes a given
 // number, and an error d of the sums moves it with a chance of about d times
 // the number of likely tokens: the one row that it is sampled from is summed
 // up again in f64.
@@ -247,8 +247,8 @@ struct Share {
 // Sums of the rows that decide about the drafts: a workgroup per kGroup ids,
 // read once into registers, so that its largest logit is known before its sum
 // and no exponential is taken twice.  Bound by HBM: 8 lanes of up to 15 drafts,
-// 131072 ids in f32, drafter's rows too: 10.4 us, 45 MB at 4.3 TB/s; 64 lanes
-// of up to 5, bf16: 11.6 us, 46 MB at 4.0, the vector units nearly full.
+// 131072 ids in f32, drafter's rows too: 10.5 us, 45 MB at 4.3 TB/s; 64 lanes
+// of up to 5, bf16: 11.5 us, 46 MB at 4.0, the vector units nearly full.
 // (In f64 18 and 32 us, 26 vector instructions a logit.)
 template <typename T>
 __global__ __launch_bounds__(kThreads, 4) void sum_kernel(DraftArgs p,
@@ -397,7 +397,7 @@ __global__ __launch_bounds__(kExact) void verdict_kernel(DraftArgs p,
 // the fallen draft out, where it has no distribution), or of the drafter's row
 // beside it, and unless they are KNOWN the verdicts.  A workgroup takes kGroup
 // ids.  Bound by the verdicts' chain of loads and, with many lanes, by the
-// exponentials in f64: 8 lanes and their drafter's rows 7.9 us, 64 lanes 13.3.
+// exponentials in f64: 8 lanes and their drafter's rows 8.1 us, 64 lanes 13.4.
 template <typename T, bool KNOWN>
 __global__ __launch_bounds__(kExact) void exact_kernel(DraftArgs p,
                                                       gdn::LaneTable tl,
@@ -520,7 +520,7 @@ __global__ __launch_bounds__(kPick) void left_kernel(DraftArgs p,
 
 // With a drafter's distribution: sums of max(p - q, 0) by slices of the row
 // where a draft fell.  The logits, in the cache still, are on their way while
-// the sums of both rows are worked out, unless these are KNOWN.  8 lanes: 5.8
+// the sums of both rows are worked out, unless these are KNOWN.  8 lanes: 5.6
 // us, bound by latency.
 template <typename T, bool KNOWN>
 __global__ __launch_bounds__(kThreads) void rest_kernel(DraftArgs p,
@@ -569,7 +569,7 @@ __global__ __launch_bounds__(kThreads) void rest_kernel(DraftArgs p,
 
 // The next token, a workgroup per lane: the slice that the border lies in,
 // then the id within it.
-// 5.6 to 6.8 us for 1 to 64 lanes, bound by latency: three passes over the
+// 5.6 to 6.6 us for 1 to 64 lanes, bound by latency: three passes over the
 // slices' sums, one over a slice.
 template <typename T>
 __global__ __launch_bounds__(kPick) void pick_kernel(DraftArgs p,

@@ -317,9 +317,10 @@ constexpr int rows4_waves() {
   return RT == 2 || D * sizeof(T) > 256 ? NW / 4 * RT : NW / 2;
 }
 // Whether a wave of rows4_kernel takes 32 rows of 128, so that K is widened
-// and V read half as often, or 16 (the same windows of 16 over 16k): 56.6 and
-// 59.1 us with the join at d = 64, 71.5 and 78.9 at 128, in f32 60.5 and 63.6
-// at 64, but 115 and 104 at 128, where 32 rows leave one wave a SIMD.
+// and V read half as often, or 16 (the same windows of 16 over 16k): 57.1 and
+// 59.5 us with the join at d = 64, 72.3 and 78.9 at 128, in f32 61.0 and 63.9
+// at 64.  At 128 f32 rows are taken by 16 (104 us): 32 of them take 115 us with
+// one wave a SIMD, and 94 with two, which spill 16 registers.
 template <int D, typename T>
 constexpr bool kWide = D * sizeof(T) <= 256;
 
@@ -343,7 +344,7 @@ __device__ __forceinline__ uint32_t cache_row(const KvArgs& a, int page, int h,
 // loads of a step are given out a whole step ahead, each into the registers
 // that the step in hand has just used up; with a branch around the last ones
 // it was 200 us.  A short cache is bound by one workgroup's chain of look-up,
-// loads, products and sums: 8 lanes of up to 1k positions 8.6 us and 4.3 for
+// loads, products and sums: 8 lanes of up to 1k positions 8.8 us and 4.2 for
 // the join.
 template <int D, typename T, int RT, bool EVEN>
 __global__ __launch_bounds__(256, (few4_waves<D, T, RT>())) void attend4_kernel(
@@ -493,7 +494,7 @@ __global__ __launch_bounds__(256, (few4_waves<D, T, RT>())) void attend4_kernel(
 // the time (K is widened, each probability cut into the three bf16 parts that
 // hold its 24 bits), matrix ones 39 % (four products a score, one for K and
 // three for V); two waves a SIMD hide little of either behind the other.  8
-// lanes x 16 tokens x 32 heads of 128 over up to 16k positions: 69 us.  With
+// lanes x 16 tokens x 32 heads of 128 over up to 16k positions: 68 us.  With
 // 16 rows a wave it was 76; with K widened once for all waves, as V is, 84,
 // bound by the reads from LDS; scores of the whole tile before its softmax, or
 // a wave's priority raised for its products, change nothing (68..69).
@@ -657,8 +658,8 @@ __global__ __launch_bounds__(64 * NW, (rows4_waves<D, T, NW, RT>())) void rows4_
 // Workgroups of a launch, as kFewBlocks and kRowsBlocks of the wider cache.
 // 32 lanes of up to 32k, 8 heads of 128: 280, 198, 197, 176, 177 us with 512,
 // 768, 1024, 1536, 2048; f32 queries, 13 lanes of up to 10k, 3 heads of 64:
-// 14.4, 14.5, 14.8, 16.0, 15.7; 8 lanes of up to 1k have fewer splits than any
-// of these.  Windows of 16, 8 lanes of up to 16k, 16 rows a wave: 88 and 7 us
+// 14.4, 14.5, 14.8, 16.0, 15.7 (the long caches decide; a short split is mostly
+// its start and end); 8 lanes of up to 1k have fewer splits than any of these.  Windows of 16, 8 lanes of up to 16k, 16 rows a wave: 88 and 7 us
 // (the join) with 256, 76 and 9 with 512, 87 and 11 with 768, 86 and 13 with
 // 1024.
 constexpr int kFew4Blocks = 2048, kRows4Blocks = 512;

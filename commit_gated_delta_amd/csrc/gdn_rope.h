@@ -6,15 +6,16 @@
 // p f_i (f_i the pair's inverse frequency):
 //   a' = a cos - b sin,   b' = b cos + a sin.
 // p f_i has at most 31 + 24 significant bits, so its product in f64 is exact
-// to half a step, and it is reduced to a fraction of a turn there: the angle
-// is as good at the far end of a long cache as at its start.
+// to half a step (for positions below 2^29 altogether), and it is reduced to a
+// fraction of a turn there: the angle is as good at the far end of a long cache
+// as at its start.
 //
 // Every row is read and written once; memory bounds a large call, the launch
 // and what the caller does for it a small one (3.3 us of kernel for 8 lanes
 // of one token, 18 heads of 256; 4.5 into 4 bits).  128 lanes x 64 tokens, 48
-// heads of 128, bf16: 46 us, 201 MB at 4.4 TB/s, a large copy runs at 4.8; the
-// same into 4 bits, the decoded rows written as well: 47.5 us, 211 MB at 4.4 (and
-// 46.2 with keys turned in f32, see code_rows).
+// heads of 128, bf16: 47 us, 201 MB at 4.3 TB/s, a large copy runs at 4.6 to 4.8;
+// the same into 4 bits, the decoded rows written as well: 48 us, 211 MB at 4.4
+// (with keys turned in f32, see code_rows, 1.3 us less).
 // What it took: a thread that turns one head works out eight angles in f64
 // for it, 102 and 107 us; with the angles kept for the same channels of
 // several heads (see slots_for) they cost nothing.

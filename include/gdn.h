@@ -577,8 +577,9 @@ int gdn_kv_append(const gdn_kv_dims* dims, const int32_t* t_lane,
  *   a' = a cos(p f_i) - b sin(p f_i),   b' = b cos(p f_i) + a sin(p f_i)
  * with f = inv_freq and (a, b) channels i and i + rot_dim / 2, or with
  * GDN_FLAG_ROPE_PAIRS channels 2 i and 2 i + 1.  Channels from rot_dim on and
- * the values are copied bit for bit.  Angles are reduced in f64, cosine, sine
- * and the products are f32, rounded once to the outputs' type.
+ * the values are copied bit for bit.  Angles are products in f64 (half a step
+ * of their size off, so of use while p f is far below 2^53) and reduced there;
+ * cosine, sine and the products are f32, rounded once to the outputs' type.
  *   dims, t_lane, page_table, kv_len, k_cache, v_cache  as for gdn_kv_append
  *               (the same places, the same rows dropped)
  *   q, k, v     device, dtype (bf16 or f32): token t of lane n has its rows
@@ -617,8 +618,10 @@ int gdn_rope_append(const gdn_kv_dims* dims, const int32_t* t_lane,
  *   k_scales, v_scales  device uint8 [n_pages][h_kv][page_size][d / 32]
  * A block's scale is the smallest power of two with max |x| <= 6 s, 2^-126 at
  * least and 2^124 at most (magnitudes past 6 * 2^124 become that), and every
- * value the nearest one that the codes have, ties to the even code; keys are
- * turned in f64 and rounded once.  A block that holds an infinity or a NaN has
+ * value the nearest one that the codes have, ties to the even code (elements
+ * and scales are those of the OCP microscaling format of 4 bits, whose own
+ * example takes a scale that cuts the largest values off); keys are turned in
+ * f64 and rounded once.  A block that holds an infinity or a NaN has
  * b = 255 and codes 0: all of it reads as NaN.
  *   k_held, v_held  device bf16 [n_lanes][t_max][h_kv][d] or NULL: the new
  *               tokens' rows as the cache holds them (exact in bf16), for a
@@ -640,12 +643,15 @@ int gdn_rope_append_mxfp(const gdn_kv_dims* dims, const int32_t* t_lane,
 
 /*
  * gdn_paged_attention over that cache (or any in its layout: scale byte 0 is
- * 2^-127, and a block whose byte is 253 to 255 reads as NaN; a value below
- * 2^-126 may count as zero).  Queries are
- * bf16 or f32, the products and sums f32 or wider; a query row that holds an
- * infinity or a NaN gives NaN.  n_pages * h_kv * page_size < 2^32
- * (GDN_EINVAL).  The rest, what masked rows may hold among it, as for
- * gdn_paged_attention, with its own workspace size.
+ * 2^-127, and a block whose byte is 253 to 255 reads as NaN).  Queries are
+ * bf16 or f32, the products and sums f32 or wider; bits of a value or a query
+ * worth less than 2^-126 may count as zero, and weighted values are summed
+ * before they are divided by the weights' sum, so that values past 2^90 may
+ * overflow.  A query row that holds an infinity or a NaN gives NaN, as does one
+ * with a score of +inf (a finite product that the scale takes past f32 among
+ * them).  n_pages * h_kv * page_size < 2^32 (GDN_EINVAL).  The rest, what
+ * masked rows may hold among it, as for gdn_paged_attention, with its own
+ * workspace size.
  */
 size_t gdn_paged_attention_mxfp_workspace_bytes(const gdn_kv_dims* dims);
 int gdn_paged_attention_mxfp(const gdn_kv_dims* dims, const int32_t* t_lane,
@@ -722,8 +728,10 @@ int gdn_token_scores(int32_t n_rows, int32_t vocab, int64_t row_stride,
  * inverse temperature is out of range: a draft falls there (accept NaN), and
  * next_token is -1 when it would be sampled there.  Where p - q leaves
  * nothing (p = q to rounding) the token is sampled from p.
- * Chances of drafts are exact to a few steps of f32; the sums that the next
- * token is looked up in are f64.
+ * Chances of drafts are off by a few 2^-24 of their value (their rows' sums are
+ * f32), at most 2^-16; the sums that the next token is looked up in are f64.
+ * Calls whose launches would hold 2^32 threads, from about 2^37 logits on, are
+ * refused (GDN_EINVAL).
  *   workspace   device, 16-byte aligned, ws_bytes >=
  *               gdn_draft_verify_workspace_bytes(...); calls that overlap in
  *               time need workspaces of their own
