@@ -66,3 +66,34 @@ def test_time_grows_as_the_vocabulary():
         print("2^%d ids: %.3f ms" % (V.bit_length() - 1, best), flush=True)
         times.append(best)
     assert times[1] <= 8 * times[0]
+
+
+def test_captured_calls_over_a_large_vocabulary():
+    """Replays on other rows, the workspace overwritten between them, against
+    eager calls."""
+    t_lane, V = [3, 0, 2], (1 << 20) + 5
+    s = _case(t_lane, V, "bf16", True)
+    m, token = (torch.zeros(3, dtype=torch.int32, device="cuda") for _ in range(2))
+    accept = torch.zeros(3, 3, device="cuda")
+    ws = torch.empty(gdn.draft_verify_workspace_bytes(3, 3, V), dtype=torch.uint8, device="cuda")
+
+    def call():
+        gdn.draft_verify(t_lane, s["logits"], s["draft"], s["tokens"], s["uniforms"], s["it"], m, token, ws,
+                         accept=accept)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for seed in range(5, 9):
+        other = _case(t_lane, V, "bf16", True, seed=seed, right=0.5)
+        for c in ("logits", "draft", "tokens", "uniforms", "it"):
+            s[c].copy_(other[c])
+        ws.fill_(seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = _run(s)
+        for n in (0, 2):
+            assert (m[n].item(), token[n].item()) == (want[0][n], want[1][n])
+            assert torch.equal(accept[n, : t_lane[n] - 1].cpu().double(), want[2][n, : t_lane[n] - 1])

@@ -145,3 +145,18 @@ def test_scores_past_f32(T):
     assert torch.isnan(o[0, T - 1, 2:]).all()
     assert torch.equal(o[0, :, :2], clean[0, :, :2]) and torch.equal(o[0, :T - 1], clean[0, :T - 1])
     assert torch.equal(o[1, :1], clean[1, :1])
+
+
+@pytest.mark.parametrize("T,h_q,d,kind", [(1, 4, 256, "bf16"), (2, 8, 128, "f32"), (24, 8, 64, "bf16"), (16, 16, 128, "f32")])
+def test_a_score_past_f32_in_a_long_cache(T, h_q, d, kind):
+    """One of many splits holds the score that scales to +inf: NaN for the heads
+    that see it, and the others as before."""
+    x = _case([T], [7000], h_q, 2, d, 16, kind)
+    x["k_codes"].zero_()
+    x["q"].fill_(1e30)
+    clean = _run(x, [T], 1e30)
+    assert torch.isfinite(clean).all()
+    x["k_codes"][int(x["table"][0, 2001 // 16]), 1, 2001 % 16] = 0x77
+    o = _run(x, [T], 1e30)
+    assert torch.isnan(o[0, :, h_q // 2:]).all()
+    assert torch.equal(o[0, :, :h_q // 2], clean[0, :, :h_q // 2])
